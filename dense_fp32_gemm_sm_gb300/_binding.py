@@ -20,6 +20,7 @@ from . import _build
 OP_N, OP_T = 0, 1
 OK, ERR_INVALID_VALUE, ERR_LAUNCH, ERR_NOT_SUPPORTED, ERR_TIMEOUT = 0, 1, 2, 3, 4
 MATH_FP32, MATH_TF32, MATH_3XTF32 = 0, 1, 2
+F32, BF16, F16 = 0, 1, 2
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +103,25 @@ def library() -> ctypes.CDLL:
             lib.fgemm_math_supported.restype = _c_int
             lib.fgemm_debug_withhold_tensor_core.argtypes = [_c_int, _c_ll]
             lib.fgemm_debug_withhold_tensor_core.restype = None
+            _sz = ctypes.c_size_t
+            for name, argtypes, restype in (
+                    ("codes_size", [_c_int] * 2, _sz),
+                    ("scales_size", [_c_int] * 2, _sz),
+                    ("quantize", [_c_int] * 3 + [_c_vp, _c_int] * 2 + [_c_vp, _c_vp, _c_int, _c_vp,
+                                                                       _c_vp], _c_int),
+                    ("quantize_grad_workspace_size", [_c_int] * 2, _sz),
+                    ("quantize_grad", [_c_int] * 3 + [_c_vp, _c_int] * 3 +
+                     [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _sz, _c_vp], _c_int),
+                    ("dequantize", [_c_int] * 3 + [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp],
+                     _c_int),
+                    ("gemm", [_c_int] * 4 + [_c_float] + [_c_vp, _c_int, _c_vp] * 2 +
+                     [_c_float, _c_vp, _c_int, _c_vp, _c_int, _c_vp], _c_int),
+                    ("linear_workspace_size", [_c_int] * 3, _sz),
+                    ("linear", [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
+                                               _c_vp, _c_int, _c_vp, _sz, _c_vp], _c_int)):
+                fn = getattr(lib, "fgemm_mxfp4_" + name)
+                fn.argtypes = argtypes
+                fn.restype = restype
             lib.fgemm_config_name.restype = ctypes.c_char_p
             lib.fgemm_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -356,4 +376,113 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
         int(stage), _ptr(workspace), int(workspace_bytes), _stream(stream, C, A, B))
     if check:
         _check(st, "fgemm_gemm_math_staged")
+    return st
+
+
+# ---- MXFP4 (see "MXFP4" in include/fgemm.h) -------------------------------------------
+
+# Element types of unquantised matrices, by fgemm_dtype value.
+_TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
+
+
+def _mat(x, type):
+    """Address of an unquantised matrix: a CUDA tensor of the call's type, or an address."""
+    if x is None:
+        return None
+    if isinstance(x, int):
+        return x or None
+    if not x.is_cuda or not 0 <= type < 3 or str(x.dtype) != _TYPE_NAMES[type]:
+        raise TypeError("fgemm type %r takes a CUDA tensor of that type (got %s on %s)"
+                        % (type, x.dtype, x.device))
+    return x.data_ptr() or None
+
+
+def _bytes(x):
+    """Address of codes, scales or a workspace: a CUDA tensor of any type, or an address."""
+    if x is None:
+        return None
+    if isinstance(x, int):
+        return x or None
+    if not x.is_cuda:
+        raise TypeError("expected a CUDA tensor (got one on %s)" % (x.device,))
+    return x.data_ptr() or None
+
+
+def mxfp4_codes_size(rows, cols) -> int:
+    """``fgemm_mxfp4_codes_size``: bytes of the codes of a rows x cols quantised matrix."""
+    return int(library().fgemm_mxfp4_codes_size(rows, cols))
+
+
+def mxfp4_scales_size(rows, cols) -> int:
+    """``fgemm_mxfp4_scales_size``: bytes of the scales of a rows x cols quantised matrix."""
+    return int(library().fgemm_mxfp4_scales_size(rows, cols))
+
+
+def mxfp4_quantize(type, M, N, X, ldx, row_codes, ld_row_codes, row_scales, col_codes,
+                   ld_col_codes, col_scales, stream=None, check=True) -> int:
+    """``fgemm_mxfp4_quantize``: X along its rows, its columns (the quantised X^T) or both;
+    None for the codes and scales of a direction that is not wanted."""
+    st = library().fgemm_mxfp4_quantize(
+        type, M, N, _mat(X, type), ldx, _bytes(row_codes), ld_row_codes, _bytes(row_scales),
+        _bytes(col_codes), ld_col_codes, _bytes(col_scales), _stream(stream, X))
+    if check:
+        _check(st, "fgemm_mxfp4_quantize")
+    return st
+
+
+def mxfp4_quantize_grad_workspace_size(M, N) -> int:
+    """``fgemm_mxfp4_quantize_grad_workspace_size``: bytes for the bias gradient's partial sums."""
+    return int(library().fgemm_mxfp4_quantize_grad_workspace_size(M, N))
+
+
+def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row_scales,
+                        col_codes, ld_col_codes, col_scales, bias_grad, workspace,
+                        workspace_bytes, stream=None, check=True) -> int:
+    """``fgemm_mxfp4_quantize_grad``: G where Y > 0 (Y None: G), quantised as by
+    ``mxfp4_quantize``, and its column sums (bias_grad None: not wanted)."""
+    st = library().fgemm_mxfp4_quantize_grad(
+        type, M, N, _mat(G, type), ldg, _mat(Y, type), ldy, _bytes(row_codes), ld_row_codes,
+        _bytes(row_scales), _bytes(col_codes), ld_col_codes, _bytes(col_scales), _ptr(bias_grad),
+        _bytes(workspace), workspace_bytes, _stream(stream, G, bias_grad))
+    if check:
+        _check(st, "fgemm_mxfp4_quantize_grad")
+    return st
+
+
+def mxfp4_dequantize(type, M, N, codes, ld_codes, scales, X, ldx, stream=None, check=True) -> int:
+    """``fgemm_mxfp4_dequantize``: X = the values of a quantised matrix."""
+    st = library().fgemm_mxfp4_dequantize(type, M, N, _bytes(codes), ld_codes, _bytes(scales),
+                                          _mat(X, type), ldx, _stream(stream, X))
+    if check:
+        _check(st, "fgemm_mxfp4_dequantize")
+    return st
+
+
+def mxfp4_gemm(type, M, N, K, alpha, A_codes, ld_A_codes, A_scales, B_codes, ld_B_codes,
+               B_scales, beta, C, ldc, bias=None, apply_relu=False, stream=None,
+               check=True) -> int:
+    """``fgemm_mxfp4_gemm``: C = relu?(alpha*A*B^T + beta*C + bias[col]), A and B quantised."""
+    st = library().fgemm_mxfp4_gemm(
+        type, M, N, K, alpha, _bytes(A_codes), ld_A_codes, _bytes(A_scales), _bytes(B_codes),
+        ld_B_codes, _bytes(B_scales), beta, _mat(C, type), ldc, _ptr(bias), 1 if apply_relu else 0,
+        _stream(stream, C))
+    if check:
+        _check(st, "fgemm_mxfp4_gemm")
+    return st
+
+
+def mxfp4_linear_workspace_size(M, N, K) -> int:
+    """``fgemm_mxfp4_linear_workspace_size``: bytes of workspace mxfp4_linear needs."""
+    return int(library().fgemm_mxfp4_linear_workspace_size(M, N, K))
+
+
+def mxfp4_linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias, apply_relu, Y, ldy,
+                 workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_mxfp4_linear``: Y = relu?(Q(X)*W^T + bias[col]), X quantised on the way."""
+    st = library().fgemm_mxfp4_linear(
+        type, M, N, K, _mat(X, type), ldx, _bytes(W_codes), ld_W_codes, _bytes(W_scales),
+        _ptr(bias), 1 if apply_relu else 0, _mat(Y, type), ldy, _bytes(workspace),
+        workspace_bytes, _stream(stream, Y))
+    if check:
+        _check(st, "fgemm_mxfp4_linear")
     return st

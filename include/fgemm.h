@@ -429,6 +429,103 @@ fgemm_status fgemm_gemm_explicit(int config, fgemm_op transa, fgemm_op transb, i
                                  int ldc, long long strideC, int batch, const float *bias,
                                  int apply_relu, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: quantised matrices, and products of them (OCP Microscaling Formats, v1.0).
+ *
+ * A quantised matrix of R rows and L columns holds, for every block of 32 consecutive
+ * elements of a row (the last one may be shorter), one scale 2^(s-127), s a byte (E8M0,
+ * 255 = NaN), and for every element a 4-bit code (E2M1: sign, two exponent bits, one
+ * mantissa bit: 0 0.5 1 1.5 2 3 4 6).  An element stands for code * scale.
+ *   codes:  row r starts at byte r * ld; element k is in byte k/2 of the row, the low
+ *           nibble for even k.  ld (bytes) is a multiple of 16 and at least
+ *           16 * ceil(L/32); the pointer is 16-byte aligned.  A row is written up to
+ *           byte 16 * ceil(L/32); the codes beyond L are 0.
+ *   scales: with nb = ceil(L/32), the byte of row r and block b is at
+ *           512 * ((r/128) * ceil(nb/4) + b/4) + 16 * (r%32) + 4 * ((r%128)/32) + b%4:
+ *           atoms of 128 rows x 4 blocks, as the tensor cores take them.  16-byte
+ *           aligned, fgemm_mxfp4_scales_size(R, L) bytes.  Scales of rows and blocks
+ *           beyond the matrix are written as 0, and read as 0 by the products.
+ * Quantising a block with largest magnitude a:  s = max(0, floor(log2 a) + 125) (0 when a
+ * is 0), codes are the nearest of the values above to x / 2^(s-127), ties to the even
+ * code, magnitudes over 6 becoming 6; the sign bit is kept.  A block that holds a NaN or
+ * an infinity gets s = 255 and codes 0: all of it stands for NaN.
+ *
+ * `type` is the element type of the unquantised matrices of a call; their pointers are
+ * aligned to an element, leading dimensions are in elements, and any alignment and
+ * leading dimension is accepted.  The conventions at the top of this file hold (device
+ * pointers, nothing allocated, asynchronous on `stream`, FGEMM_MAX_DIM, invalid arguments
+ * refused before anything is launched).  Inputs and outputs of a call must not overlap.
+ * ------------------------------------------------------------------------- */
+typedef enum fgemm_dtype { FGEMM_F32 = 0, FGEMM_BF16 = 1, FGEMM_F16 = 2 } fgemm_dtype;
+
+/* Bytes of the codes of a rows x cols quantised matrix with the smallest ld (rows * 16 *
+ * ceil(cols/32)), and of its scales.  0 for a size below 1. */
+size_t fgemm_mxfp4_codes_size(int rows, int cols);
+size_t fgemm_mxfp4_scales_size(int rows, int cols);
+
+/*
+ * Quantise X (M x N, leading dimension ldx) along its rows, along its columns, or both in
+ * one pass over X:
+ *   row_codes, row_scales:  the quantised matrix M x N, blocks along a row of X
+ *   col_codes, col_scales:  the quantised matrix N x M (that of X^T), blocks down a column
+ * Both pointers of a direction are NULL when it is not wanted (its ld is then ignored); one
+ * direction at least is.  A layer Y = X W with X (M x K) and W (K x N) takes X's rows and
+ * W's columns forward, W's rows for the gradient of X and X's columns for that of W.
+ */
+fgemm_status fgemm_mxfp4_quantize(fgemm_dtype type, int M, int N, const void *X, int ldx,
+                                  void *row_codes, int ld_row_codes, void *row_scales,
+                                  void *col_codes, int ld_col_codes, void *col_scales,
+                                  cudaStream_t stream);
+
+/*
+ * The same for the gradient of a layer's output, Y = ReLU(X W + b):
+ *     g[i][j] = Y[i][j] > 0 ? G[i][j] : 0        (Y == NULL: g = G, no activation)
+ * is quantised as above (what G holds behind a closed gate, NaN included, does not
+ * matter), and bias_grad (N floats, or NULL) becomes sum_i g[i][j], summed in FP32 in a
+ * fixed order.  M = 0 writes bias_grad as 0.  G and Y have element type `type`.
+ * workspace: 16-byte aligned device memory, fgemm_mxfp4_quantize_grad_workspace_size(M, N)
+ * bytes at least; it may be NULL when bias_grad is NULL.
+ */
+size_t fgemm_mxfp4_quantize_grad_workspace_size(int M, int N);
+
+fgemm_status fgemm_mxfp4_quantize_grad(fgemm_dtype type, int M, int N, const void *G, int ldg,
+                                       const void *Y, int ldy, void *row_codes, int ld_row_codes,
+                                       void *row_scales, void *col_codes, int ld_col_codes,
+                                       void *col_scales, float *bias_grad, void *workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/* X (M x N, leading dimension ldx) = the values of a quantised matrix, rounded to `type`. */
+fgemm_status fgemm_mxfp4_dequantize(fgemm_dtype type, int M, int N, const void *codes, int ld_codes,
+                                    const void *scales, void *X, int ldx, cudaStream_t stream);
+
+/*
+ * Product of quantised matrices, A (M x K) and B (N x K), both with blocks along K:
+ *     C[i][j] = act( alpha * sum_k A[i][k] B[j][k] + beta * C[i][j] + bias[j] )
+ * C (M x N, leading dimension ldc) has element type `type`; bias: N floats or NULL; a
+ * nonzero apply_relu is act(x) = max(0, x).  Products and sums are formed in FP32 and C is
+ * rounded once.  alpha, beta, empty sizes: as for fgemm_sgemm (beta == 0 does not read C;
+ * alpha == 0 or K == 0 reads neither A nor B).
+ */
+fgemm_status fgemm_mxfp4_gemm(fgemm_dtype type, int M, int N, int K, float alpha,
+                              const void *A_codes, int ld_A_codes, const void *A_scales,
+                              const void *B_codes, int ld_B_codes, const void *B_scales,
+                              float beta, void *C, int ldc, const float *bias, int apply_relu,
+                              cudaStream_t stream);
+
+/*
+ * A layer on unquantised tokens: Y (M x N) = act(Q(X) W^T + bias), Q(X) being X (M x K)
+ * quantised along its rows as fgemm_mxfp4_quantize does and W (N x K) a quantised matrix.
+ * X and Y have element type `type`.
+ * workspace: 16-byte aligned device memory of fgemm_mxfp4_linear_workspace_size(M, N, K)
+ * bytes at least (0 for the few rows that are quantised on the way; NULL is then fine).
+ */
+size_t fgemm_mxfp4_linear_workspace_size(int M, int N, int K);
+
+fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const void *X, int ldx,
+                                const void *W_codes, int ld_W_codes, const void *W_scales,
+                                const float *bias, int apply_relu, void *Y, int ldy,
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
