@@ -61,5 +61,12 @@ struct GemmArgs {
 };
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream);
 
+// How a product runs: tiles of `nt` rows of A by 128 rows of B, each tile's K divided among
+// `ranks` CTAs of a cluster (0: whole tiles, by persistent CTAs).
+struct GemmPlan {
+    int nt, ranks;
+};
+GemmPlan plan_gemm(long long M, long long N, long long K, int sms);
+
 }  // namespace mx
 }  // namespace fgemm

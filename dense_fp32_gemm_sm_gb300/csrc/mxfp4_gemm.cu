@@ -1,6 +1,7 @@
-// mxfp4_gemm.cu -- the product of two quantised matrices.
-//
-// C[i][j] = act(alpha * sum_b 2^(sa + sb - 254) * sum_{k in block b} a[i][k] b[j][k] + beta C + bias)
+// mxfp4_gemm.cu -- the product of two quantised matrices: which kernel runs it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "fgemm_internal.h"
@@ -8,74 +9,28 @@
 
 namespace fgemm {
 namespace mx {
+
+template <class T>
+fgemm_status launch_tc_type(const GemmArgs &g, int nt, int ranks, cudaStream_t stream);
+extern template fgemm_status launch_tc_type<float>(const GemmArgs &, int, int, cudaStream_t);
+extern template fgemm_status launch_tc_type<__nv_bfloat16>(const GemmArgs &, int, int, cudaStream_t);
+extern template fgemm_status launch_tc_type<__half>(const GemmArgs &, int, int, cudaStream_t);
+
 namespace {
 
-constexpr int TILE = 64;
-
-// One 64 x 64 tile of C per CTA, 4 x 4 per thread; both operands' codes as FP32 in shared
-// memory, one block of 32 at a time, whose sum then gets both scales at once (their product
-// may be in range where a factor times a code is not).
+// C = act(beta * C + bias): alpha or K is 0.
 template <class T>
-__global__ void __launch_bounds__(256) gemm_simple_kernel(const GemmArgs g)
+__global__ void __launch_bounds__(256) no_products_kernel(const GemmArgs g)
 {
-    __shared__ float as[BLOCK][TILE + 1], bs[BLOCK][TILE + 1];
-    __shared__ int ea[TILE], eb[TILE];  // scale bytes, from 127; far out for NaN
-    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
-    const long long tiles_n = (g.N + TILE - 1) / TILE, tiles = tiles_n * ((g.M + TILE - 1) / TILE);
-    const long long blocks = blocks_of(g.K), atoms = atoms_of(blocks);
-    for (long long w = blockIdx.x; w < tiles; w += gridDim.x) {
-        const long long i0 = w / tiles_n * TILE, j0 = w % tiles_n * TILE;
-        float acc[4][4] = {};
-        for (long long b = 0; b < blocks; ++b) {
-            if (t < 2 * TILE) {
-                const bool first = t < TILE;
-                const int row = t % TILE;
-                const long long r = (first ? i0 : j0) + row;
-                const bool in = r < (first ? g.M : g.N);
-                uint4 c = make_uint4(0, 0, 0, 0);
-                int s = 0;
-                if (in) {
-                    c = *reinterpret_cast<const uint4 *>((first ? g.a + r * g.lda : g.b + r * g.ldb) + 16 * b);
-                    s = (first ? g.a_scales : g.b_scales)[scale_offset(r, b, atoms)];
-                }
-                (first ? ea : eb)[row] = s - 127;
-                const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x[8];
-                    decode8(words[q], x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) (first ? as : bs)[8 * q + k][row] = s == 255 ? __uint_as_float(0x7FFFFFFFu) : x[k];
-                }
-            }
-            __syncthreads();
-            float dot[4][4] = {};
-#pragma unroll 8
-            for (int k = 0; k < BLOCK; ++k) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) dot[i][j] = fmaf(as[k][ty + 16 * i], bs[k][tx + 16 * j], dot[i][j]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += ldexpf(dot[i][j], ea[ty + 16 * i] + eb[tx + 16 * j]);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const long long r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-                if (r >= g.M || c >= g.N) continue;
-                T *const out = static_cast<T *>(g.c) + r * g.ldc + c;
-                float o = g.alpha * acc[i][j];
-                if (g.beta != 0.0f) o = fmaf(g.beta, to_float(*out), o);
-                if (g.bias) o += g.bias[c];
-                if (g.relu) o = fmaxf(o, 0.0f);
-                *out = from_float<T>(o);
-            }
+    const long long total = (long long)g.M * g.N;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long r = i / g.N, c = i - r * g.N;
+        T *const out = static_cast<T *>(g.c) + r * g.ldc + c;
+        float o = 0.0f;
+        if (g.beta != 0.0f) o = g.beta * to_float(*out);
+        if (g.bias) o += g.bias[c];
+        if (g.relu) o = fmaxf(o, 0.0f);
+        *out = from_float<T>(o);
     }
 }
 
@@ -87,12 +42,28 @@ fgemm_status run_gemm(const GemmArgs &g, cudaStream_t stream)
         (void)cudaGetLastError();
         return FGEMM_ERR_LAUNCH;
     }
-    const long long tiles = ((g.N + TILE - 1) / TILE) * (long long)((g.M + TILE - 1) / TILE);
-    gemm_simple_kernel<T><<<(unsigned)std::min<long long>(tiles, 8ll * sms), 256, 0, stream>>>(g);
-    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    if (g.K == 0) {
+        const long long total = (long long)g.M * g.N;
+        no_products_kernel<T><<<(unsigned)std::min<long long>((total + 255) / 256, 8ll * sms), 256, 0, stream>>>(g);
+        return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    }
+    const GemmPlan plan = plan_gemm(g.M, g.N, g.K, sms);
+    return launch_tc_type<T>(g, plan.nt, plan.ranks, stream);
 }
 
 }  // namespace
+
+GemmPlan plan_gemm(long long M, long long N, long long K, int sms)
+{
+    const long long stages = (blocks_of(K) + 7) / 8, tiles_w = (N + 127) / 128;
+    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const long long tiles = tiles_w * ((M + nt - 1) / nt);
+    if (nt == 128 && tiles_w * ((M + 255) / 256) >= sms) return GemmPlan{256, 0};
+    if (nt == 128 && tiles >= sms) return GemmPlan{128, 0};
+    int ranks = 1;
+    while (ranks < 8 && 2 * ranks * tiles <= 2 * sms && 2 * ranks <= stages) ranks *= 2;
+    return GemmPlan{nt, ranks};
+}
 
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream)
 {

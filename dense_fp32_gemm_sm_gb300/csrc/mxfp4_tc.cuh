@@ -1,0 +1,380 @@
+// mxfp4_tc.cuh -- the product of two MXFP4 matrices on the tensor cores of sm_103a
+// (tcgen05.mma kind::mxf4, one E8M0 scale for every 32 codes, FP32 accumulators).
+//
+// C[i][j] = act(alpha * sum_b 2^(sa + sb - 254) sum_{k in b} a[i][k] b[j][k] + beta C + bias[j])
+//
+// The MMA's 128 rows are rows of B (columns of C) and its NT columns are rows of A: an
+// accumulator lane is then a column of C, a warp's 32 lanes are neighbours in a row of C,
+// and the epilogue stores whole segments of rows straight from registers, for any leading
+// dimension, alignment and type, with no pass through shared memory.  Few rows of A take a
+// narrow NT (16 and up) without touching the 128 rows of B that the MMA wants.
+//
+// A stage is 256 deep: 128 bytes of codes a row, the 128-byte swizzle's row, and two atoms of
+// scales (512 bytes, 128 rows x 4 blocks), which lie in memory as tcgen05.cp wants them.  One
+// warp's lane streams stages by TMA, another's copies each stage's scales to tensor memory
+// and issues four MMAs of depth 64; eight warps store the accumulators of the previous tile
+// meanwhile.  Few tiles with a long K are split over a cluster of CTAs, each with a range of
+// stages; their sums meet in shared memory and are added in rank order.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "mxfp4_device.cuh"
+#include "tc_gemm.cuh"
+
+namespace fgemm {
+namespace mx {
+
+constexpr int TC_ROWS = 128;     // rows of B a tile: tensor-memory lanes
+constexpr int TC_DEPTH = 256;    // codes a stage: 128 bytes a row
+constexpr int TC_BLOCKS = TC_DEPTH / BLOCK;
+constexpr int TC_THREADS = 320;  // producer, MMA, eight epilogue warps
+constexpr int EPI_WARPS = 8;
+
+template <int NT>
+struct TcTile {
+    static constexpr int W_BYTES = TC_ROWS * 128;
+    static constexpr int X_BYTES = NT * 128;
+    static constexpr int GROUPS = NT > 128 ? 2 : 1;  // 128-row groups of A's scales
+    static constexpr int SF_BYTES = 2 * ATOM_BYTES * (1 + GROUPS);
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
+    static constexpr int STAGES = NT > 128 ? 4 : NT > 64 ? 6 : 4;
+    // Tensor memory: two accumulators of NT columns, then two buffers of scales (4 columns an
+    // atom).  At NT = 256 those are 560 columns of the 512: the accumulators overlap by 64,
+    // and the epilogue reads the shared columns first.
+    static constexpr int ACC_STEP = NT == 256 ? 192 : NT;
+    static constexpr int SF_COLS = 8 * (1 + GROUPS);
+    static constexpr int SF_BASE = ACC_STEP + NT;
+    static constexpr int TMEM_USED = SF_BASE + 2 * SF_COLS;
+    static constexpr int TMEM_COLS = TMEM_USED > 256 ? 512 : TMEM_USED > 128 ? 256 : TMEM_USED > 64 ? 128 : 64;
+    static_assert(TMEM_USED <= 512, "tensor memory");
+    static constexpr int CHUNK = NT < 32 ? NT : 32;  // accumulator columns read at a time
+    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    // full[S], empty[S], acc_full[2], acc_free[2], drain, tensor-memory slot
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFFSET + (2 * STAGES + 5) * 8 + 8;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(STAGES * STAGE_BYTES >= TC_ROWS * NT * 4, "a split tile's sums take the stages' place");
+};
+
+struct TcArgs {
+    CUtensorMap w, x;  // codes of B and A: (bytes along K, rows), boxes of 128 bytes
+    const uint8_t *w_scales, *x_scales;
+    void *c;
+    const float *bias;
+    long long ldc, atoms;  // atoms: scale atoms of a 128-row group
+    int M, N, blocks;      // blocks: ceil(K / 32)
+    float alpha, beta;
+    int relu;
+    int tiles_x, tiles_w;
+    unsigned long long wait_limit_ns;
+    int withhold;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// kind::mxf4: A and B E2M1, scales E8M0, both K-major, 128 x n; the pair of scales (0 or 2)
+// of each 32-bit column that the MMA takes.
+__host__ __device__ constexpr uint32_t mxf4_idesc(int n, int pair)
+{
+    return ((uint32_t)pair << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(TC_ROWS >> 4) << 24) | ((uint32_t)pair << 29);
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// One atom of scales from shared memory to four columns of tensor memory (32 lanes of 16
+// bytes, repeated in each quarter).  The descriptor: 8 rows of 16 bytes are 128 bytes apart.
+__device__ __forceinline__ void copy_atom(uint32_t tmem, uint32_t smem_addr)
+{
+    const uint64_t desc = (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N])
+{
+    static_assert(N == 16 || N == 32, "columns");
+    if constexpr (N == 32) {
+        tc::tmem_ld_32cols(taddr, r);
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    }
+}
+
+// One element of C from its sum.
+template <class T>
+__device__ __forceinline__ void store_c(const TcArgs &p, T *out, float sum, float bias)
+{
+    float o = p.alpha * sum;
+    if (p.beta != 0.0f) o = fmaf(p.beta, to_float(*out), o);
+    o += bias;
+    if (p.relu) o = fmaxf(o, 0.0f);
+    *out = from_float<T>(o);
+}
+
+// SPLIT: the tile's stages are divided among the CTAs of a cluster, one tile a cluster;
+// otherwise CTAs walk over tiles.
+template <int NT, class T, bool SPLIT>
+__global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_constant__ TcArgs p, unsigned *err)
+{
+    using L = TcTile<NT>;
+    constexpr int S = L::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = tc::cvta_smem(smem), bars = sbase + L::BAR_OFFSET;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto acc_full_bar = [&](int a) { return bars + 8u * (2 * S + a); };
+    auto acc_free_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 5));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long lim = p.wait_limit_ns;
+    const int stages_k = (p.blocks + TC_BLOCKS - 1) / TC_BLOCKS;
+    int ranks = 1, rank = 0;
+    if constexpr (SPLIT) {
+        ranks = (int)cooperative_groups::this_cluster().num_blocks();
+        rank = (int)cooperative_groups::this_cluster().block_rank();
+    }
+    // This CTA's stages of every tile of its own, and its tiles.
+    const int k_first = (int)((long long)stages_k * rank / ranks), k_last = (int)((long long)stages_k * (rank + 1) / ranks);
+    const long long tiles = (long long)p.tiles_x * p.tiles_w;
+    const long long first_tile = SPLIT ? blockIdx.x / ranks : blockIdx.x;
+    const long long tile_step = SPLIT ? tiles : gridDim.x;
+    // Tile t: rows of A from x0, rows of B from w0.  Eight tiles along A are swept along B
+    // together, so that tiles in flight share operands in L2.
+    auto tile_at = [&](long long t, int &x0, int &w0) {
+        const long long per_group = 8ll * p.tiles_w, group = t / per_group, in_group = t - group * per_group;
+        const int height = min(p.tiles_x - (int)group * 8, 8);
+        x0 = ((int)group * 8 + (int)(in_group % height)) * NT;
+        w0 = (int)(in_group / height) * TC_ROWS;
+    };
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            tc::mbar_init(full_bar(s), 1);
+            tc::mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(acc_full_bar(a), 1);
+            tc::mbar_init(acc_free_bar(a), EPI_WARPS);
+        }
+        tc::mbar_init(drain_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::cvta_smem(tmem_slot)),
+                     "r"(L::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+
+    if (warp == 0) {
+        // ---- producer ----
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            for (long long t = first_tile; ok && t < tiles; t += tile_step) {
+                int x0, w0;
+                tile_at(t, x0, w0);
+                const uint8_t *const ws = p.w_scales + (long long)(w0 / 128) * p.atoms * ATOM_BYTES;
+                const uint8_t *const xs = p.x_scales + (long long)(x0 / 128) * p.atoms * ATOM_BYTES;
+                // The second group of A's scales, where the tile reaches into it.
+                const int groups = L::GROUPS == 2 && x0 + 128 < p.M ? 2 : 1;
+                for (int k = k_first; k < k_last; ++k, ++g) {
+                    const int s = g % S, round = g / S;
+                    if (round > 0 && !tc::mbar_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) {
+                        ok = false;
+                        break;
+                    }
+                    if (g == p.withhold) {  // testing: as if this copy never arrived
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
+                    const uint32_t sf_bytes = (int)min(p.atoms - 2ll * k, 2ll) * ATOM_BYTES;  // the last may be alone
+                    tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + L::X_BYTES + (1 + groups) * sf_bytes);
+                    tma_load_2d(at, &p.w, full_bar(s), k * 128, w0);
+                    tma_load_2d(at + L::W_BYTES, &p.x, full_bar(s), k * 128, x0);
+                    bulk_load(sf, ws + (long long)k * 2 * ATOM_BYTES, sf_bytes, full_bar(s));
+                    for (int i = 0; i < groups; ++i)
+                        bulk_load(sf + (1 + i) * 2 * ATOM_BYTES, xs + ((long long)i * p.atoms + 2ll * k) * ATOM_BYTES,
+                                  sf_bytes, full_bar(s));
+                }
+            }
+            // Never leave with copies in flight into this CTA's shared memory.
+            for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
+                tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA ----
+        if (lane == 0) {
+            int g = 0, j = 0;
+            bool ok = true;
+            for (long long t = first_tile; ok && t < tiles; t += tile_step, ++j) {
+                int x0, w0;
+                tile_at(t, x0, w0);
+                const int acc = j & 1;
+                // Tile j - 2's accumulator has been read; where the two overlap, the shared
+                // columns of tile j - 1's too.
+                const int before = NT == 256 ? j - 1 : j - 2;
+                if (before >= 0 &&
+                    !tc::mbar_wait(acc_free_bar(before & 1), (before >> 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
+                for (int k = k_first; k < k_last; ++k, ++g) {
+                    const int s = g % S;
+                    ok = tc::mbar_wait(full_bar(s), (g / S) & 1, err, tc::ERR_MMA_WAIT, lim);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
+                    const uint32_t sfw = tmem + L::SF_BASE + (uint32_t)((g & 1) * L::SF_COLS), sfx = sfw + 8;
+                    const int left = p.blocks - k * TC_BLOCKS;  // blocks from here on
+                    // Scales: atom a of B, then of each group of A.  (The MMAs that still read
+                    // this buffer come earlier in the tensor core's order.)
+                    for (int a = 0; a < (left > 4 ? 2 : 1); ++a) {
+                        copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
+                        for (int i = 0; i < L::GROUPS; ++i)
+                            copy_atom(sfx + 4 * (a * L::GROUPS + i), sf + (2 + 2 * i + a) * ATOM_BYTES);
+                    }
+                    const uint64_t wd = tc::kmajor_sw128_desc(at), xd = tc::kmajor_sw128_desc(at + L::W_BYTES);
+                    // A tile of 64 rows may start in the middle of its group's scales.
+                    const uint32_t sfx_at = sfx + (uint32_t)(NT < 128 ? (x0 % 128) / 32 : 0);
+                    const int steps = min((left + 1) / 2, 4);  // two blocks an MMA
+                    for (int i = 0; i < steps; ++i)
+                        mma_mxf4(d, wd + 2u * i, xd + 2u * i, mxf4_idesc(NT, 2 * (i & 1)), sfw + 4 * (i >> 1),
+                                 sfx_at + 4 * L::GROUPS * (i >> 1), k > k_first || i > 0);
+                    tc::umma_commit(empty_bar(s));
+                }
+                if (ok) tc::umma_commit(acc_full_bar(acc));
+            }
+            if (!ok) {  // give up: nothing issued may still be running at teardown
+                tc::umma_commit(drain_bar);
+                tc::mbar_wait(drain_bar, 0, err, tc::ERR_DRAIN, lim, false);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: warps of two sets of four, a set takes every other chunk ----
+        const int q = warp & 3, set = (warp - 2) >> 2;
+        int j = 0;
+        for (long long t = first_tile; t < tiles; t += tile_step, ++j) {
+            int x0, w0;
+            tile_at(t, x0, w0);
+            const int acc = j & 1;
+            if (!tc::mbar_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
+            tc::tc_fence_after();
+            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::ACC_STEP);
+            const int n = w0 + 32 * q + lane;
+            const float bias = !SPLIT && p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+            T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
+            constexpr int CHUNKS = NT / L::CHUNK;
+#pragma unroll 1
+            for (int i = set; i < CHUNKS; i += 2) {
+                // The first accumulator's last columns are the second one's first: those first.
+                const int c0 = (NT == 256 && acc == 0 ? CHUNKS - 1 - i : i) * L::CHUNK;
+                uint32_t r[L::CHUNK];
+                tmem_load(src + (uint32_t)c0, r);
+                if (NT == 256 && i == set) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(acc_free_bar(acc));
+                }
+                if constexpr (SPLIT) {
+                    // Column c of the tile: 128 sums, one for each row of B.
+                    float *const part = reinterpret_cast<float *>(smem) + c0 * TC_ROWS + 32 * q + lane;
+#pragma unroll
+                    for (int c = 0; c < L::CHUNK; ++c) part[c * TC_ROWS] = __uint_as_float(r[c]);
+                } else if (n < p.N) {
+                    if (x0 + c0 + L::CHUNK <= p.M) {
+#pragma unroll
+                        for (int c = 0; c < L::CHUNK; ++c)
+                            store_c(p, out + (c0 + c) * p.ldc, __uint_as_float(r[c]), bias);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < L::CHUNK; ++c)
+                            if (x0 + c0 + c < p.M) store_c(p, out + (c0 + c) * p.ldc, __uint_as_float(r[c]), bias);
+                    }
+                }
+            }
+            if (NT != 256) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(acc_free_bar(acc));
+            }
+        }
+        __syncwarp();
+    }
+
+    if constexpr (SPLIT) {
+        // Every CTA of the cluster adds up its share of the tile's columns over the ranks, in
+        // rank order.  (A rank that gave up leaves its memory as it was; the error word says
+        // that C is undefined.)
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        int x0, w0;
+        tile_at(first_tile, x0, w0);
+        const int from = NT * rank / ranks, to = NT * (rank + 1) / ranks;
+        for (int i = threadIdx.x; i < (to - from) * TC_ROWS; i += TC_THREADS) {
+            const int c = from + i / TC_ROWS, row = i % TC_ROWS, n = w0 + row;
+            if (x0 + c >= p.M || n >= p.N) continue;
+            float sum = 0.0f;
+            for (int r = 0; r < ranks; ++r)
+                sum += *cluster.map_shared_rank(reinterpret_cast<float *>(smem) + c * TC_ROWS + row, r);
+            store_c(p, static_cast<T *>(p.c) + (long long)(x0 + c) * p.ldc + n, sum, p.bias ? __ldg(p.bias + n) : 0.0f);
+        }
+        cluster.sync();
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM_COLS) : "memory");
+    }
+}
+
+}  // namespace mx
+}  // namespace fgemm
+

@@ -13,6 +13,7 @@
 #include "ctx_id.h"
 #include "fgemm_internal.h"
 #include "tc_gemm.cuh"
+#include "tc_host.h"
 
 namespace fgemm {
 
@@ -26,7 +27,9 @@ namespace {
 std::atomic<int> g_withhold_kb{-1};
 std::atomic<unsigned long long> g_wait_limit_ns{tc::kWaitLimitNs};
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn()
 {
     static std::atomic<void *> fn{nullptr};
     void *f = fn.load(std::memory_order_acquire);
@@ -41,6 +44,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
+int tc_withheld_k_block() { return g_withhold_kb.load(std::memory_order_relaxed); }
+unsigned long long tc_wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+
+namespace {
+
 // One operand as a 3-D tensor map (inner, outer, batch), `batch` problems `stride`
 // elements apart.  K-major storage (rows x K, K contiguous): inner = K, boxes of
 // 32 x box_rows with the 128-byte swizzle (the canonical UMMA layout).  MN-major
@@ -49,7 +57,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 bool make_operand_map(CUtensorMap *map, const float *base, bool kmajor, long long rows, long long K,
                       long long ld, long long batch, long long stride, int box_rows)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tc_encode_fn();
     if (!enc) return false;
     const long long outer = kmajor ? rows : K;
     if (batch <= 1) stride = ld * outer;  // unused extent-1 dimension; any legal stride
@@ -72,7 +80,7 @@ bool make_operand_map(CUtensorMap *map, const float *base, bool kmajor, long lon
 bool make_output_map(CUtensorMap *map, float *base, long long M, long long N, long long ldc,
                      long long batch, long long stride)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tc_encode_fn();
     if (!enc) return false;
     if (batch <= 1) stride = ldc * M;
     const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)batch};
@@ -86,9 +94,11 @@ bool make_output_map(CUtensorMap *map, float *base, long long M, long long N, lo
 
 int current_device(int *dev) { return cudaGetDevice(dev) == cudaSuccess ? 0 : -1; }
 
-// Device address of g_tc_error in the current context, looked up once per context
-// (a device reset loads the module again, and the variable may move).
-unsigned *error_word()
+}  // namespace
+
+// Looked up once per context (a device reset loads the module again, and the variable
+// may move).
+unsigned *tc_error_word()
 {
     struct Entry {
         unsigned long long ctx;
@@ -112,6 +122,8 @@ unsigned *error_word()
     cache[dev & 63] = Entry{current_context_id(), static_cast<unsigned *>(addr)};
     return static_cast<unsigned *>(addr);
 }
+
+namespace {
 
 // The kernel's dynamic shared memory attribute, set once per context.
 template <int MODE, int TA, int TB>
@@ -141,7 +153,7 @@ fgemm_status launch_tc_mode(const TcProblem &q, tc::TcParams &p, cudaStream_t st
         return FGEMM_ERR_NOT_SUPPORTED;
     p.tiles_m = (q.M + Shape::TILE_M - 1) / Shape::TILE_M;
     p.tiles_n = (q.N + Shape::TILE_N - 1) / Shape::TILE_N;
-    unsigned *err = error_word();
+    unsigned *err = tc_error_word();
     int sms = 0;
     if (!err || prepare_tc<MODE, TA, TB>() != cudaSuccess || device_sm_count(&sms) != 0) {
         (void)cudaGetLastError();
@@ -176,7 +188,7 @@ bool tc_supported(const TcProblem &q)
     if (q.lda >= lim || q.ldb >= lim || q.sA >= lim || q.sB >= lim) return false;
     // (the smallest tile of any instance is 128 x 128)
     if ((long long)((q.M + 127) / 128) * ((q.N + 127) / 128) > INT_MAX) return false;
-    return encode_fn() != nullptr;
+    return tc_encode_fn() != nullptr;
 }
 
 fgemm_status launch_tc(int mode, const TcProblem &q, cudaStream_t stream)
