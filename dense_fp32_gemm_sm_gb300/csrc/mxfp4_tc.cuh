@@ -65,6 +65,7 @@ struct TcArgs {
     int M, N, blocks;      // blocks: ceil(K / 32)
     float alpha, beta;
     int relu;
+    int c_pairs;  // 16-bit C: pairs of columns are 4-byte aligned
     int tiles_x, tiles_w;
     unsigned long long wait_limit_ns;
     int withhold;
@@ -114,6 +115,28 @@ __device__ __forceinline__ void copy_atom(uint32_t tmem, uint32_t smem_addr)
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xFFFFFFFF;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(one));
+    return one != 0;
+}
+
+// tc::mbar_wait by a whole warp: the same answer in all lanes, known to be uniform.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned *err, unsigned code,
+                                          unsigned long long limit_ns)
+{
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity, err, code, limit_ns));
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N])
 {
@@ -132,14 +155,66 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N])
 }
 
 // One element of C from its sum.
-template <class T>
-__device__ __forceinline__ void store_c(const TcArgs &p, T *out, float sum, float bias)
+template <class T, bool BETA, bool RELU>
+__device__ __forceinline__ float finish(const TcArgs &p, const T *out, float sum, float bias)
 {
-    float o = p.alpha * sum;
-    if (p.beta != 0.0f) o = fmaf(p.beta, to_float(*out), o);
-    o += bias;
-    if (p.relu) o = fmaxf(o, 0.0f);
-    *out = from_float<T>(o);
+    float o = fmaf(p.alpha, sum, bias);
+    if constexpr (BETA) o = fmaf(p.beta, to_float(*out), o);
+    if constexpr (RELU) o = fmaxf(o, 0.0f);
+    return o;
+}
+
+// N sums of this lane's column of C to `rows` rows of it, the first at `out`.  The 16-bit
+// types, where pairs of columns are aligned (`pairs`): lanes 2i and 2i + 1 exchange their
+// values of two rows, and each stores both columns of one row, 4 bytes a lane in place of 2.
+template <class T, bool BETA, bool RELU, int N>
+__device__ __forceinline__ void store_rows(const TcArgs &p, T *out, const uint32_t (&r)[N], float bias, int rows, bool in,
+                                           bool pairs)
+{
+    if constexpr (sizeof(T) == 2 && !BETA) {
+        if (pairs) {
+            const int odd = threadIdx.x & 1;
+            T *dst = out + (odd ? p.ldc - 1 : 0);
+#pragma unroll
+            for (int c = 0; c < N; c += 2, dst += 2 * p.ldc) {
+                const T a = from_float<T>(finish<T, BETA, RELU>(p, out, __uint_as_float(r[c]), bias));
+                const T b = from_float<T>(finish<T, BETA, RELU>(p, out, __uint_as_float(r[c + 1]), bias));
+                const uint32_t own = (uint32_t)reinterpret_cast<const uint16_t &>(a) |
+                                     (uint32_t)reinterpret_cast<const uint16_t &>(b) << 16;
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                const uint32_t both = __byte_perm(own, other, odd ? 0x3276u : 0x5410u);
+                if (in && c + odd < rows) *reinterpret_cast<uint32_t *>(dst) = both;
+            }
+            return;
+        }
+    }
+    if (!in) return;
+    if (rows >= N) {
+#pragma unroll
+        for (int c = 0; c < N; ++c, out += p.ldc)
+            *out = from_float<T>(finish<T, BETA, RELU>(p, out, __uint_as_float(r[c]), bias));
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c, out += p.ldc)
+            if (c < rows) *out = from_float<T>(finish<T, BETA, RELU>(p, out, __uint_as_float(r[c]), bias));
+    }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_chunk(const TcArgs &p, T *out, const uint32_t (&r)[N], float bias, int rows, bool in,
+                                            bool pairs)
+{
+    if (p.beta != 0.0f) {
+        if (p.relu)
+            store_rows<T, true, true>(p, out, r, bias, rows, in, pairs);
+        else
+            store_rows<T, true, false>(p, out, r, bias, rows, in, pairs);
+    } else {
+        if (p.relu)
+            store_rows<T, false, true>(p, out, r, bias, rows, in, pairs);
+        else
+            store_rows<T, false, false>(p, out, r, bias, rows, in, pairs);
+    }
 }
 
 // SPLIT: the tile's stages are divided among the CTAs of a cluster, one tile a cluster;
@@ -159,7 +234,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     const uint32_t drain_bar = bars + 8u * (2 * S + 4);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 5));
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (Through a shuffle, so that branches on the warp are known to be uniform.)
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const unsigned long long lim = p.wait_limit_ns;
     const int stages_k = (p.blocks + TC_BLOCKS - 1) / TC_BLOCKS;
     int ranks = 1, rank = 0;
@@ -203,95 +279,99 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
 
     if (warp == 0) {
-        // ---- producer ----
-        if (lane == 0) {
-            int g = 0;
-            bool ok = true;
-            for (long long t = first_tile; ok && t < tiles; t += tile_step) {
-                int x0, w0;
-                tile_at(t, x0, w0);
-                const uint8_t *const ws = p.w_scales + (long long)(w0 / 128) * p.atoms * ATOM_BYTES;
-                const uint8_t *const xs = p.x_scales + (long long)(x0 / 128) * p.atoms * ATOM_BYTES;
-                // The second group of A's scales, where the tile reaches into it.
-                const int groups = L::GROUPS == 2 && x0 + 128 < p.M ? 2 : 1;
-                for (int k = k_first; k < k_last; ++k, ++g) {
-                    const int s = g % S, round = g / S;
-                    if (round > 0 && !tc::mbar_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) {
-                        ok = false;
-                        break;
-                    }
-                    if (g == p.withhold) {  // testing: as if this copy never arrived
-                        ok = false;
-                        break;
-                    }
+        // ---- producer: the whole warp walks along, one lane issues ----
+        int g = 0;
+        bool ok = true;
+        for (long long t = first_tile; ok && t < tiles; t += tile_step) {
+            int x0, w0;
+            tile_at(t, x0, w0);
+            const uint8_t *const ws = p.w_scales + (long long)(w0 / 128) * p.atoms * ATOM_BYTES;
+            const uint8_t *const xs = p.x_scales + (long long)(x0 / 128) * p.atoms * ATOM_BYTES;
+            // The second group of A's scales, where the tile reaches into it.
+            const int groups = L::GROUPS == 2 && x0 + 128 < p.M ? 2 : 1;
+            for (int k = k_first; k < k_last; ++k, ++g) {
+                const int s = g % S, round = g / S;
+                ok = (round == 0 || warp_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) &&
+                     g != p.withhold;  // (testing: as if this copy never arrived)
+                if (!ok) break;
+                if (elect_one()) {
                     const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
-                    const uint32_t sf_bytes = (int)min(p.atoms - 2ll * k, 2ll) * ATOM_BYTES;  // the last may be alone
+                    const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;  // the last may be alone
                     tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + L::X_BYTES + (1 + groups) * sf_bytes);
                     tma_load_2d(at, &p.w, full_bar(s), k * 128, w0);
                     tma_load_2d(at + L::W_BYTES, &p.x, full_bar(s), k * 128, x0);
                     bulk_load(sf, ws + (long long)k * 2 * ATOM_BYTES, sf_bytes, full_bar(s));
-                    for (int i = 0; i < groups; ++i)
-                        bulk_load(sf + (1 + i) * 2 * ATOM_BYTES, xs + ((long long)i * p.atoms + 2ll * k) * ATOM_BYTES,
-                                  sf_bytes, full_bar(s));
+                    bulk_load(sf + 2 * ATOM_BYTES, xs + 2ll * k * ATOM_BYTES, sf_bytes, full_bar(s));
+                    if (groups == 2)
+                        bulk_load(sf + 4 * ATOM_BYTES, xs + (p.atoms + 2ll * k) * ATOM_BYTES, sf_bytes, full_bar(s));
                 }
+                __syncwarp();
             }
-            // Never leave with copies in flight into this CTA's shared memory.
-            for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
-                tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
         }
+        // Never leave with copies in flight into this CTA's shared memory.
+        for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
+            tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
         __syncwarp();
     } else if (warp == 1) {
-        // ---- MMA ----
-        if (lane == 0) {
-            int g = 0, j = 0;
-            bool ok = true;
-            for (long long t = first_tile; ok && t < tiles; t += tile_step, ++j) {
-                int x0, w0;
-                tile_at(t, x0, w0);
-                const int acc = j & 1;
-                // Tile j - 2's accumulator has been read; where the two overlap, the shared
-                // columns of tile j - 1's too.
-                const int before = NT == 256 ? j - 1 : j - 2;
-                if (before >= 0 &&
-                    !tc::mbar_wait(acc_free_bar(before & 1), (before >> 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
-                    ok = false;
-                    break;
-                }
+        // ---- MMA: the whole warp walks along, one lane issues ----
+        // (Inside a branch on the lane number, the operands of each tcgen05 instruction have to be
+        // moved to uniform registers one by one, and issuing took 128 cycles an MMA.)
+        int g = 0, j = 0;
+        bool ok = true;
+        for (long long t = first_tile; ok && t < tiles; t += tile_step, ++j) {
+            int x0, w0;
+            tile_at(t, x0, w0);
+            const int acc = j & 1;
+            // Tile j - 2's accumulator has been read; where the two overlap, the shared
+            // columns of tile j - 1's too.
+            const int before = NT == 256 ? j - 1 : j - 2;
+            if (before >= 0 && !warp_wait(acc_free_bar(before & 1), (before >> 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
+                ok = false;
+                break;
+            }
+            tc::tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
+            for (int k = k_first; k < k_last; ++k, ++g) {
+                const int s = g % S;
+                ok = warp_wait(full_bar(s), (g / S) & 1, err, tc::ERR_MMA_WAIT, lim);
+                if (!ok) break;
                 tc::tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
-                for (int k = k_first; k < k_last; ++k, ++g) {
-                    const int s = g % S;
-                    ok = tc::mbar_wait(full_bar(s), (g / S) & 1, err, tc::ERR_MMA_WAIT, lim);
-                    if (!ok) break;
-                    tc::tc_fence_after();
+                if (elect_one()) {
                     const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
                     const uint32_t sfw = tmem + L::SF_BASE + (uint32_t)((g & 1) * L::SF_COLS), sfx = sfw + 8;
                     const int left = p.blocks - k * TC_BLOCKS;  // blocks from here on
-                    // Scales: atom a of B, then of each group of A.  (The MMAs that still read
-                    // this buffer come earlier in the tensor core's order.)
-                    for (int a = 0; a < (left > 4 ? 2 : 1); ++a) {
-                        copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
-                        for (int i = 0; i < L::GROUPS; ++i)
-                            copy_atom(sfx + 4 * (a * L::GROUPS + i), sf + (2 + 2 * i + a) * ATOM_BYTES);
-                    }
                     const uint64_t wd = tc::kmajor_sw128_desc(at), xd = tc::kmajor_sw128_desc(at + L::W_BYTES);
                     // A tile of 64 rows may start in the middle of its group's scales.
                     const uint32_t sfx_at = sfx + (uint32_t)(NT < 128 ? (x0 % 128) / 32 : 0);
-                    const int steps = min((left + 1) / 2, 4);  // two blocks an MMA
-                    for (int i = 0; i < steps; ++i)
-                        mma_mxf4(d, wd + 2u * i, xd + 2u * i, mxf4_idesc(NT, 2 * (i & 1)), sfw + 4 * (i >> 1),
-                                 sfx_at + 4 * L::GROUPS * (i >> 1), k > k_first || i > 0);
+                    // Two atoms of scales, each for two MMAs of two blocks.  (The MMAs that still
+                    // read this buffer come earlier in the tensor core's order.)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        if (left > 4 * a) {
+                            copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
+#pragma unroll
+                            for (int i = 0; i < L::GROUPS; ++i)
+                                copy_atom(sfx + 4 * (a * L::GROUPS + i), sf + (2 + 2 * i + a) * ATOM_BYTES);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (left > 2 * i)
+                            mma_mxf4(d, wd + 2u * i, xd + 2u * i, mxf4_idesc(NT, 2 * (i & 1)), sfw + 4 * (i >> 1),
+                                     sfx_at + 4 * L::GROUPS * (i >> 1), k > k_first || i > 0);
                     tc::umma_commit(empty_bar(s));
+                    if (k + 1 == k_last) tc::umma_commit(acc_full_bar(acc));
                 }
-                if (ok) tc::umma_commit(acc_full_bar(acc));
+                __syncwarp();
             }
-            if (!ok) {  // give up: nothing issued may still be running at teardown
-                tc::umma_commit(drain_bar);
-                tc::mbar_wait(drain_bar, 0, err, tc::ERR_DRAIN, lim, false);
-            }
+        }
+        if (!ok) {  // give up: nothing issued may still be running at teardown
+            if (elect_one()) tc::umma_commit(drain_bar);
+            __syncwarp();
+            tc::mbar_wait(drain_bar, 0, err, tc::ERR_DRAIN, lim, false);
         }
         __syncwarp();
     } else {
@@ -308,6 +388,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             const int n = w0 + 32 * q + lane;
             const float bias = !SPLIT && p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
             T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
+            // (N even: a pair is inside or outside as a whole)
+            const bool pairs = p.c_pairs && (p.N & 1) == 0;
             constexpr int CHUNKS = NT / L::CHUNK;
 #pragma unroll 1
             for (int i = set; i < CHUNKS; i += 2) {
@@ -325,16 +407,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                     float *const part = reinterpret_cast<float *>(smem) + c0 * TC_ROWS + 32 * q + lane;
 #pragma unroll
                     for (int c = 0; c < L::CHUNK; ++c) part[c * TC_ROWS] = __uint_as_float(r[c]);
-                } else if (n < p.N) {
-                    if (x0 + c0 + L::CHUNK <= p.M) {
-#pragma unroll
-                        for (int c = 0; c < L::CHUNK; ++c)
-                            store_c(p, out + (c0 + c) * p.ldc, __uint_as_float(r[c]), bias);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < L::CHUNK; ++c)
-                            if (x0 + c0 + c < p.M) store_c(p, out + (c0 + c) * p.ldc, __uint_as_float(r[c]), bias);
-                    }
+                } else {
+                    store_chunk(p, out + c0 * p.ldc, r, bias, p.M - x0 - c0, n < p.N, pairs);
                 }
             }
             if (NT != 256) {
@@ -362,7 +436,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             float sum = 0.0f;
             for (int r = 0; r < ranks; ++r)
                 sum += *cluster.map_shared_rank(reinterpret_cast<float *>(smem) + c * TC_ROWS + row, r);
-            store_c(p, static_cast<T *>(p.c) + (long long)(x0 + c) * p.ldc + n, sum, p.bias ? __ldg(p.bias + n) : 0.0f);
+            T *const out = static_cast<T *>(p.c) + (long long)(x0 + c) * p.ldc + n;
+            const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
+            float o = p.beta != 0.0f ? finish<T, true, false>(p, out, sum, bias) : finish<T, false, false>(p, out, sum, bias);
+            if (p.relu) o = fmaxf(o, 0.0f);
+            *out = from_float<T>(o);
         }
         cluster.sync();
     }

@@ -64,6 +64,7 @@ static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t s
     p.alpha = g.alpha;
     p.beta = g.beta;
     p.relu = g.relu;
+    p.c_pairs = reinterpret_cast<uintptr_t>(g.c) % 4 == 0 && g.ldc % 2 == 0;
     p.tiles_x = (int)(((long long)g.M + NT - 1) / NT);
     p.tiles_w = (int)(((long long)g.N + TC_ROWS - 1) / TC_ROWS);
     p.wait_limit_ns = tc_wait_limit_ns();
