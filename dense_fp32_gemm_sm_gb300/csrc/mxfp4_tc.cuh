@@ -453,6 +453,268 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     }
 }
 
+// ---- pairs of CTAs ----------------------------------------------------------------------
+
+// Large products: a cluster of two CTAs works on 256 rows of B x 256 rows of A with
+// tcgen05.mma.cta_group::2.  Each holds 128 rows of both operands in its shared memory and
+// the sums of its own 128 rows of B in its tensor memory, so a stage brings 35 KB to each SM
+// where one CTA alone needs 51 KB for as many sums: L2's bandwidth is what bounds that (the
+// 51 KB stages came at 24 TB/s).  CTA 0 issues for both; its `full` barriers count the
+// bytes that arrive in either CTA.
+template <int NT>
+struct PairTile {
+    static constexpr int W_BYTES = 128 * 128, X_BYTES = NT / 2 * 128;  // bytes of either operand's rows
+    static constexpr int SF_BYTES = 3 * 2 * ATOM_BYTES;  // own rows of B, both groups of A
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
+    static constexpr int STAGES = NT == 256 ? 6 : 7;
+    static constexpr int ACC_STEP = 192, SF_BASE = ACC_STEP + NT, SF_COLS = 24;
+    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFFSET + (2 * STAGES + 5) * 8 + 8;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(STAGE_BYTES % 1024 == 0, "the swizzle's alignment");
+};
+
+struct PairArgs {
+    CUtensorMap w, x;    // codes: (bytes along K, rows), boxes of 128 x 128
+    CUtensorMap sw, sx;  // scales: (words of an atom, atoms along K, groups of 128 rows)
+    TcArgs t;            // the rest (its own maps and scale pointers are not used)
+};
+
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// TMA loads of a CTA pair: into this CTA's memory, counted by a barrier of either CTA.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_copy_atom(uint32_t tmem, uint32_t smem_addr)
+{
+    const uint64_t desc = (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` of both CTAs when the MMAs and copies issued so far are complete.
+__device__ __forceinline__ void pair_commit(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int NT, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
+    mxfp4_pair_kernel(const __grid_constant__ PairArgs args, unsigned *err)
+{
+    using L = PairTile<NT>;
+    constexpr int S = L::STAGES;
+    const TcArgs &p = args.t;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = tc::cvta_smem(smem), bars = sbase + L::BAR_OFFSET;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto acc_full_bar = [&](int a) { return bars + 8u * (2 * S + a); };
+    auto acc_free_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 5));
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    const unsigned long long lim = p.wait_limit_ns;
+    const int stages_k = (p.blocks + TC_BLOCKS - 1) / TC_BLOCKS;
+    const long long tiles = (long long)p.tiles_x * p.tiles_w;
+    const long long first_tile = blockIdx.x / 2, tile_step = gridDim.x / 2;
+    auto tile_at = [&](long long t, int &x0, int &w0) {  // as above; w0: the pair's first row of B
+        const long long per_group = 8ll * p.tiles_w, group = t / per_group, in_group = t - group * per_group;
+        const int height = min(p.tiles_x - (int)group * 8, 8);
+        x0 = ((int)group * 8 + (int)(in_group % height)) * NT;
+        w0 = (int)(in_group / height) * 256;
+    };
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            tc::mbar_init(full_bar(s), 1);
+            tc::mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(acc_full_bar(a), 1);
+            tc::mbar_init(acc_free_bar(a), 2 * EPI_WARPS);
+        }
+        tc::mbar_init(drain_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::cvta_smem(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc::tc_fence_before();
+    cluster.sync();
+    tc::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
+
+    if (warp == 0) {
+        // ---- producer, one in each CTA ----
+        int g = 0;
+        bool ok = true;
+        for (long long t = first_tile; ok && t < tiles; t += tile_step) {
+            int x0, w0;
+            tile_at(t, x0, w0);
+            for (int k = 0; k < stages_k; ++k, ++g) {
+                const int s = g % S, round = g / S;
+                ok = (round == 0 || warp_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) &&
+                     g != p.withhold;  // (testing: as if this copy never arrived)
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
+                    if (rank == 0) tc::mbar_arrive_expect_tx(full_bar(s), 2 * L::STAGE_BYTES);
+                    const uint32_t bar = map_to_rank(full_bar(s), 0);
+                    pair_load_2d(at, &args.w, bar, k * 128, w0 + 128 * rank);
+                    pair_load_2d(at + L::W_BYTES, &args.x, bar, k * 128, x0 + NT / 2 * rank);
+                    pair_load_3d(sf, &args.sw, bar, 0, 2 * k, w0 / 128 + rank);
+                    pair_load_3d(sf + 2 * ATOM_BYTES, &args.sx, bar, 0, 2 * k, x0 / 128);
+                }
+                __syncwarp();
+            }
+        }
+        // Never leave with copies in flight into either CTA's shared memory.
+        if (rank == 0)
+            for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
+                tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA, by CTA 0 for both ----
+        if (rank == 0) {
+            int g = 0, j = 0;
+            bool ok = true;
+            for (long long t = first_tile; ok && t < tiles; t += tile_step, ++j) {
+                int x0, w0;
+                tile_at(t, x0, w0);
+                const int acc = j & 1, before = NT == 256 ? j - 1 : j - 2;
+                if (before >= 0 && !warp_wait(acc_free_bar(before & 1), (before >> 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
+                for (int k = 0; k < stages_k; ++k, ++g) {
+                    const int s = g % S;
+                    ok = warp_wait(full_bar(s), (g / S) & 1, err, tc::ERR_MMA_WAIT, lim);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
+                        const uint32_t sfw = tmem + L::SF_BASE + (uint32_t)((g & 1) * L::SF_COLS), sfx = sfw + 8;
+                        const int left = p.blocks - k * TC_BLOCKS;
+                        const uint64_t wd = tc::kmajor_sw128_desc(at), xd = tc::kmajor_sw128_desc(at + L::W_BYTES);
+                        const uint32_t sfx_at = sfx + (uint32_t)(x0 % 128) / 32;  // a tile may start inside its group
+                        constexpr uint32_t tall = (uint32_t)(TC_ROWS >> 4) << 24;  // 256 rows in place of 128
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            if (left > 4 * a) {
+                                pair_copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
+                                pair_copy_atom(sfx + 8 * a, sf + (2 + a) * ATOM_BYTES);
+                                pair_copy_atom(sfx + 8 * a + 4, sf + (4 + a) * ATOM_BYTES);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (left > 2 * i)
+                                pair_mma(d, wd + 2u * i, xd + 2u * i, mxf4_idesc(NT, 2 * (i & 1)) + tall,
+                                         sfw + 4 * (i >> 1), sfx_at + 8 * (i >> 1), k > 0 || i > 0);
+                        pair_commit(empty_bar(s));
+                        if (k + 1 == stages_k) pair_commit(acc_full_bar(acc));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {  // give up: nothing issued may still be running at teardown
+                if (elect_one()) pair_commit(drain_bar);
+                __syncwarp();
+                tc::mbar_wait(drain_bar, 0, err, tc::ERR_DRAIN, lim, false);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue, each CTA its own 128 rows of B ----
+        const int q = warp & 3, set = (warp - 2) >> 2;
+        const bool pairs = p.c_pairs && (p.N & 1) == 0;
+        int j = 0;
+        for (long long t = first_tile; t < tiles; t += tile_step, ++j) {
+            int x0, w0;
+            tile_at(t, x0, w0);
+            const int acc = j & 1;
+            if (!warp_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
+            tc::tc_fence_after();
+            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::ACC_STEP);
+            const int n = w0 + 128 * rank + 32 * q + lane;
+            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+            T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
+#pragma unroll 1
+            for (int i = set; i < NT / 32; i += 2) {
+                const int c0 = (NT == 256 && acc == 0 ? 7 - i : i) * 32;
+                uint32_t r[32];
+                tmem_load(src + (uint32_t)c0, r);
+                if (NT == 256 ? i == set : i + 2 >= NT / 32) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(map_to_rank(acc_free_bar(acc), 0));
+                }
+                store_chunk(p, out + c0 * p.ldc, r, bias, p.M - x0 - c0, n < p.N, pairs);
+            }
+        }
+        __syncwarp();
+    }
+
+    // Neither CTA leaves while the other may still reach its memory.
+    tc::tc_fence_before();
+    cluster.sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
 }  // namespace mx
 }  // namespace fgemm
-

@@ -26,32 +26,24 @@ static bool make_codes_map(CUtensorMap *map, const uint8_t *codes, long long row
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, class T, bool SPLIT>
-static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t stream)
+// Scales as a tensor map of whole atoms: (128 words, atoms along K, 128-row groups), boxes of
+// two atoms of `groups` groups; beyond the matrix it reads 0.
+static bool make_scales_map(CUtensorMap *map, const uint8_t *scales, long long rows, long long atoms, int groups)
 {
-    using L = TcTile<NT>;
-    const auto kernel = mxfp4_tc_kernel<NT, T, SPLIT>;
-    static std::atomic<unsigned long long> ready_ctx[64];
-    int dev = 0, sms = 0;
-    unsigned *const err = tc_error_word();
-    if (!err || cudaGetDevice(&dev) != cudaSuccess || device_sm_count(&sms) != 0) {
-        (void)cudaGetLastError();
-        return FGEMM_ERR_LAUNCH;
-    }
-    std::atomic<unsigned long long> &ready = ready_ctx[dev & 63];
-    const unsigned long long ctx = current_context_id();
-    if (ctx == 0 || ready.load(std::memory_order_acquire) != ctx) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return FGEMM_ERR_LAUNCH;
-        }
-        ready.store(current_context_id(), std::memory_order_release);
-    }
-    TcArgs p;
-    std::memset(&p, 0, sizeof(p));
+    const auto encode = tc_encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {ATOM_BYTES / 4, (cuuint64_t)atoms, (cuuint64_t)((rows + ATOM_ROWS - 1) / ATOM_ROWS)};
+    const cuuint64_t strides[2] = {ATOM_BYTES, (cuuint64_t)(atoms * ATOM_BYTES)};
+    const cuuint32_t box[3] = {ATOM_BYTES / 4, 2, (cuuint32_t)groups}, estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The arguments that do not depend on the kernel, for tiles of tile_x rows of A and tile_w of B.
+static void fill_args(TcArgs &p, const GemmArgs &g, int tile_x, int tile_w)
+{
     const long long blocks = blocks_of(g.K);
-    if (!make_codes_map(&p.w, g.b, g.N, blocks, g.ldb, TC_ROWS) || !make_codes_map(&p.x, g.a, g.M, blocks, g.lda, NT))
-        return FGEMM_ERR_NOT_SUPPORTED;
     p.w_scales = g.b_scales;
     p.x_scales = g.a_scales;
     p.c = g.c;
@@ -65,10 +57,68 @@ static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t s
     p.beta = g.beta;
     p.relu = g.relu;
     p.c_pairs = reinterpret_cast<uintptr_t>(g.c) % 4 == 0 && g.ldc % 2 == 0;
-    p.tiles_x = (int)(((long long)g.M + NT - 1) / NT);
-    p.tiles_w = (int)(((long long)g.N + TC_ROWS - 1) / TC_ROWS);
+    p.tiles_x = (int)(((long long)g.M + tile_x - 1) / tile_x);
+    p.tiles_w = (int)(((long long)g.N + tile_w - 1) / tile_w);
     p.wait_limit_ns = tc_wait_limit_ns();
     p.withhold = tc_withheld_k_block();
+}
+
+// What a launch needs besides its arguments: the error word, the SM count, and the kernel
+// opted in to its shared memory, once per context (`Kernel` keeps instances' records apart).
+template <class Kernel, Kernel kernel>
+static bool prepare(int smem_bytes, unsigned **err, int *sms)
+{
+    static std::atomic<unsigned long long> ready_ctx[64];
+    int dev = 0;
+    *err = tc_error_word();
+    if (!*err || cudaGetDevice(&dev) != cudaSuccess || device_sm_count(sms) != 0) return false;
+    std::atomic<unsigned long long> &ready = ready_ctx[dev & 63];
+    const unsigned long long ctx = current_context_id();
+    if (ctx != 0 && ready.load(std::memory_order_acquire) == ctx) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess) return false;
+    ready.store(current_context_id(), std::memory_order_release);
+    return true;
+}
+
+// Pairs of CTAs, tiles of 256 rows of B by NT of A.
+template <int NT, class T>
+static fgemm_status launch_pairs(const GemmArgs &g, cudaStream_t stream)
+{
+    using L = PairTile<NT>;
+    unsigned *err = nullptr;
+    int sms = 0;
+    constexpr auto kernel = &mxfp4_pair_kernel<NT, T>;
+    if (!prepare<decltype(kernel), kernel>(L::SMEM_BYTES, &err, &sms)) {
+        (void)cudaGetLastError();
+        return FGEMM_ERR_LAUNCH;
+    }
+    PairArgs p;
+    std::memset(&p, 0, sizeof(p));
+    fill_args(p.t, g, NT, 256);
+    if (!make_codes_map(&p.w, g.b, g.N, p.t.blocks, g.ldb, 128) || !make_codes_map(&p.x, g.a, g.M, p.t.blocks, g.lda, NT / 2) ||
+        !make_scales_map(&p.sw, g.b_scales, g.N, p.t.atoms, 1) || !make_scales_map(&p.sx, g.a_scales, g.M, p.t.atoms, 2))
+        return FGEMM_ERR_NOT_SUPPORTED;
+    const long long tiles = (long long)p.t.tiles_x * p.t.tiles_w, most = sms / 2;
+    kernel<<<(unsigned)(2 * (tiles < most ? tiles : most)), TC_THREADS, L::SMEM_BYTES, stream>>>(p, err);
+    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+}
+
+template <int NT, class T, bool SPLIT>
+static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t stream)
+{
+    using L = TcTile<NT>;
+    constexpr auto kernel = &mxfp4_tc_kernel<NT, T, SPLIT>;
+    unsigned *err = nullptr;
+    int sms = 0;
+    if (!prepare<decltype(kernel), kernel>(L::SMEM_BYTES, &err, &sms)) {
+        (void)cudaGetLastError();
+        return FGEMM_ERR_LAUNCH;
+    }
+    TcArgs p;
+    std::memset(&p, 0, sizeof(p));
+    fill_args(p, g, NT, TC_ROWS);
+    if (!make_codes_map(&p.w, g.b, g.N, p.blocks, g.ldb, TC_ROWS) || !make_codes_map(&p.x, g.a, g.M, p.blocks, g.lda, NT))
+        return FGEMM_ERR_NOT_SUPPORTED;
     const long long tiles = (long long)p.tiles_x * p.tiles_w;
     if (!SPLIT) {
         kernel<<<(unsigned)(tiles < sms ? tiles : sms), TC_THREADS, L::SMEM_BYTES, stream>>>(p, err);
@@ -98,6 +148,8 @@ static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t s
 template <class T>
 fgemm_status launch_tc_type(const GemmArgs &g, int nt, int ranks, cudaStream_t stream)
 {
+    if (ranks == 0 && nt == 512) return launch_pairs<256, T>(g, stream);
+    if (ranks == 0 && nt == 384) return launch_pairs<192, T>(g, stream);
     if (ranks == 0)
         return nt == 256 ? launch_instance<256, T, false>(g, 0, stream) : launch_instance<128, T, false>(g, 0, stream);
     switch (nt) {
