@@ -385,11 +385,22 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
 _TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
 
 
+try:  # the current stream's handle without building a Stream object (2 us a call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    _raw_stream = None
+
+
+def _on(stream, x):
+    """Handle of the stream a call runs on: the given one, or torch's current one on x's device."""
+    if stream is None and _raw_stream is not None and not isinstance(x, int) and x is not None:
+        return _raw_stream(x.get_device()) or None
+    return _stream(stream, x)
+
+
 def _mat(x, type):
     """Address of an unquantised matrix: a CUDA tensor of the call's type, or an address."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x or None
     if not x.is_cuda or not 0 <= type < 3 or str(x.dtype) != _TYPE_NAMES[type]:
         raise TypeError("fgemm type %r takes a CUDA tensor of that type (got %s on %s)"
@@ -399,9 +410,7 @@ def _mat(x, type):
 
 def _bytes(x):
     """Address of codes, scales or a workspace: a CUDA tensor of any type, or an address."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x or None
     if not x.is_cuda:
         raise TypeError("expected a CUDA tensor (got one on %s)" % (x.device,))
@@ -424,7 +433,7 @@ def mxfp4_quantize(type, M, N, X, ldx, row_codes, ld_row_codes, row_scales, col_
     None for the codes and scales of a direction that is not wanted."""
     st = library().fgemm_mxfp4_quantize(
         type, M, N, _mat(X, type), ldx, _bytes(row_codes), ld_row_codes, _bytes(row_scales),
-        _bytes(col_codes), ld_col_codes, _bytes(col_scales), _stream(stream, X))
+        _bytes(col_codes), ld_col_codes, _bytes(col_scales), _on(stream, X))
     if check:
         _check(st, "fgemm_mxfp4_quantize")
     return st
@@ -443,7 +452,7 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
     st = library().fgemm_mxfp4_quantize_grad(
         type, M, N, _mat(G, type), ldg, _mat(Y, type), ldy, _bytes(row_codes), ld_row_codes,
         _bytes(row_scales), _bytes(col_codes), ld_col_codes, _bytes(col_scales), _ptr(bias_grad),
-        _bytes(workspace), workspace_bytes, _stream(stream, G, bias_grad))
+        _bytes(workspace), workspace_bytes, _on(stream, bias_grad if G is None else G))
     if check:
         _check(st, "fgemm_mxfp4_quantize_grad")
     return st
@@ -452,7 +461,7 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
 def mxfp4_dequantize(type, M, N, codes, ld_codes, scales, X, ldx, stream=None, check=True) -> int:
     """``fgemm_mxfp4_dequantize``: X = the values of a quantised matrix."""
     st = library().fgemm_mxfp4_dequantize(type, M, N, _bytes(codes), ld_codes, _bytes(scales),
-                                          _mat(X, type), ldx, _stream(stream, X))
+                                          _mat(X, type), ldx, _on(stream, X))
     if check:
         _check(st, "fgemm_mxfp4_dequantize")
     return st
@@ -465,7 +474,7 @@ def mxfp4_gemm(type, M, N, K, alpha, A_codes, ld_A_codes, A_scales, B_codes, ld_
     st = library().fgemm_mxfp4_gemm(
         type, M, N, K, alpha, _bytes(A_codes), ld_A_codes, _bytes(A_scales), _bytes(B_codes),
         ld_B_codes, _bytes(B_scales), beta, _mat(C, type), ldc, _ptr(bias), 1 if apply_relu else 0,
-        _stream(stream, C))
+        _on(stream, C))
     if check:
         _check(st, "fgemm_mxfp4_gemm")
     return st
@@ -482,7 +491,7 @@ def mxfp4_linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias, app
     st = library().fgemm_mxfp4_linear(
         type, M, N, K, _mat(X, type), ldx, _bytes(W_codes), ld_W_codes, _bytes(W_scales),
         _ptr(bias), 1 if apply_relu else 0, _mat(Y, type), ldy, _bytes(workspace),
-        workspace_bytes, _stream(stream, Y))
+        workspace_bytes, _on(stream, Y))
     if check:
         _check(st, "fgemm_mxfp4_linear")
     return st

@@ -37,6 +37,7 @@ struct QuantParams {
     long long ld_col;
     float *bias_grad;  // or null
     float *partial;    // one partial column sum per 128 rows
+    int early;         // let the next kernel of the stream start (it waits before it reads)
 };
 fgemm_status launch_quantize(fgemm_dtype type, const QuantParams &p, cudaStream_t stream);
 
@@ -58,15 +59,25 @@ struct GemmArgs {
     long long ldc;
     const float *bias;
     int relu;
+    int dependent;  // A is written by the quantising kernel launched just before, with `early`
 };
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream);
 
 // How a product runs: tiles of `nt` rows of A by 128 rows of B, each tile's K divided among
-// `ranks` CTAs of a cluster (0: whole tiles, by persistent CTAs).
+// `ranks` CTAs of a cluster (0: whole tiles, by persistent CTAs; nt is then 128, or 512 for
+// pairs of CTAs with 256 rows of A, 384 for pairs with 192).
 struct GemmPlan {
     int nt, ranks;
 };
 GemmPlan plan_gemm(long long M, long long N, long long K, int sms);
+
+// A layer on at most LINEAR_ROWS unquantised tokens in one kernel: every CTA of a cluster of
+// eight at most quantises its part of them into FUSED_SMEM bytes of shared memory.
+constexpr int LINEAR_ROWS = 4;
+constexpr int FUSED_SMEM = 64 * 1024;
+bool linear_fused(long long M, long long K);
+GemmPlan plan_linear(long long N, long long K, int sms);
+fgemm_status launch_linear(fgemm_dtype type, const void *x, long long ldx, const GemmArgs &g, cudaStream_t stream);
 
 }  // namespace mx
 }  // namespace fgemm

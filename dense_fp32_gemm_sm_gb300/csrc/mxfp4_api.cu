@@ -202,7 +202,7 @@ fgemm_status fgemm_mxfp4_gemm(fgemm_dtype type, int M, int N, int K, float alpha
 
 size_t fgemm_mxfp4_linear_workspace_size(int M, int N, int K)
 {
-    if (M < 1 || N < 1 || K < 1) return 0;
+    if (M < 1 || N < 1 || K < 1 || linear_fused(M, K)) return 0;
     return sat_add(round256(codes_bytes(M, K)), scales_bytes(M, K));
 }
 
@@ -221,22 +221,11 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
     const size_t need = fgemm_mxfp4_linear_workspace_size(M, N, K);
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return FGEMM_ERR_INVALID_VALUE;
     if (!dims_supported(M, N, K)) return FGEMM_ERR_NOT_SUPPORTED;
-    uint8_t *const codes = static_cast<uint8_t *>(workspace);
-    uint8_t *const scales = K > 0 ? codes + round256(codes_bytes(M, K)) : nullptr;
-    const int ld = (int)(16 * blocks_of(K > 0 ? K : 1));
-    if (K > 0) {
-        const fgemm_status st = launch_quantize(type, quant_params(M, K, X, ldx, Direction{codes, ld, scales},
-                                                                    Direction{nullptr, 0, nullptr}), stream);
-        if (st != FGEMM_OK) return st;
-    }
     GemmArgs g{};
     g.M = M;
     g.N = N;
     g.K = K;
     g.alpha = 1.0f;
-    g.a = codes;
-    g.a_scales = scales;
-    g.lda = ld;
     g.b = static_cast<const uint8_t *>(W_codes);
     g.b_scales = static_cast<const uint8_t *>(W_scales);
     g.ldb = ld_W_codes;
@@ -244,6 +233,19 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
     g.ldc = ldy;
     g.bias = bias;
     g.relu = apply_relu ? 1 : 0;
+    if (K == 0) return launch_gemm(type, g, stream);
+    if (linear_fused(M, K)) return launch_linear(type, X, ldx, g, stream);
+    uint8_t *const codes = static_cast<uint8_t *>(workspace);
+    uint8_t *const scales = codes + round256(codes_bytes(M, K));
+    const int ld = (int)(16 * blocks_of(K));
+    QuantParams q = quant_params(M, K, X, ldx, Direction{codes, ld, scales}, Direction{nullptr, 0, nullptr});
+    q.early = 1;
+    const fgemm_status st = launch_quantize(type, q, stream);
+    if (st != FGEMM_OK) return st;
+    g.a = codes;
+    g.a_scales = scales;
+    g.lda = ld;
+    g.dependent = 1;
     return launch_gemm(type, g, stream);
 }
 

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const QuantParams p, 
     const long long tiles_n = (p.N + TILE - 1) / TILE, tiles_m = (p.M + TILE - 1) / TILE;
     const long long row_blocks = blocks_of(p.N), col_blocks = blocks_of(p.M);
     constexpr int V = 16 / (int)sizeof(T);  // elements of a 16-byte load
+    if (p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     for (long long w = blockIdx.x; w < tiles_n * tiles_m; w += gridDim.x) {
         const long long tm = w / tiles_n, tn = w - tm * tiles_n;

@@ -31,14 +31,22 @@ constexpr int TC_BLOCKS = TC_DEPTH / BLOCK;
 constexpr int TC_THREADS = 320;  // producer, MMA, eight epilogue warps
 constexpr int EPI_WARPS = 8;
 
-template <int NT>
+// How a kernel divides the work: whole tiles by persistent CTAs; a tile's stages over a
+// cluster; and the latter with A unquantised (SPLIT_FUSED), quantised by the epilogue's warps
+// while the first stages of B are on their way.
+enum TcMode { WHOLE = 0, SPLIT = 1, SPLIT_FUSED = 2 };
+
+template <int NT, int MODE>
 struct TcTile {
+    static constexpr bool FUSED = MODE == SPLIT_FUSED;
     static constexpr int W_BYTES = TC_ROWS * 128;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int GROUPS = NT > 128 ? 2 : 1;  // 128-row groups of A's scales
-    static constexpr int SF_BYTES = 2 * ATOM_BYTES * (1 + GROUPS);
-    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
-    static constexpr int STAGES = NT > 128 ? 4 : NT > 64 ? 6 : 4;
+    static constexpr int X_SF_BYTES = 2 * ATOM_BYTES * GROUPS;
+    static constexpr int STAGE_BYTES = W_BYTES + 2 * ATOM_BYTES + (FUSED ? 0 : X_BYTES + X_SF_BYTES);
+    static constexpr int STAGES = NT > 64 && NT <= 128 ? 6 : 4;
+    // Fused: A's codes and scales of each of this CTA's stages follow the ring and the barriers.
+    static constexpr int FUSED_BYTES = FUSED ? X_BYTES + X_SF_BYTES : 0;
     // Tensor memory: two accumulators of NT columns, then two buffers of scales (4 columns an
     // atom).  At NT = 256 those are 560 columns of the 512: the accumulators overlap by 64,
     // and the epilogue reads the shared columns first.
@@ -50,9 +58,11 @@ struct TcTile {
     static_assert(TMEM_USED <= 512, "tensor memory");
     static constexpr int CHUNK = NT < 32 ? NT : 32;  // accumulator columns read at a time
     static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
-    // full[S], empty[S], acc_full[2], acc_free[2], drain, tensor-memory slot
-    static constexpr int SMEM_BYTES = 1024 + BAR_OFFSET + (2 * STAGES + 5) * 8 + 8;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    // full[S], empty[S], acc_full[2], acc_free[2], drain, x_ready, tensor-memory slot
+    static constexpr int BAR_BYTES = (2 * STAGES + 6) * 8 + 8;
+    static constexpr int X_OFFSET = BAR_OFFSET + 1024;
+    static constexpr int SMEM_BYTES = 1024 + (FUSED ? X_OFFSET : BAR_OFFSET + BAR_BYTES);  // + alignment
+    static_assert(SMEM_BYTES <= 227 * 1024 && BAR_BYTES <= 1024, "shared memory");
     static_assert(STAGES * STAGE_BYTES >= TC_ROWS * NT * 4, "a split tile's sums take the stages' place");
 };
 
@@ -60,6 +70,9 @@ struct TcArgs {
     CUtensorMap w, x;  // codes of B and A: (bytes along K, rows), boxes of 128 bytes
     const uint8_t *w_scales, *x_scales;
     void *c;
+    const void *x_plain;  // fused: A as it is, M x K
+    long long ldx;
+    int K, x_vec;         // x_vec: A allows 16-byte loads
     const float *bias;
     long long ldc, atoms;  // atoms: scale atoms of a 128-row group
     int M, N, blocks;      // blocks: ceil(K / 32)
@@ -69,6 +82,7 @@ struct TcArgs {
     int tiles_x, tiles_w;
     unsigned long long wait_limit_ns;
     int withhold;
+    int dependent;  // the kernel before this one in the stream writes A, and only A
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1)
@@ -217,13 +231,66 @@ __device__ __forceinline__ void store_chunk(const TcArgs &p, T *out, const uint3
     }
 }
 
-// SPLIT: the tile's stages are divided among the CTAs of a cluster, one tile a cluster;
-// otherwise CTAs walk over tiles.
-template <int NT, class T, bool SPLIT>
+// Quantise A's p.M (at most LINEAR_ROWS) rows, from code k0 on, into `stages` stages' tiles of
+// codes (NT rows, the 128-byte swizzle) and atoms of scales, by `threads` threads (t of them).
+template <int NT, class T>
+__device__ __forceinline__ void quantize_tokens(const TcArgs &p, uint8_t *codes, uint8_t *scales, int stages, long long k0,
+                                                int t, int threads)
+{
+    // Four lanes a block, eight elements each, of every row: all rows' loads are in flight
+    // before the first is used.  (stages * 32 items: whole warps, for the shuffles.)
+    for (int o = t; o < stages * TC_BLOCKS * 4; o += threads) {
+        const long long k = k0 + o * 8;
+        T e[LINEAR_ROWS][8];
+#pragma unroll
+        for (int row = 0; row < LINEAR_ROWS; ++row) {
+            if (row >= p.M) break;
+            const T *const src = static_cast<const T *>(p.x_plain) + row * p.ldx + k;
+            if (p.x_vec && k + 8 <= p.K) {
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                    reinterpret_cast<uint4 *>(e[row])[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[row][j] = k + j < p.K ? src[j] : from_float<T>(0.0f);
+            }
+        }
+        const int stage = o / (TC_BLOCKS * 4), b = (o >> 2) % TC_BLOCKS, part = o & 3;
+#pragma unroll
+        for (int row = 0; row < LINEAR_ROWS; ++row) {
+            if (row >= p.M) break;
+            float v[8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = to_float(e[row][j]);
+                top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            }
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const uint32_t s = scale_byte(top);
+            const float f = inverse_scale(s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= f;
+            const uint32_t c = s == 255u ? 0u : encode8(v);
+            *reinterpret_cast<uint32_t *>(codes + stage * NT * 128 + row * 128 + ((b ^ (row & 7)) << 4) + part * 4) = c;
+            if (part == 0) scales[(stage * 2 + b / 4) * ATOM_BYTES + row * 16 + b % 4] = (uint8_t)s;
+        }
+    }
+    // Rows beyond A: codes 0 (their columns of the accumulator are not stored, whatever their scales).
+    const int beyond = (NT - p.M) * 8;  // 16-byte pieces a stage
+    for (int i = t; i < stages * beyond; i += threads) {
+        const int stage = i / beyond, o = i - stage * beyond;
+        reinterpret_cast<uint4 *>(codes + stage * NT * 128 + p.M * 128)[o] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int NT, class T, int MODE>
 __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_constant__ TcArgs p, unsigned *err)
 {
-    using L = TcTile<NT>;
+    using L = TcTile<NT, MODE>;
     constexpr int S = L::STAGES;
+    constexpr bool FUSED = L::FUSED;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = tc::cvta_smem(smem), bars = sbase + L::BAR_OFFSET;
@@ -231,23 +298,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto acc_full_bar = [&](int a) { return bars + 8u * (2 * S + a); };
     auto acc_free_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 5));
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4), x_ready_bar = bars + 8u * (2 * S + 5);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 6));
 
     // (Through a shuffle, so that branches on the warp are known to be uniform.)
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const unsigned long long lim = p.wait_limit_ns;
     const int stages_k = (p.blocks + TC_BLOCKS - 1) / TC_BLOCKS;
     int ranks = 1, rank = 0;
-    if constexpr (SPLIT) {
+    if constexpr (MODE != WHOLE) {
         ranks = (int)cooperative_groups::this_cluster().num_blocks();
         rank = (int)cooperative_groups::this_cluster().block_rank();
     }
     // This CTA's stages of every tile of its own, and its tiles.
     const int k_first = (int)((long long)stages_k * rank / ranks), k_last = (int)((long long)stages_k * (rank + 1) / ranks);
     const long long tiles = (long long)p.tiles_x * p.tiles_w;
-    const long long first_tile = SPLIT ? blockIdx.x / ranks : blockIdx.x;
-    const long long tile_step = SPLIT ? tiles : gridDim.x;
+    const long long first_tile = MODE != WHOLE ? blockIdx.x / ranks : blockIdx.x;
+    const long long tile_step = MODE != WHOLE ? tiles : gridDim.x;
     // Tile t: rows of A from x0, rows of B from w0.  Eight tiles along A are swept along B
     // together, so that tiles in flight share operands in L2.
     auto tile_at = [&](long long t, int &x0, int &w0) {
@@ -267,6 +334,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             tc::mbar_init(acc_free_bar(a), EPI_WARPS);
         }
         tc::mbar_init(drain_bar, 1);
+        tc::mbar_init(x_ready_bar, EPI_WARPS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -283,30 +351,56 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
 
     if (warp == 0) {
         // ---- producer: the whole warp walks along, one lane issues ----
+        // A stage: B's codes and scales, then A's codes and scales.
+        auto load_w = [&](int k, int s, int w0, uint32_t x_bytes) {
+            const uint32_t at = sbase + s * L::STAGE_BYTES;
+            const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;  // the last may be alone
+            tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + sf_bytes + x_bytes);
+            tma_load_2d(at, &p.w, full_bar(s), k * 128, w0);
+            bulk_load(at + L::W_BYTES, p.w_scales + ((long long)(w0 / 128) * p.atoms + 2ll * k) * ATOM_BYTES, sf_bytes,
+                      full_bar(s));
+        };
+        auto x_bytes_of = [&](int k, int groups) -> uint32_t {
+            return FUSED ? 0u : (uint32_t)(L::X_BYTES + groups * (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES);
+        };
+        auto load_x = [&](int k, int s, int x0, int groups) {
+            const uint32_t xc = sbase + s * L::STAGE_BYTES + L::W_BYTES + 2 * ATOM_BYTES, xf = xc + L::X_BYTES;
+            const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;
+            const uint8_t *const xs = p.x_scales + ((long long)(x0 / 128) * p.atoms + 2ll * k) * ATOM_BYTES;
+            tma_load_2d(xc, &p.x, full_bar(s), k * 128, x0);
+            bulk_load(xf, xs, sf_bytes, full_bar(s));
+            if (groups == 2) bulk_load(xf + 2 * ATOM_BYTES, xs + p.atoms * ATOM_BYTES, sf_bytes, full_bar(s));
+        };
         int g = 0;
         bool ok = true;
         for (long long t = first_tile; ok && t < tiles; t += tile_step) {
-            int x0, w0;
+            int x0, w0, k = k_first;
             tile_at(t, x0, w0);
-            const uint8_t *const ws = p.w_scales + (long long)(w0 / 128) * p.atoms * ATOM_BYTES;
-            const uint8_t *const xs = p.x_scales + (long long)(x0 / 128) * p.atoms * ATOM_BYTES;
             // The second group of A's scales, where the tile reaches into it.
             const int groups = L::GROUPS == 2 && x0 + 128 < p.M ? 2 : 1;
-            for (int k = k_first; k < k_last; ++k, ++g) {
+            if (MODE == SPLIT && p.dependent) {
+                // Launched while the kernel that writes A may still run: B's part of the first
+                // stages, then the wait for that kernel, then A's.
+                int n = min(S, k_last - k_first);
+                if (p.withhold >= 0) n = min(n, p.withhold);
+                if (elect_one())
+                    for (int i = 0; i < n; ++i) load_w(k_first + i, i, w0, x_bytes_of(k_first + i, groups));
+                __syncwarp();
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                if (elect_one())
+                    for (int i = 0; i < n; ++i) load_x(k_first + i, i, x0, groups);
+                __syncwarp();
+                k += n;
+                g = n;
+            }
+            for (; k < k_last; ++k, ++g) {
                 const int s = g % S, round = g / S;
                 ok = (round == 0 || warp_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) &&
                      g != p.withhold;  // (testing: as if this copy never arrived)
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
-                    const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;  // the last may be alone
-                    tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + L::X_BYTES + (1 + groups) * sf_bytes);
-                    tma_load_2d(at, &p.w, full_bar(s), k * 128, w0);
-                    tma_load_2d(at + L::W_BYTES, &p.x, full_bar(s), k * 128, x0);
-                    bulk_load(sf, ws + (long long)k * 2 * ATOM_BYTES, sf_bytes, full_bar(s));
-                    bulk_load(sf + 2 * ATOM_BYTES, xs + 2ll * k * ATOM_BYTES, sf_bytes, full_bar(s));
-                    if (groups == 2)
-                        bulk_load(sf + 4 * ATOM_BYTES, xs + (p.atoms + 2ll * k) * ATOM_BYTES, sf_bytes, full_bar(s));
+                    load_w(k, s, w0, x_bytes_of(k, groups));
+                    if constexpr (!FUSED) load_x(k, s, x0, groups);
                 }
                 __syncwarp();
             }
@@ -332,6 +426,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 ok = false;
                 break;
             }
+            if (FUSED && !warp_wait(x_ready_bar, 0, err, tc::ERR_MMA_WAIT, lim)) {
+                ok = false;
+                break;
+            }
             tc::tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
             for (int k = k_first; k < k_last; ++k, ++g) {
@@ -340,10 +438,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 if (!ok) break;
                 tc::tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
+                    const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES;
+                    uint32_t xc = sf + 2 * ATOM_BYTES, xf = xc + L::X_BYTES;
+                    if constexpr (FUSED) {
+                        xc = sbase + L::X_OFFSET + (k - k_first) * L::X_BYTES;
+                        xf = sbase + L::X_OFFSET + (k_last - k_first) * L::X_BYTES + (k - k_first) * L::X_SF_BYTES;
+                    }
                     const uint32_t sfw = tmem + L::SF_BASE + (uint32_t)((g & 1) * L::SF_COLS), sfx = sfw + 8;
                     const int left = p.blocks - k * TC_BLOCKS;  // blocks from here on
-                    const uint64_t wd = tc::kmajor_sw128_desc(at), xd = tc::kmajor_sw128_desc(at + L::W_BYTES);
+                    const uint64_t wd = tc::kmajor_sw128_desc(at), xd = tc::kmajor_sw128_desc(xc);
                     // A tile of 64 rows may start in the middle of its group's scales.
                     const uint32_t sfx_at = sfx + (uint32_t)(NT < 128 ? (x0 % 128) / 32 : 0);
                     // Two atoms of scales, each for two MMAs of two blocks.  (The MMAs that still
@@ -354,7 +457,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                             copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
 #pragma unroll
                             for (int i = 0; i < L::GROUPS; ++i)
-                                copy_atom(sfx + 4 * (a * L::GROUPS + i), sf + (2 + 2 * i + a) * ATOM_BYTES);
+                                copy_atom(sfx + 4 * (a * L::GROUPS + i), xf + (2 * i + a) * ATOM_BYTES);
                         }
                     }
 #pragma unroll
@@ -377,6 +480,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     } else {
         // ---- epilogue: warps of two sets of four, a set takes every other chunk ----
         const int q = warp & 3, set = (warp - 2) >> 2;
+        if constexpr (FUSED) {
+            const int stages = k_last - k_first;
+            uint8_t *const codes = smem + L::X_OFFSET;
+            quantize_tokens<NT, T>(p, codes, codes + stages * L::X_BYTES, stages, (long long)k_first * TC_DEPTH,
+                                   (int)threadIdx.x - 64, 32 * EPI_WARPS);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads them
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(x_ready_bar);
+        }
         int j = 0;
         for (long long t = first_tile; t < tiles; t += tile_step, ++j) {
             int x0, w0;
@@ -386,7 +498,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             tc::tc_fence_after();
             const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::ACC_STEP);
             const int n = w0 + 32 * q + lane;
-            const float bias = !SPLIT && p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
             T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
             // (N even: a pair is inside or outside as a whole)
             const bool pairs = p.c_pairs && (p.N & 1) == 0;
@@ -402,7 +514,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(acc_free_bar(acc));
                 }
-                if constexpr (SPLIT) {
+                if (MODE != WHOLE && ranks > 1) {
                     // Column c of the tile: 128 sums, one for each row of B.
                     float *const part = reinterpret_cast<float *>(smem) + c0 * TC_ROWS + 32 * q + lane;
 #pragma unroll
@@ -420,27 +532,43 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
         __syncwarp();
     }
 
-    if constexpr (SPLIT) {
-        // Every CTA of the cluster adds up its share of the tile's columns over the ranks, in
-        // rank order.  (A rank that gave up leaves its memory as it was; the error word says
-        // that C is undefined.)
-        namespace cg = cooperative_groups;
-        cg::cluster_group cluster = cg::this_cluster();
+    if (MODE != WHOLE && ranks > 1) {
+        // Every CTA of the cluster adds up its share of the tile over the ranks, in rank order:
+        // four rows of B (columns of C) of one row of A at a time.  (A rank that gave up leaves its
+        // memory as it was; the error word says that C is undefined.)
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
         cluster.sync();
         int x0, w0;
         tile_at(first_tile, x0, w0);
-        const int from = NT * rank / ranks, to = NT * (rank + 1) / ranks;
-        for (int i = threadIdx.x; i < (to - from) * TC_ROWS; i += TC_THREADS) {
-            const int c = from + i / TC_ROWS, row = i % TC_ROWS, n = w0 + row;
-            if (x0 + c >= p.M || n >= p.N) continue;
-            float sum = 0.0f;
-            for (int r = 0; r < ranks; ++r)
-                sum += *cluster.map_shared_rank(reinterpret_cast<float *>(smem) + c * TC_ROWS + row, r);
+        const int columns = min(NT, p.M - x0), from = columns * rank / ranks, to = columns * (rank + 1) / ranks;
+        for (int i = threadIdx.x; i < (to - from) * (TC_ROWS / 4); i += TC_THREADS) {
+            const int c = from + i / (TC_ROWS / 4), row = i % (TC_ROWS / 4) * 4, n = w0 + row;
+            if (n >= p.N) continue;
+            float4 part[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < ranks)
+                    part[r] = *reinterpret_cast<const float4 *>(
+                        cluster.map_shared_rank(reinterpret_cast<float *>(smem) + c * TC_ROWS + row, r));
+            float sum[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < ranks) {
+                    sum[0] += part[r].x;
+                    sum[1] += part[r].y;
+                    sum[2] += part[r].z;
+                    sum[3] += part[r].w;
+                }
             T *const out = static_cast<T *>(p.c) + (long long)(x0 + c) * p.ldc + n;
-            const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
-            float o = p.beta != 0.0f ? finish<T, true, false>(p, out, sum, bias) : finish<T, false, false>(p, out, sum, bias);
-            if (p.relu) o = fmaxf(o, 0.0f);
-            *out = from_float<T>(o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (n + e >= p.N) break;
+                const float bias = p.bias ? __ldg(p.bias + n + e) : 0.0f;
+                float o = p.beta != 0.0f ? finish<T, true, false>(p, out + e, sum[e], bias)
+                                         : finish<T, false, false>(p, out + e, sum[e], bias);
+                if (p.relu) o = fmaxf(o, 0.0f);
+                out[e] = from_float<T>(o);
+            }
         }
         cluster.sync();
     }

@@ -1,10 +1,12 @@
-// mxfp4_tc_f16.cu -- the MXFP4 product's instances with C of type f16.
+// mxfp4_tc_f16.cu -- the MXFP4 product's instances with C (and unquantised A) of type f16.
 #include "mxfp4_tc_launch.cuh"
 
 namespace fgemm {
 namespace mx {
 
 template fgemm_status launch_tc_type<__half>(const GemmArgs &g, int nt, int ranks, cudaStream_t stream);
+template fgemm_status launch_fused_type<__half>(const GemmArgs &g, const void *x, long long ldx, int nt, int ranks,
+                                            cudaStream_t stream);
 
 }  // namespace mx
 }  // namespace fgemm

@@ -53,6 +53,8 @@ static void fill_args(TcArgs &p, const GemmArgs &g, int tile_x, int tile_w)
     p.M = g.M;
     p.N = g.N;
     p.blocks = (int)blocks;
+    p.K = g.K;
+    p.dependent = g.dependent;
     p.alpha = g.alpha;
     p.beta = g.beta;
     p.relu = g.relu;
@@ -103,38 +105,53 @@ static fgemm_status launch_pairs(const GemmArgs &g, cudaStream_t stream)
     return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
 }
 
-template <int NT, class T, bool SPLIT>
-static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t stream)
+// One CTA a tile (WHOLE), or a cluster of `ranks`.  x, ldx: the unquantised A of SPLIT_FUSED.
+template <int NT, class T, int MODE>
+static fgemm_status launch_instance(const GemmArgs &g, const void *x, long long ldx, int ranks, cudaStream_t stream)
 {
-    using L = TcTile<NT>;
-    constexpr auto kernel = &mxfp4_tc_kernel<NT, T, SPLIT>;
+    using L = TcTile<NT, MODE>;
+    constexpr auto kernel = &mxfp4_tc_kernel<NT, T, MODE>;
     unsigned *err = nullptr;
     int sms = 0;
-    if (!prepare<decltype(kernel), kernel>(L::SMEM_BYTES, &err, &sms)) {
-        (void)cudaGetLastError();
-        return FGEMM_ERR_LAUNCH;
-    }
     TcArgs p;
     std::memset(&p, 0, sizeof(p));
     fill_args(p, g, NT, TC_ROWS);
-    if (!make_codes_map(&p.w, g.b, g.N, p.blocks, g.ldb, TC_ROWS) || !make_codes_map(&p.x, g.a, g.M, p.blocks, g.lda, NT))
+    const int stages = (p.blocks + TC_BLOCKS - 1) / TC_BLOCKS;
+    // A rank without stages would leave its sums unwritten.
+    if (MODE != WHOLE && (ranks < 1 || ranks > 8 || ranks > stages)) return FGEMM_ERR_NOT_SUPPORTED;
+    const int smem = L::SMEM_BYTES + (MODE == SPLIT_FUSED ? (stages + ranks - 1) / ranks * L::FUSED_BYTES : 0);
+    constexpr int most = MODE == SPLIT_FUSED ? L::SMEM_BYTES + FUSED_SMEM : L::SMEM_BYTES;
+    if (smem > most) return FGEMM_ERR_NOT_SUPPORTED;
+    if (!prepare<decltype(kernel), kernel>(most, &err, &sms)) {
+        (void)cudaGetLastError();
+        return FGEMM_ERR_LAUNCH;
+    }
+    if (!make_codes_map(&p.w, g.b, g.N, p.blocks, g.ldb, TC_ROWS)) return FGEMM_ERR_NOT_SUPPORTED;
+    if (MODE == SPLIT_FUSED) {
+        p.x_plain = x;
+        p.ldx = ldx;
+        p.x_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (long long)sizeof(T) % 16 == 0;
+    } else if (!make_codes_map(&p.x, g.a, g.M, p.blocks, g.lda, NT)) {
         return FGEMM_ERR_NOT_SUPPORTED;
+    }
     const long long tiles = (long long)p.tiles_x * p.tiles_w;
-    if (!SPLIT) {
-        kernel<<<(unsigned)(tiles < sms ? tiles : sms), TC_THREADS, L::SMEM_BYTES, stream>>>(p, err);
+    if (MODE == WHOLE) {
+        kernel<<<(unsigned)(tiles < sms ? tiles : sms), TC_THREADS, smem, stream>>>(p, err);
     } else {
         if (tiles * ranks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(tiles * ranks));
         cfg.blockDim = dim3(TC_THREADS);
-        cfg.dynamicSmemBytes = L::SMEM_BYTES;
+        cfg.dynamicSmemBytes = (size_t)smem;
         cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)ranks;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = p.dependent ? 2 : 1;
         if (cudaLaunchKernelEx(&cfg, kernel, p, err) != cudaSuccess) {
             (void)cudaGetLastError();
             return FGEMM_ERR_LAUNCH;
@@ -144,20 +161,32 @@ static fgemm_status launch_instance(const GemmArgs &g, int ranks, cudaStream_t s
 }
 
 // The product with tiles of `nt` rows of A, each over a cluster of `ranks` CTAs (0: whole
-// tiles, persistent CTAs).
+// tiles; 384 and 512: by pairs, of 192 and 256).
 template <class T>
 fgemm_status launch_tc_type(const GemmArgs &g, int nt, int ranks, cudaStream_t stream)
 {
-    if (ranks == 0 && nt == 512) return launch_pairs<256, T>(g, stream);
-    if (ranks == 0 && nt == 384) return launch_pairs<192, T>(g, stream);
-    if (ranks == 0)
-        return nt == 256 ? launch_instance<256, T, false>(g, 0, stream) : launch_instance<128, T, false>(g, 0, stream);
-    switch (nt) {
-    case 16: return launch_instance<16, T, true>(g, ranks, stream);
-    case 32: return launch_instance<32, T, true>(g, ranks, stream);
-    case 64: return launch_instance<64, T, true>(g, ranks, stream);
-    default: return launch_instance<128, T, true>(g, ranks, stream);
+    if (ranks == 0) {
+        switch (nt) {
+        case 512: return launch_pairs<256, T>(g, stream);
+        case 384: return launch_pairs<192, T>(g, stream);
+        case 256: return launch_instance<256, T, WHOLE>(g, nullptr, 0, 0, stream);
+        default: return launch_instance<128, T, WHOLE>(g, nullptr, 0, 0, stream);
+        }
     }
+    switch (nt) {
+    case 16: return launch_instance<16, T, SPLIT>(g, nullptr, 0, ranks, stream);
+    case 32: return launch_instance<32, T, SPLIT>(g, nullptr, 0, ranks, stream);
+    case 64: return launch_instance<64, T, SPLIT>(g, nullptr, 0, ranks, stream);
+    default: return launch_instance<128, T, SPLIT>(g, nullptr, 0, ranks, stream);
+    }
+}
+
+// The same with A as x (M x K, unquantised, element type T, at most LINEAR_ROWS rows).
+template <class T>
+fgemm_status launch_fused_type(const GemmArgs &g, const void *x, long long ldx, int nt, int ranks, cudaStream_t stream)
+{
+    (void)nt;  // 16
+    return launch_instance<16, T, SPLIT_FUSED>(g, x, ldx, ranks, stream);
 }
 
 }  // namespace mx
