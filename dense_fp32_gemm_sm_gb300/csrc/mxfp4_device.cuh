@@ -77,5 +77,19 @@ __device__ __forceinline__ void decode8(uint32_t codes, float (&x)[8])
     }
 }
 
+// The two codes of a byte to their values.
+__device__ __forceinline__ float2 decode2(uint32_t byte)
+{
+    uint32_t h;
+    asm("{\n"
+        ".reg .b8 b0, b1, b2, b3;\n"
+        "mov.b32 {b0, b1, b2, b3}, %1;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "}\n"
+        : "=r"(h)
+        : "r"(byte));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
 }  // namespace mx
 }  // namespace fgemm

@@ -19,11 +19,11 @@ constexpr int TILE = 128;  // a tile is 128 x 128: one scale atom in each direct
 
 // The kernel's shape by element size.  A thread takes one block of a row and one of a column
 // (FP32), or two blocks of rows and the same block of two neighbouring columns (16 bits).
-template <int ES>
+template <int ES, bool GATED>
 struct QuantShape {
     static constexpr int THREADS = ES == 4 ? 512 : 256;
-    static constexpr int CTAS_PER_SM = ES == 4 ? 1 : 2;
-    static constexpr int STAGES = 3;  // 192 KB an SM: two tiles (64 KB FP32) on their way behind one at work
+    static constexpr int CTAS_PER_SM = ES == 4 ? 1 : GATED ? 2 : 3;  // (a gate's pieces wait in 32 registers)
+    static constexpr int STAGES = ES == 4 || GATED ? 3 : 2;          // 192 KB an SM in all
     static constexpr int TILE_BYTES = TILE * TILE * ES;
     static constexpr int SMEM_BYTES = STAGES * TILE_BYTES;
     static constexpr int CHUNKS_PER_ROW = TILE * ES / 16;
@@ -56,11 +56,11 @@ __device__ __forceinline__ void copy_async_4(uint32_t dst, const void *src, int 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// The larger magnitude; a NaN stays.
-__device__ __forceinline__ float max_magnitude(float a, float b)
+// The largest magnitude; a NaN stays.
+__device__ __forceinline__ float max_magnitude(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ __nv_bfloat162 max_magnitude(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2_nan(a, __habs2(b)); }
@@ -75,9 +75,34 @@ template <class P> __device__ __forceinline__ P pair_of_zeros()
 template <class T> struct PairOf;
 template <> struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
 template <> struct PairOf<__half> { using type = __half2; };
+// Four bytes of a row: an FP32 element, or two of 16 bits.
+template <class T> struct WordOf { using type = typename PairOf<T>::type; };
+template <> struct WordOf<float> { using type = float; };
+template <class W> __device__ __forceinline__ W zero_word() { return pair_of_zeros<W>(); }
 
 __device__ __forceinline__ float2 unpack(__nv_bfloat162 x) { return __bfloat1622float2(x); }
 __device__ __forceinline__ float2 unpack(__half2 x) { return __half22float2(x); }
+
+// Two values times f.x and f.y, both powers of two: exact, in bf16 itself (it has f's range).
+__device__ __forceinline__ float2 scaled(__nv_bfloat162 x, __nv_bfloat162 f) { return __bfloat1622float2(__hmul2(x, f)); }
+__device__ __forceinline__ float2 scaled(__half2 x, float2 f)
+{
+    const float2 v = __half22float2(x);
+    return make_float2(v.x * f.x, v.y * f.y);
+}
+template <class P> struct FactorOf;
+template <> struct FactorOf<__nv_bfloat162> {
+    using type = __nv_bfloat162;
+    static __device__ __forceinline__ type make(float x, float y) { return __floats2bfloat162_rn(x, y); }
+};
+template <> struct FactorOf<__half2> {
+    using type = float2;
+    static __device__ __forceinline__ type make(float x, float y) { return make_float2(x, y); }
+};
+
+// x where y > 0, else 0, for a pair.
+__device__ __forceinline__ uint32_t gated(__nv_bfloat162 y, uint32_t x) { return __hgt2_mask(y, pair_of_zeros<__nv_bfloat162>()) & x; }
+__device__ __forceinline__ uint32_t gated(__half2 y, uint32_t x) { return __hgt2_mask(y, pair_of_zeros<__half2>()) & x; }
 
 // Words w[i ^ x] to their places.
 __device__ __forceinline__ uint4 exchange(const uint32_t (&w)[4], int x)
@@ -87,13 +112,13 @@ __device__ __forceinline__ uint4 exchange(const uint32_t (&w)[4], int x)
     return two ? make_uint4(c, d, a, b) : make_uint4(a, b, c, d);
 }
 
-// Eight values times f to eight codes; 0 in a NaN's block.
-__device__ __forceinline__ uint32_t encode_scaled(const float (&x)[8], float f, uint32_t s)
+// Eight values times f to eight codes.
+__device__ __forceinline__ uint32_t encode_scaled(const float (&x)[8], float f)
 {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = x[i] * f;
-    return s == 255u ? 0u : encode8(v);
+    return encode8(v);
 }
 
 // The block `blk` of tile row `row`: its codes, and its scale byte.  g: which of the lanes that
@@ -109,8 +134,8 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(tile + piece_at(row, blk * 8 + (j ^ rot)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max_magnitude(top, x[j][i]);
+            top = max_magnitude(top, x[j][0], x[j][1]);
+            top = max_magnitude(top, x[j][2], x[j][3]);
         }
         const uint32_t s = scale_byte(__float_as_uint(top));
         const float f = inverse_scale(s);
@@ -118,9 +143,9 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
         for (int j = 0; j < 4; ++j) {
             const float v[8] = {x[2 * j][0],     x[2 * j][1],     x[2 * j][2],     x[2 * j][3],
                                 x[2 * j + 1][0], x[2 * j + 1][1], x[2 * j + 1][2], x[2 * j + 1][3]};
-            w[j] = __byte_perm(encode_scaled(v, f, s), 0, rot & 1 ? 0x1032 : 0x3210);
+            w[j] = __byte_perm(encode_scaled(v, f), 0, rot & 1 ? 0x1032 : 0x3210);
         }
-        codes = exchange(w, rot >> 1);
+        codes = s == 255u ? make_uint4(0, 0, 0, 0) : exchange(w, rot >> 1);
         return s;
     } else {
         using P = typename PairOf<T>::type;
@@ -134,48 +159,32 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
             for (int i = 0; i < 4; ++i) top2 = max_magnitude(top2, x[j][i]);
         }
         const float2 t2 = unpack(top2);
-        const uint32_t s = scale_byte(__float_as_uint(max_magnitude(t2.x, t2.y)));
-        const float f = inverse_scale(s);
+        const uint32_t s = scale_byte(__float_as_uint(max_magnitude(t2.x, t2.y, 0.0f)));
+        const auto f = FactorOf<P>::make(inverse_scale(s), inverse_scale(s));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 u = unpack(x[j][i]);
+                const float2 u = scaled(x[j][i], f);
                 v[2 * i] = u.x;
                 v[2 * i + 1] = u.y;
             }
-            w[j] = encode_scaled(v, f, s);
+            w[j] = encode8(v);
         }
-        codes = exchange(w, rot);
+        codes = s == 255u ? make_uint4(0, 0, 0, 0) : exchange(w, rot);
         return s;
     }
 }
 
-// Rows 32 * blk + (i ^ 2 * blk) of a column, i = 0 .. 31, as FP32: its codes, scale byte and sum.
-__device__ __forceinline__ uint32_t encode_column_block(const float (&x)[32], float top, int blk, uint4 &codes)
-{
-    const uint32_t s = scale_byte(__float_as_uint(top));
-    const float f = inverse_scale(s);
-    const uint32_t sel = blk == 0 ? 0x3210u : blk == 1 ? 0x2301u : blk == 2 ? 0x1032u : 0x0123u;  // byte p of p ^ blk
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float v[8] = {x[8 * j],     x[8 * j + 1], x[8 * j + 2], x[8 * j + 3],
-                            x[8 * j + 4], x[8 * j + 5], x[8 * j + 6], x[8 * j + 7]};
-        w[j] = __byte_perm(encode_scaled(v, f, s), 0, sel);
-    }
-    codes = make_uint4(w[0], w[1], w[2], w[3]);
-    return s;
-}
-
 // Bound by memory: the matrix once in, 17/32 bytes an element and direction out.  Persistent
 // CTAs; while a tile is worked on, the next two are copied.
-template <class T, bool GATED>
-__global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<sizeof(T)>::CTAS_PER_SM)
-    quantize_kernel(const QuantParams p, int mode, int stages)
+// ELEMENTS: mode is COPY_ELEMENTS (an instance of its own, for the registers that its loads take).
+template <class T, bool GATED, bool ELEMENTS>
+__global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantShape<sizeof(T), GATED>::CTAS_PER_SM)
+    quantize_kernel(const QuantParams p, int mode)
 {
-    using L = QuantShape<sizeof(T)>;
+    using L = QuantShape<sizeof(T), GATED>;
     constexpr int ES = (int)sizeof(T), V = 16 / ES;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -183,15 +192,24 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
     const long long row_blocks = blocks_of(p.N), col_blocks = blocks_of(p.M);
     const T *const X = static_cast<const T *>(p.x);
     const T *const Y = static_cast<const T *>(p.gate);
+    // (Whatever comes next and was told that it may start waits before it reads.)
     if (p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // Start the copies of tile w into a stage (asynchronous modes); beyond the matrix: zeros.
     auto start = [&](long long w, int stage) {
-        if (w < tiles && mode != COPY_ELEMENTS) {
+        if (w < tiles) {
             const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem) + stage * L::TILE_BYTES;
-            if (mode == COPY_16) {
+            if (mode == COPY_16 && r0 + TILE <= p.M && c0 + TILE <= p.N) {
+                // An interior tile: pieces THREADS apart are whole rows apart, a multiple of 8.
+                const int row = t / L::CHUNKS_PER_ROW, c = t % L::CHUNKS_PER_ROW;
+                constexpr int STEP = L::THREADS / L::CHUNKS_PER_ROW;
+                const uint32_t at = dst + piece_at(row, c);
+                const T *src = X + (r0 + row) * p.ldx + c0 + c * V;
 #pragma unroll
+                for (int j = 0; j < L::CHUNKS; ++j, src += STEP * p.ldx) copy_async_16(at + j * STEP * 128, src, 16);
+            } else if (mode == COPY_16) {
+#pragma unroll 1
                 for (int j = 0; j < L::CHUNKS; ++j) {
                     const int q = t + j * L::THREADS, row = q / L::CHUNKS_PER_ROW, c = q % L::CHUNKS_PER_ROW;
                     const long long left = p.N - c0 - c * V;
@@ -211,10 +229,17 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // The gate of this thread's own 16-byte pieces of tile w.
-    uint4 gate[GATED ? L::CHUNKS : 1];
+    uint4 gate[GATED && !ELEMENTS ? L::CHUNKS : 1];
     auto fetch_gate = [&](long long w) {
-        if (!GATED || w >= tiles || mode != COPY_16) return;
+        if (!GATED || ELEMENTS || w >= tiles || mode != COPY_16) return;
         const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
+        if (r0 + TILE <= p.M && c0 + TILE <= p.N) {
+            const T *src = Y + (r0 + t / L::CHUNKS_PER_ROW) * p.ldgate + c0 + t % L::CHUNKS_PER_ROW * V;
+#pragma unroll
+            for (int j = 0; j < L::CHUNKS; ++j, src += L::THREADS / L::CHUNKS_PER_ROW * p.ldgate)
+                gate[j] = __ldcs(reinterpret_cast<const uint4 *>(src));
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < L::CHUNKS; ++j) {
             const int q = t + j * L::THREADS, row = q / L::CHUNKS_PER_ROW, c = q % L::CHUNKS_PER_ROW;
@@ -230,16 +255,18 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
         }
     };
 
-    for (int s = 0; s + 1 < stages; ++s) start(blockIdx.x + (long long)s * gridDim.x, s);
-    fetch_gate(blockIdx.x);
+    if constexpr (!ELEMENTS) {
+        for (int s = 0; s + 1 < L::STAGES; ++s) start(blockIdx.x + (long long)s * gridDim.x, s);
+        fetch_gate(blockIdx.x);
+    }
     int stage = 0;
     for (long long w = blockIdx.x; w < tiles; w += gridDim.x) {
         const long long tm = w / tiles_n, tn = w - tm * tiles_n;
         const long long r0 = tm * TILE, c0 = tn * TILE;
         uint8_t *const tile = smem + stage * L::TILE_BYTES;
-        if (mode == COPY_ELEMENTS) {
+        if constexpr (ELEMENTS) {
             __syncthreads();  // the previous tile has been read (one stage)
-            constexpr int BATCH = 16;
+            constexpr int BATCH = 32;  // loads in flight
             for (int j = 0; j < TILE * TILE / L::THREADS; j += BATCH) {
                 T e[BATCH];
 #pragma unroll
@@ -256,24 +283,28 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
             }
         } else {
             // This tile's copies are this thread's oldest group; at most stages - 2 follow it.
-            if (stages == 3)
+            if (L::STAGES == 3)
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             else
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         if constexpr (GATED) {
             // Each thread closes the gates of the pieces it has copied itself.
-            if (mode == COPY_16) {
+            if (!ELEMENTS && mode == COPY_16) {
 #pragma unroll
                 for (int j = 0; j < L::CHUNKS; ++j) {
                     const int q = t + j * L::THREADS, row = q / L::CHUNKS_PER_ROW, c = q % L::CHUNKS_PER_ROW;
                     uint4 *const at = reinterpret_cast<uint4 *>(tile + piece_at(row, c));
-                    T x[V], y[V];
+                    uint32_t x[4];
+                    const uint32_t y[4] = {gate[j].x, gate[j].y, gate[j].z, gate[j].w};
                     *reinterpret_cast<uint4 *>(x) = *at;
-                    *reinterpret_cast<uint4 *>(y) = gate[j];
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (!(to_float(y[i]) > 0.0f)) x[i] = from_float<T>(0.0f);
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (ES == 4)
+                            x[i] = __uint_as_float(y[i]) > 0.0f ? x[i] : 0u;
+                        else
+                            x[i] = gated(reinterpret_cast<const typename PairOf<T>::type &>(y[i]), x[i]);
+                    }
                     *at = *reinterpret_cast<const uint4 *>(x);
                 }
             } else {
@@ -295,10 +326,9 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
             }
         }
         __syncthreads();
-        if (mode != COPY_ELEMENTS) {
+        if constexpr (!ELEMENTS) {
             // Into the stage that the previous tile has left (the barrier above: all have read it).
-            if (stages == 3)
-                start(w + 2ll * gridDim.x, stage == 0 ? 2 : stage - 1);
+            start(w + (L::STAGES - 1ll) * gridDim.x, stage == 0 ? L::STAGES - 1 : stage - 1);
             fetch_gate(w + gridDim.x);
         }
 
@@ -321,96 +351,140 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, QuantShape<siz
             const int col = (8 * warp + (lane & 7)) * COLS;
             const uint8_t *const src = tile + (col * ES / 128) * (TILE * 128);
             const int piece = (col * ES / 16) & 7, within = (col * ES) % 16;
-            float x[COLS][32], top[COLS], sum[COLS];
-            if constexpr (ES == 4) {
-                top[0] = 0.0f;
+            using Word = typename WordOf<T>::type;
+            Word x[32];  // rows 32 blk + (i ^ 2 blk): byte p of a word of codes is then byte p ^ blk of its place
+            float top[COLS] = {}, sum[COLS];
+            Word top2 = zero_word<Word>();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int row = 32 * blk + (i ^ (2 * blk));
-                    x[0][i] = *reinterpret_cast<const float *>(src + row * 128 + (((piece ^ row) & 7) << 4) + within);
-                    top[0] = max_magnitude(top[0], x[0][i]);
+            for (int i = 0; i < 32; ++i) {
+                const int row = 32 * blk + (i ^ (2 * blk));
+                x[i] = *reinterpret_cast<const Word *>(src + row * 128 + (((piece ^ row) & 7) << 4) + within);
+                if constexpr (ES == 4) {
+                    if (i & 1) top[0] = max_magnitude(top[0], x[i - 1], x[i]);
+                } else {
+                    top2 = max_magnitude(top2, x[i]);
                 }
-            } else {
-                using P = typename PairOf<T>::type;
-                P top2 = pair_of_zeros<P>();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int row = 32 * blk + (i ^ (2 * blk));
-                    const P u = *reinterpret_cast<const P *>(src + row * 128 + (((piece ^ row) & 7) << 4) + within);
-                    top2 = max_magnitude(top2, u);
-                    const float2 f = unpack(u);
-                    x[0][i] = f.x;
-                    x[COLS - 1][i] = f.y;
-                }
+            }
+            if constexpr (ES == 2) {
                 const float2 f = unpack(top2);
                 top[0] = f.x;
                 top[COLS - 1] = f.y;
             }
+            if (p.bias_grad) {
+                float part[4][COLS] = {};
 #pragma unroll
-            for (int e = 0; e < COLS; ++e) {
-                if (p.bias_grad) {
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < 32; ++i) {
+                    if constexpr (ES == 4) {
+                        part[i & 3][0] += x[i];
+                    } else {
+                        const float2 f = unpack(x[i]);
+                        part[i & 3][0] += f.x;
+                        part[i & 3][COLS - 1] += f.y;
+                    }
+                }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) part[i & 3] += x[e][i];
-                    sum[e] = (part[0] + part[1]) + (part[2] + part[3]);
+                for (int e = 0; e < COLS; ++e) {
+                    sum[e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 8);
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 16);
                     if (blk == 0 && c0 + col + e < p.N)
                         (tiles_m == 1 ? p.bias_grad : p.partial + tm * p.N)[c0 + col + e] = sum[e];
                 }
-                if (p.col_codes) {
-                    uint4 codes;
-                    const uint32_t s = encode_column_block(x[e], top[e], blk, codes);
+            }
+            if (p.col_codes) {
+                const uint32_t sel = blk == 0 ? 0x3210u : blk == 1 ? 0x2301u : blk == 2 ? 0x1032u : 0x0123u;
+                uint32_t s[COLS], codes[COLS][4];
+#pragma unroll
+                for (int e = 0; e < COLS; ++e) s[e] = scale_byte(__float_as_uint(top[e]) & 0x7FFFFFFFu);
+                if constexpr (ES == 4) {
+                    const float f = inverse_scale(s[0]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        codes[0][j] = encode_scaled(reinterpret_cast<const float (&)[8]>(x[8 * j]), f);
+                } else {
+                    const auto f = FactorOf<Word>::make(inverse_scale(s[0]), inverse_scale(s[COLS - 1]));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float v[2][8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 u = scaled(x[8 * j + i], f);
+                            v[0][i] = u.x;
+                            v[1][i] = u.y;
+                        }
+                        codes[0][j] = encode8(v[0]);
+                        codes[COLS - 1][j] = encode8(v[1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < COLS; ++e) {
                     const int c = col + e;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = s[e] == 255u ? 0u : __byte_perm(codes[e][j], 0, sel);
                     if (c0 + c < p.N && r0 / 32 + blk < col_blocks)
-                        *reinterpret_cast<uint4 *>(p.col_codes + (c0 + c) * p.ld_col + (r0 / 32 + blk) * 16) = codes;
-                    p.col_scales[(tn * atoms_of(col_blocks) + tm) * ATOM_BYTES + (c % 32) * 16 + (c / 32) * 4 + blk] = (uint8_t)s;
+                        *reinterpret_cast<uint4 *>(p.col_codes + (c0 + c) * p.ld_col + (r0 / 32 + blk) * 16) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    p.col_scales[(tn * atoms_of(col_blocks) + tm) * ATOM_BYTES + (c % 32) * 16 + (c / 32) * 4 + blk] = (uint8_t)s[e];
                 }
             }
         }
-        if (mode != COPY_ELEMENTS) stage = stage + 1 == stages ? 0 : stage + 1;
+        if constexpr (!ELEMENTS) stage = stage + 1 == L::STAGES ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// bias_grad[j] = the sum of the partial sums of column j, in the order of the rows.
+// bias_grad[j] = the sum of column j's partial sums, always in the same order: eight warps take
+// every eighth part of 32 columns.
 __global__ void __launch_bounds__(256) bias_grad_kernel(const float *partial, int parts, int N, float *bias_grad)
 {
-    for (long long j = blockIdx.x * 256ll + threadIdx.x; j < N; j += gridDim.x * 256ll) {
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partial sums are being formed
+    for (long long j0 = blockIdx.x * 32ll; j0 < N; j0 += gridDim.x * 32ll) {
+        const long long j = j0 + lane;
         float s = 0.0f;
-        for (int i = 0; i < parts; ++i) s += partial[(long long)i * N + j];
-        bias_grad[j] = s;
+        if (j < N) {
+#pragma unroll 8
+            for (int i = warp; i < parts; i += 8) s += partial[(long long)i * N + j];
+        }
+        sums[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && j < N) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i) s += sums[i][lane];
+            bias_grad[j] = s;
+        }
+        __syncthreads();
     }
 }
 
 // Values from codes, 16 bytes of them a lane: a warp writes 512 consecutive bytes of a row.
 // Bound by the writes.  VEC: X allows 16-byte stores; otherwise a lane's elements are 32 apart,
 // so that each store of a warp still falls on consecutive addresses.
-template <class T, bool VEC>
+template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
 {
     constexpr int V = 16 / (int)sizeof(T), SPAN = 32 * V;  // elements a lane, a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long spans = (p.N + SPAN - 1) / SPAN, groups = ((long long)p.M + 31) / 32, atoms = atoms_of(blocks_of(p.N));
-    // A CTA: 32 rows of a span; a warp: rows warp, warp + 8, ...
-    for (long long w = blockIdx.x; w < spans * groups; w += gridDim.x) {
-        const long long g = w / spans, k0 = (w - g * spans) * SPAN;
-        const long long r0 = g * 32 + warp;
+    const long long atoms = atoms_of(blocks_of(p.N)), k0 = (long long)blockIdx.x * SPAN;
+    // A CTA: 8 * ROWS rows of a span; a warp: rows warp, warp + 8, ...
+    for (long long r0 = (long long)blockIdx.y * (8 * ROWS) + warp; r0 < p.M; r0 += (long long)gridDim.y * (8 * ROWS)) {
         if constexpr (VEC) {
             const long long k = k0 + lane * V;
-            uint32_t codes[4];
-            uint32_t s[4];
+            const uint8_t *const scales = p.scales + k0 / 128 * ATOM_BYTES + (V == 8 ? lane / 16 * ATOM_BYTES + lane / 4 % 4 : lane / 8);
+            uint32_t codes[ROWS], s[ROWS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const long long r = r0 + 8 * i;
                 if (r < p.M && k < p.N) {
                     const uint8_t *const src = p.codes + r * p.ld + k / 2;
                     codes[i] = V == 8 ? *reinterpret_cast<const uint32_t *>(src) : *reinterpret_cast<const uint16_t *>(src);
-                    s[i] = p.scales[scale_offset(r, k / 32, atoms)];
+                    s[i] = scales[scale_offset(r, 0, atoms)];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const long long r = r0 + 8 * i;
                 if (r >= p.M || k >= p.N) continue;
                 float x[8];
@@ -429,28 +503,31 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
                 }
             }
         } else {
+            const uint8_t *const scales = p.scales + k0 / 128 * ATOM_BYTES;
+            uint32_t c[ROWS][V], s[ROWS][V];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const long long r = r0 + 8 * i;
                 if (r >= p.M) break;
-                const uint8_t *const src = p.codes + r * p.ld;
-                uint32_t c[V], s[V];
+                const uint8_t *const src = p.codes + r * p.ld + (k0 + lane) / 2, *const sr = scales + scale_offset(r, 0, atoms);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const long long k = k0 + 32 * e + lane;
-                    if (k < p.N) {
-                        c[e] = src[k / 2];
-                        s[e] = p.scales[scale_offset(r, k / 32, atoms)];
+                for (int e = 0; e < V; ++e)
+                    if (k0 + 32 * e + lane < p.N) {
+                        c[i][e] = src[16 * e];
+                        s[i][e] = sr[e / 4 * ATOM_BYTES + e % 4];
                     }
-                }
+            }
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const long long k = k0 + 32 * e + lane;
-                    if (k >= p.N) continue;
-                    float x[8];
-                    decode8(c[e] >> (4 * (lane & 1)), x);  // (k is odd where the lane is)
-                    static_cast<T *>(p.x)[r * p.ldx + k] = from_float<T>(x[0] * scale_value(s[e]));
-                }
+            for (int i = 0; i < ROWS; ++i) {
+                const long long r = r0 + 8 * i;
+                if (r >= p.M) break;
+                T *const dst = static_cast<T *>(p.x) + r * p.ldx + k0 + lane;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (k0 + 32 * e + lane < p.N) {
+                        const float2 x = decode2(c[i][e]);  // (the element is odd where the lane is)
+                        dst[32 * e] = from_float<T>((lane & 1 ? x.y : x.x) * scale_value(s[i][e]));
+                    }
             }
         }
     }
@@ -461,38 +538,69 @@ bool aligned_to(const void *ptr, long long ld_bytes, int to)
     return reinterpret_cast<uintptr_t>(ptr) % to == 0 && ld_bytes % to == 0;
 }
 
-template <class T, bool GATED>
-fgemm_status run_quantize(const QuantParams &p, cudaStream_t stream)
+template <class T, bool GATED, bool ELEMENTS>
+fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int sms, cudaStream_t stream)
 {
-    using L = QuantShape<sizeof(T)>;
+    using L = QuantShape<sizeof(T), GATED>;
     static std::atomic<unsigned long long> ready_ctx[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || device_sm_count(&sms) != 0) {
+    constexpr int smem = ELEMENTS ? L::TILE_BYTES : L::SMEM_BYTES;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return FGEMM_ERR_LAUNCH;
     }
     std::atomic<unsigned long long> &ready = ready_ctx[dev & 63];
     const unsigned long long ctx = current_context_id();
     if (ctx == 0 || ready.load(std::memory_order_acquire) != ctx) {
-        if (cudaFuncSetAttribute(quantize_kernel<T, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 L::SMEM_BYTES) != cudaSuccess) {
+        if (cudaFuncSetAttribute(quantize_kernel<T, GATED, ELEMENTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess) {
             (void)cudaGetLastError();
             return FGEMM_ERR_LAUNCH;
         }
         ready.store(current_context_id(), std::memory_order_release);
     }
+    quantize_kernel<T, GATED, ELEMENTS><<<(unsigned)std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms), L::THREADS,
+                                          smem, stream>>>(p, mode);
+    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+}
+
+template <class T, bool GATED>
+fgemm_status run_quantize(const QuantParams &p, cudaStream_t stream)
+{
+    int sms = 0;
+    if (device_sm_count(&sms) != 0) {
+        (void)cudaGetLastError();
+        return FGEMM_ERR_LAUNCH;
+    }
+    QuantParams q = p;
     const long long es = sizeof(T), tiles_m = (p.M + TILE - 1) / TILE, tiles = tiles_m * ((p.N + TILE - 1) / TILE);
     const int mode = aligned_to(p.x, p.ldx * es, 16) && (!GATED || aligned_to(p.gate, p.ldgate * es, 16)) ? COPY_16
                      : aligned_to(p.x, p.ldx * es, 4)                                                    ? COPY_4
                                                                                                          : COPY_ELEMENTS;
-    const int stages = mode == COPY_ELEMENTS ? 1 : L::STAGES;
-    quantize_kernel<T, GATED><<<(unsigned)std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms), L::THREADS,
-                                stages * L::TILE_BYTES, stream>>>(p, mode, stages);
-    if (cudaGetLastError() != cudaSuccess) return FGEMM_ERR_LAUNCH;
+    if (p.bias_grad && tiles_m > 1) q.early = 1;
+    fgemm_status st;
+    if constexpr (sizeof(T) == 2) {
+        st = mode == COPY_ELEMENTS ? start_quantize<T, GATED, true>(q, mode, tiles, sms, stream)
+                                   : start_quantize<T, GATED, false>(q, mode, tiles, sms, stream);
+    } else {
+        st = start_quantize<T, GATED, false>(q, mode, tiles, sms, stream);  // (FP32 is always 4-byte aligned)
+    }
+    if (st != FGEMM_OK) return st;
     if (p.bias_grad && tiles_m > 1) {
-        bias_grad_kernel<<<(unsigned)std::min<long long>((p.N + 255) / 256, 8ll * sms), 256, 0, stream>>>(
-            p.partial, (int)tiles_m, p.N, p.bias_grad);
-        if (cudaGetLastError() != cudaSuccess) return FGEMM_ERR_LAUNCH;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)std::min<long long>(((long long)p.N + 31) / 32, 8ll * sms));
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, bias_grad_kernel, (const float *)p.partial, (int)tiles_m, p.N, p.bias_grad) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return FGEMM_ERR_LAUNCH;
+        }
     }
     return FGEMM_OK;
 }
@@ -506,12 +614,22 @@ fgemm_status run_dequantize(const DequantParams &p, cudaStream_t stream)
         return FGEMM_ERR_LAUNCH;
     }
     constexpr int SPAN = 512 / (int)sizeof(T);
-    const long long items = ((p.N + SPAN - 1) / SPAN) * (((long long)p.M + 31) / 32);
-    const unsigned grid = (unsigned)std::min<long long>(items, 16ll * sms);
-    if (aligned_to(p.x, p.ldx * (long long)sizeof(T), 16))
-        dequantize_kernel<T, true><<<grid, 256, 0, stream>>>(p);
-    else
-        dequantize_kernel<T, false><<<grid, 256, 0, stream>>>(p);
+    const long long spans = ((long long)p.N + SPAN - 1) / SPAN, groups = ((long long)p.M + 31) / 32;
+    const bool vec = aligned_to(p.x, p.ldx * (long long)sizeof(T), 16);
+    // Few rows of work: one a warp, over more CTAs.
+    if (spans * groups < 2ll * sms) {
+        const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(((long long)p.M + 7) / 8, 65535));
+        if (vec)
+            dequantize_kernel<T, true, 1><<<grid, 256, 0, stream>>>(p);
+        else
+            dequantize_kernel<T, false, 1><<<grid, 256, 0, stream>>>(p);
+    } else {
+        const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(groups, 65535));
+        if (vec)
+            dequantize_kernel<T, true, 4><<<grid, 256, 0, stream>>>(p);
+        else
+            dequantize_kernel<T, false, 4><<<grid, 256, 0, stream>>>(p);
+    }
     return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
 }
 
