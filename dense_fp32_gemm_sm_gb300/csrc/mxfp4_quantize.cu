@@ -196,33 +196,38 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
     if (p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // Start the copies of tile w into a stage (asynchronous modes); beyond the matrix: zeros.
+    // (A thread's pieces lie in one column of pieces, a whole number of rows apart.)
     auto start = [&](long long w, int stage) {
         if (w < tiles) {
             const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
+            const int rows = (int)min((long long)TILE, p.M - r0), cols = (int)min((long long)TILE, p.N - c0);
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem) + stage * L::TILE_BYTES;
-            if (mode == COPY_16 && r0 + TILE <= p.M && c0 + TILE <= p.N) {
-                // An interior tile: pieces THREADS apart are whole rows apart, a multiple of 8.
-                const int row = t / L::CHUNKS_PER_ROW, c = t % L::CHUNKS_PER_ROW;
+            if (mode == COPY_16) {
                 constexpr int STEP = L::THREADS / L::CHUNKS_PER_ROW;
+                static_assert(STEP % 8 == 0, "the swizzle repeats");
+                const int row = t / L::CHUNKS_PER_ROW, c = t % L::CHUNKS_PER_ROW;
+                const int inside = max(0, min(cols - c * V, V)) * ES;
                 const uint32_t at = dst + piece_at(row, c);
                 const T *src = X + (r0 + row) * p.ldx + c0 + c * V;
+                if (rows == TILE && inside == 16) {
 #pragma unroll
-                for (int j = 0; j < L::CHUNKS; ++j, src += STEP * p.ldx) copy_async_16(at + j * STEP * 128, src, 16);
-            } else if (mode == COPY_16) {
-#pragma unroll 1
-                for (int j = 0; j < L::CHUNKS; ++j) {
-                    const int q = t + j * L::THREADS, row = q / L::CHUNKS_PER_ROW, c = q % L::CHUNKS_PER_ROW;
-                    const long long left = p.N - c0 - c * V;
-                    const int bytes = r0 + row < p.M && left > 0 ? (int)min(left, (long long)V) * ES : 0;
-                    copy_async_16(dst + piece_at(row, c), bytes ? X + (r0 + row) * p.ldx + c0 + c * V : X, bytes);
+                    for (int j = 0; j < L::CHUNKS; ++j, src += STEP * p.ldx) copy_async_16(at + j * STEP * 128, src, 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < L::CHUNKS; ++j, src += STEP * p.ldx) {
+                        const int bytes = row + j * STEP < rows ? inside : 0;
+                        copy_async_16(at + j * STEP * 128, bytes ? src : X, bytes);
+                    }
                 }
             } else {
+                constexpr int WORDS = TILE * ES / 4, STEP = L::THREADS / WORDS;  // words a row
+                const int row = t / WORDS, col = t % WORDS * (4 / ES);
+                const int inside = max(0, min(cols - col, 4 / ES)) * ES;
+                const T *src = X + (r0 + row) * p.ldx + c0 + col;
 #pragma unroll 8
-                for (int j = 0; j < 4 * L::CHUNKS; ++j) {
-                    const int q = t + j * L::THREADS, row = q / (4 * L::CHUNKS_PER_ROW), col = q % (4 * L::CHUNKS_PER_ROW) * (4 / ES);
-                    const long long left = p.N - c0 - col;
-                    const int bytes = r0 + row < p.M && left > 0 ? (int)min(left, 4ll / ES) * ES : 0;
-                    copy_async_4(dst + element_at<ES>(row, col), bytes ? X + (r0 + row) * p.ldx + c0 + col : X, bytes);
+                for (int j = 0; j < TILE / STEP; ++j, src += STEP * p.ldx) {
+                    const int bytes = row + j * STEP < rows ? inside : 0;
+                    copy_async_4(dst + element_at<ES>(row + j * STEP, col), bytes ? src : X, bytes);
                 }
             }
         }
@@ -264,33 +269,59 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
         const long long tm = w / tiles_n, tn = w - tm * tiles_n;
         const long long r0 = tm * TILE, c0 = tn * TILE;
         uint8_t *const tile = smem + stage * L::TILE_BYTES;
+        // This thread's elements one by one: a column's, OWN_STEP rows apart.
+        constexpr int OWN = TILE * TILE / L::THREADS, OWN_STEP = L::THREADS / TILE;
+        [[maybe_unused]] const int own_row = t / TILE, own_col = t % TILE;
+        [[maybe_unused]] const int own_rows = c0 + own_col < p.N ? (int)min((long long)TILE, p.M - r0) : 0;
+        [[maybe_unused]] uint32_t open[OWN / 32];  // COPY_4: gates of this thread's elements
         if constexpr (ELEMENTS) {
             __syncthreads();  // the previous tile has been read (one stage)
-            constexpr int BATCH = 32;  // loads in flight
-            for (int j = 0; j < TILE * TILE / L::THREADS; j += BATCH) {
-                T e[BATCH];
+            constexpr int BATCH = GATED ? 16 : 32;  // loads in flight
+            const T *src = X + (r0 + own_row) * p.ldx + c0 + own_col;
+            const T *gsrc = GATED ? Y + (r0 + own_row) * p.ldgate + c0 + own_col : nullptr;
+            for (int j = 0; j < OWN; j += BATCH) {
+                T e[BATCH], y[GATED ? BATCH : 1];
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int q = t + (j + i) * L::THREADS, row = q / TILE, col = q % TILE;
-                    const bool in = r0 + row < p.M && c0 + col < p.N;
-                    e[i] = in ? X[(r0 + row) * p.ldx + c0 + col] : from_float<T>(0.0f);
+                for (int i = 0; i < BATCH; ++i, src += OWN_STEP * p.ldx, gsrc += GATED ? OWN_STEP * p.ldgate : 0) {
+                    const bool in = own_row + (j + i) * OWN_STEP < own_rows;
+                    e[i] = in ? *src : from_float<T>(0.0f);
+                    if constexpr (GATED) y[i] = in ? *gsrc : from_float<T>(0.0f);
+                }
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (!(to_float(y[i]) > 0.0f)) e[i] = from_float<T>(0.0f);
                 }
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int q = t + (j + i) * L::THREADS;
-                    *reinterpret_cast<T *>(tile + element_at<ES>(q / TILE, q % TILE)) = e[i];
-                }
+                for (int i = 0; i < BATCH; ++i)
+                    *reinterpret_cast<T *>(tile + element_at<ES>(own_row + (j + i) * OWN_STEP, own_col)) = e[i];
             }
         } else {
+            // (The gates, a bit an element, while the copies are on their way.)
+            if constexpr (GATED) {
+                if (mode == COPY_4) {
+                    const T *gsrc = Y + (r0 + own_row) * p.ldgate + c0 + own_col;
+#pragma unroll
+                    for (int h = 0; h < OWN / 32; ++h) {
+                        T y[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i, gsrc += OWN_STEP * p.ldgate)
+                            y[i] = own_row + (32 * h + i) * OWN_STEP < own_rows ? *gsrc : from_float<T>(0.0f);
+                        open[h] = 0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) open[h] |= (uint32_t)(to_float(y[i]) > 0.0f) << i;
+                    }
+                }
+            }
             // This tile's copies are this thread's oldest group; at most stages - 2 follow it.
             if (L::STAGES == 3)
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             else
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
-        if constexpr (GATED) {
-            // Each thread closes the gates of the pieces it has copied itself.
-            if (!ELEMENTS && mode == COPY_16) {
+        if constexpr (GATED && !ELEMENTS) {
+            if (mode == COPY_16) {
+                // Each thread closes the gates of the pieces it has copied itself.
 #pragma unroll
                 for (int j = 0; j < L::CHUNKS; ++j) {
                     const int q = t + j * L::THREADS, row = q / L::CHUNKS_PER_ROW, c = q % L::CHUNKS_PER_ROW;
@@ -308,21 +339,11 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
                     *at = *reinterpret_cast<const uint4 *>(x);
                 }
             } else {
-                constexpr int BATCH = 16;
                 __syncthreads();
-                for (int j = 0; j < TILE * TILE / L::THREADS; j += BATCH) {
-                    bool open[BATCH];
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int q = t + (j + i) * L::THREADS, row = q / TILE, col = q % TILE;
-                        open[i] = r0 + row < p.M && c0 + col < p.N && to_float(Y[(r0 + row) * p.ldgate + c0 + col]) > 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int q = t + (j + i) * L::THREADS;
-                        if (!open[i]) *reinterpret_cast<T *>(tile + element_at<ES>(q / TILE, q % TILE)) = from_float<T>(0.0f);
-                    }
-                }
+                for (int j = 0; j < OWN; ++j)
+                    if (!(open[j / 32] >> (j % 32) & 1u))
+                        *reinterpret_cast<T *>(tile + element_at<ES>(own_row + j * OWN_STEP, own_col)) = from_float<T>(0.0f);
             }
         }
         __syncthreads();
