@@ -116,6 +116,7 @@ def library() -> ctypes.CDLL:
                      _c_int),
                     ("gemm", [_c_int] * 4 + [_c_float] + [_c_vp, _c_int, _c_vp] * 2 +
                      [_c_float, _c_vp, _c_int, _c_vp, _c_int, _c_vp], _c_int),
+                    ("plan", [_c_int] * 5, _c_int),
                     ("linear_workspace_size", [_c_int] * 3, _sz),
                     ("linear", [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
                                                _c_vp, _c_int, _c_vp, _sz, _c_vp], _c_int)):
@@ -381,8 +382,16 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
 
 # ---- MXFP4 (see "MXFP4" in include/fgemm.h) -------------------------------------------
 
-# Element types of unquantised matrices, by fgemm_dtype value.
+# Element types of unquantised matrices, by fgemm_dtype value; torch's own types join them as
+# they are met (this module does not import torch).
 _TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
+_types = {}
+
+
+def _type_of(dtype):
+    name = str(dtype)
+    t = _types[dtype] = _TYPE_NAMES.index(name) if name in _TYPE_NAMES else -1
+    return t
 
 
 try:  # the current stream's handle without building a Stream object (2 us a call)
@@ -402,10 +411,11 @@ def _mat(x, type):
     """Address of an unquantised matrix: a CUDA tensor of the call's type, or an address."""
     if x is None or x.__class__ is int:
         return x or None
-    if not x.is_cuda or not 0 <= type < 3 or str(x.dtype) != _TYPE_NAMES[type]:
+    dtype = x.dtype
+    if not x.is_cuda or (_types[dtype] if dtype in _types else _type_of(dtype)) != type:
         raise TypeError("fgemm type %r takes a CUDA tensor of that type (got %s on %s)"
-                        % (type, x.dtype, x.device))
-    return x.data_ptr() or None
+                        % (type, dtype, x.device))
+    return x.data_ptr()
 
 
 def _bytes(x):
@@ -414,7 +424,12 @@ def _bytes(x):
         return x or None
     if not x.is_cuda:
         raise TypeError("expected a CUDA tensor (got one on %s)" % (x.device,))
-    return x.data_ptr() or None
+    return x.data_ptr()
+
+
+def _vector(x):
+    """Address of a float vector (a bias or its gradient), or None."""
+    return None if x is None else _mat(x, F32)
 
 
 def mxfp4_codes_size(rows, cols) -> int:
@@ -431,7 +446,7 @@ def mxfp4_quantize(type, M, N, X, ldx, row_codes, ld_row_codes, row_scales, col_
                    ld_col_codes, col_scales, stream=None, check=True) -> int:
     """``fgemm_mxfp4_quantize``: X along its rows, its columns (the quantised X^T) or both;
     None for the codes and scales of a direction that is not wanted."""
-    st = library().fgemm_mxfp4_quantize(
+    st = (_lib or library()).fgemm_mxfp4_quantize(
         type, M, N, _mat(X, type), ldx, _bytes(row_codes), ld_row_codes, _bytes(row_scales),
         _bytes(col_codes), ld_col_codes, _bytes(col_scales), _on(stream, X))
     if check:
@@ -449,9 +464,9 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
                         workspace_bytes, stream=None, check=True) -> int:
     """``fgemm_mxfp4_quantize_grad``: G where Y > 0 (Y None: G), quantised as by
     ``mxfp4_quantize``, and its column sums (bias_grad None: not wanted)."""
-    st = library().fgemm_mxfp4_quantize_grad(
+    st = (_lib or library()).fgemm_mxfp4_quantize_grad(
         type, M, N, _mat(G, type), ldg, _mat(Y, type), ldy, _bytes(row_codes), ld_row_codes,
-        _bytes(row_scales), _bytes(col_codes), ld_col_codes, _bytes(col_scales), _ptr(bias_grad),
+        _bytes(row_scales), _bytes(col_codes), ld_col_codes, _bytes(col_scales), _vector(bias_grad),
         _bytes(workspace), workspace_bytes, _on(stream, bias_grad if G is None else G))
     if check:
         _check(st, "fgemm_mxfp4_quantize_grad")
@@ -460,7 +475,7 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
 
 def mxfp4_dequantize(type, M, N, codes, ld_codes, scales, X, ldx, stream=None, check=True) -> int:
     """``fgemm_mxfp4_dequantize``: X = the values of a quantised matrix."""
-    st = library().fgemm_mxfp4_dequantize(type, M, N, _bytes(codes), ld_codes, _bytes(scales),
+    st = (_lib or library()).fgemm_mxfp4_dequantize(type, M, N, _bytes(codes), ld_codes, _bytes(scales),
                                           _mat(X, type), ldx, _on(stream, X))
     if check:
         _check(st, "fgemm_mxfp4_dequantize")
@@ -471,13 +486,18 @@ def mxfp4_gemm(type, M, N, K, alpha, A_codes, ld_A_codes, A_scales, B_codes, ld_
                B_scales, beta, C, ldc, bias=None, apply_relu=False, stream=None,
                check=True) -> int:
     """``fgemm_mxfp4_gemm``: C = relu?(alpha*A*B^T + beta*C + bias[col]), A and B quantised."""
-    st = library().fgemm_mxfp4_gemm(
+    st = (_lib or library()).fgemm_mxfp4_gemm(
         type, M, N, K, alpha, _bytes(A_codes), ld_A_codes, _bytes(A_scales), _bytes(B_codes),
-        ld_B_codes, _bytes(B_scales), beta, _mat(C, type), ldc, _ptr(bias), 1 if apply_relu else 0,
+        ld_B_codes, _bytes(B_scales), beta, _mat(C, type), ldc, _vector(bias), 1 if apply_relu else 0,
         _on(stream, C))
     if check:
         _check(st, "fgemm_mxfp4_gemm")
     return st
+
+
+def mxfp4_plan(type, M, N, K, num_sms) -> int:
+    """``fgemm_mxfp4_plan``: 16 * tile + ranks of mxfp4_gemm's kernel for a product; host-only."""
+    return library().fgemm_mxfp4_plan(type, M, N, K, num_sms)
 
 
 def mxfp4_linear_workspace_size(M, N, K) -> int:
@@ -488,9 +508,9 @@ def mxfp4_linear_workspace_size(M, N, K) -> int:
 def mxfp4_linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias, apply_relu, Y, ldy,
                  workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
     """``fgemm_mxfp4_linear``: Y = relu?(Q(X)*W^T + bias[col]), X quantised on the way."""
-    st = library().fgemm_mxfp4_linear(
+    st = (_lib or library()).fgemm_mxfp4_linear(
         type, M, N, K, _mat(X, type), ldx, _bytes(W_codes), ld_W_codes, _bytes(W_scales),
-        _ptr(bias), 1 if apply_relu else 0, _mat(Y, type), ldy, _bytes(workspace),
+        _vector(bias), 1 if apply_relu else 0, _mat(Y, type), ldy, _bytes(workspace),
         workspace_bytes, _on(stream, Y))
     if check:
         _check(st, "fgemm_mxfp4_linear")

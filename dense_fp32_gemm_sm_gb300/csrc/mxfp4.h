@@ -63,20 +63,21 @@ struct GemmArgs {
 };
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream);
 
-// How a product runs: tiles of `nt` rows of A by 128 rows of B, each tile's K divided among
-// `ranks` CTAs of a cluster (0: whole tiles, by persistent CTAs; nt is then 128, or 512 for
-// pairs of CTAs with 256 rows of A, 384 for pairs with 192).
+// How a product runs.  nt 16, 32, 64: tiles of 128 rows of B by nt of A, each tile's K divided
+// among the `ranks` CTAs of a cluster.  nt 128: tiles of 128 x 128 by persistent CTAs.
+// PAIRS_192, PAIRS_256: tiles of 256 rows of B by 192 or 256 of A by persistent pairs of CTAs.
+enum { PAIRS_192 = 384, PAIRS_256 = 512 };
 struct GemmPlan {
     int nt, ranks;
 };
-GemmPlan plan_gemm(long long M, long long N, long long K, int sms);
+GemmPlan plan_gemm(long long M, long long N, long long K, int element_size, int sms);
 
 // A layer on at most LINEAR_ROWS unquantised tokens in one kernel: every CTA of a cluster of
 // eight at most quantises its part of them into FUSED_SMEM bytes of shared memory.
 constexpr int LINEAR_ROWS = 4;
 constexpr int FUSED_SMEM = 64 * 1024;
 bool linear_fused(long long M, long long K);
-GemmPlan plan_linear(long long N, long long K, int sms);
+int linear_ranks(long long N, long long K, int sms);  // CTAs of its clusters
 fgemm_status launch_linear(fgemm_dtype type, const void *x, long long ldx, const GemmArgs &g, cudaStream_t stream);
 
 }  // namespace mx

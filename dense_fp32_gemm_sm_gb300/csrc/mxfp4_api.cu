@@ -200,6 +200,13 @@ fgemm_status fgemm_mxfp4_gemm(fgemm_dtype type, int M, int N, int K, float alpha
     return launch_gemm(type, g, stream);
 }
 
+int fgemm_mxfp4_plan(fgemm_dtype type, int M, int N, int K, int num_sms)
+{
+    if (!valid_type(type) || M < 1 || N < 1 || K < 1 || num_sms < 2 || !dims_supported(M, N, K)) return -1;
+    const GemmPlan plan = plan_gemm(M, N, K, (int)type_size(type), num_sms);
+    return 16 * plan.nt + plan.ranks;
+}
+
 size_t fgemm_mxfp4_linear_workspace_size(int M, int N, int K)
 {
     if (M < 1 || N < 1 || K < 1 || linear_fused(M, K)) return 0;

@@ -11,17 +11,16 @@ namespace fgemm {
 namespace mx {
 
 template <class T>
-fgemm_status launch_tc_type(const GemmArgs &g, int nt, int ranks, cudaStream_t stream);
-extern template fgemm_status launch_tc_type<float>(const GemmArgs &, int, int, cudaStream_t);
-extern template fgemm_status launch_tc_type<__nv_bfloat16>(const GemmArgs &, int, int, cudaStream_t);
-extern template fgemm_status launch_tc_type<__half>(const GemmArgs &, int, int, cudaStream_t);
+fgemm_status launch_tc_type(const GemmArgs &g, GemmPlan plan, cudaStream_t stream);
+extern template fgemm_status launch_tc_type<float>(const GemmArgs &, GemmPlan, cudaStream_t);
+extern template fgemm_status launch_tc_type<__nv_bfloat16>(const GemmArgs &, GemmPlan, cudaStream_t);
+extern template fgemm_status launch_tc_type<__half>(const GemmArgs &, GemmPlan, cudaStream_t);
 
 template <class T>
-fgemm_status launch_fused_type(const GemmArgs &g, const void *x, long long ldx, int nt, int ranks, cudaStream_t stream);
-extern template fgemm_status launch_fused_type<float>(const GemmArgs &, const void *, long long, int, int, cudaStream_t);
-extern template fgemm_status launch_fused_type<__nv_bfloat16>(const GemmArgs &, const void *, long long, int, int,
-                                                              cudaStream_t);
-extern template fgemm_status launch_fused_type<__half>(const GemmArgs &, const void *, long long, int, int, cudaStream_t);
+fgemm_status launch_fused_type(const GemmArgs &g, const void *x, long long ldx, int ranks, cudaStream_t stream);
+extern template fgemm_status launch_fused_type<float>(const GemmArgs &, const void *, long long, int, cudaStream_t);
+extern template fgemm_status launch_fused_type<__nv_bfloat16>(const GemmArgs &, const void *, long long, int, cudaStream_t);
+extern template fgemm_status launch_fused_type<__half>(const GemmArgs &, const void *, long long, int, cudaStream_t);
 
 namespace {
 
@@ -57,40 +56,51 @@ fgemm_status run_gemm(const GemmArgs &g, cudaStream_t stream)
         no_products_kernel<T><<<(unsigned)std::min<long long>((total + 255) / 256, 8ll * sms), 256, 0, stream>>>(g);
         return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
     }
-    const GemmPlan plan = plan_gemm(g.M, g.N, g.K, sms);
-    return launch_tc_type<T>(g, plan.nt, plan.ranks, stream);
+    return launch_tc_type<T>(g, plan_gemm(g.M, g.N, g.K, (int)sizeof(T), sms), stream);
 }
 
 }  // namespace
 
-// Microseconds of a tile's stages over `ranks` CTAs, up to a constant: the stages of a CTA one
-// after the other (two CTAs on an SM share it), or B's bytes at the memory's rate; then what
-// joining the ranks' sums takes.
-static double split_time(long long N, long long K, long long tiles, long long stages, int ranks, int sms)
+// Estimated microseconds of the ways a product can run, fitted to measurements on one GB300 (30
+// shapes from 96 x 300 x 2000 to 8192 x 11008 x 4096, FP32 and BF16: the way with the least
+// estimate took 0.3 % longer than the fastest on average, 8 % at most).  Tiles over CTAs (or
+// pairs) come in rounds, each of so many stages and a boundary; C is written beside them.
+static double rounds(long long M, long long tile_m, long long N, long long tile_n, long long units)
 {
-    const double join[4] = {0.0, 1.0, 1.1, 2.7};
-    const long long ctas = tiles * ranks, waves = (ctas + sms - 1) / sms;
-    const double steps = 0.21 * (double)((stages + ranks - 1) / ranks) * (double)waves;
-    return std::max(steps, (double)N * (double)blocks_of(K) * 17.0 / 6.5e6) +
-           join[ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3];
+    const long long tiles = ((M + tile_m - 1) / tile_m) * ((N + tile_n - 1) / tile_n);
+    return (double)((tiles + units - 1) / units);
 }
 
-static int best_ranks(long long N, long long K, long long tiles, long long stages, int sms)
+// Of a split over `ranks` CTAs: the stages of a CTA one after the other, or B at the memory's
+// rate, then the joining of the sums.
+static double split_time(long long tiles, double stages, double b_time, int ranks, int sms)
 {
-    int best = 1;
-    for (int r = 2; r <= 8 && r <= stages; r *= 2)
-        if (split_time(N, K, tiles, stages, r, sms) < split_time(N, K, tiles, stages, best, sms)) best = r;
-    return best;
+    const double join = ranks == 1 ? 0.0 : ranks == 2 ? 1.6 : ranks == 4 ? 1.7 : 3.3;
+    const double waves = (double)((tiles * ranks + sms - 1) / sms), steps = (double)(((long long)stages + ranks - 1) / ranks);
+    return 4.0 + std::max(0.25 * steps * waves + 0.9 * (waves - 1.0), b_time) + join;
 }
 
-GemmPlan plan_gemm(long long M, long long N, long long K, int sms)
+GemmPlan plan_gemm(long long M, long long N, long long K, int element_size, int sms)
 {
-    const long long stages = (blocks_of(K) + 7) / 8, tiles_w = (N + 127) / 128;
+    const double stages = (double)((blocks_of(K) + 7) / 8);
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    const long long tiles = tiles_w * ((M + nt - 1) / nt);
-    if (nt == 64 && tiles_w * ((M + 255) / 256) >= sms) return GemmPlan{512, 0};
-    if (nt == 64 && tiles >= 2 * sms) return GemmPlan{128, 0};
-    return GemmPlan{nt, best_ranks(N, K, tiles, stages, sms)};
+    const long long tiles = ((M + nt - 1) / nt) * ((N + 127) / 128);
+    const double b_time = (double)N * (double)blocks_of(K) * 17.0 / 6.5e6, c_time = (double)M * (double)N * element_size / 6.5e6;
+    GemmPlan best{nt, 1};
+    double least = split_time(tiles, stages, b_time, 1, sms);
+    auto consider = [&](GemmPlan plan, double time) {
+        if (time < least) {
+            best = plan;
+            least = time;
+        }
+    };
+    for (int r = 2; r <= 8 && r <= stages && tiles * r <= sms; r *= 2)
+        consider(GemmPlan{nt, r}, split_time(tiles, stages, b_time, r, sms));
+    if (nt < 64) return best;
+    consider(GemmPlan{128, 0}, 3.5 + rounds(M, 128, N, 128, sms) * (0.7 + 0.26 * stages) + 0.25 * c_time);
+    consider(GemmPlan{PAIRS_192, 0}, 4.8 + rounds(M, 192, N, 256, sms / 2) * (1.6 + 0.215 * stages) + 0.30 * c_time);
+    consider(GemmPlan{PAIRS_256, 0}, 4.6 + rounds(M, 256, N, 256, sms / 2) * (1.8 + 0.295 * stages) + 0.40 * c_time);
+    return best;
 }
 
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream)
@@ -107,7 +117,7 @@ bool linear_fused(long long M, long long K)
     return M <= LINEAR_ROWS && (blocks_of(K) + 7) / 8 <= 8 * FUSED_STAGES;
 }
 
-GemmPlan plan_linear(long long N, long long K, int sms)
+int linear_ranks(long long N, long long K, int sms)
 {
     // As many ranks as two CTAs an SM allow: they divide the quantising too.  (A cluster of
     // eight costs more than it saves, and is for a K whose tokens need their shared memory.)
@@ -115,7 +125,7 @@ GemmPlan plan_linear(long long N, long long K, int sms)
     int ranks = 1;
     while (ranks < 8 && 2 * ranks <= stages && (stages > ranks * FUSED_STAGES || (ranks < 4 && 2 * ranks * tiles <= 2 * sms)))
         ranks *= 2;
-    return GemmPlan{16, ranks};
+    return ranks;
 }
 
 fgemm_status launch_linear(fgemm_dtype type, const void *x, long long ldx, const GemmArgs &g, cudaStream_t stream)
@@ -125,11 +135,11 @@ fgemm_status launch_linear(fgemm_dtype type, const void *x, long long ldx, const
         (void)cudaGetLastError();
         return FGEMM_ERR_LAUNCH;
     }
-    const GemmPlan plan = plan_linear(g.N, g.K, sms);
+    const int ranks = linear_ranks(g.N, g.K, sms);
     switch (type) {
-    case FGEMM_F32: return launch_fused_type<float>(g, x, ldx, plan.nt, plan.ranks, stream);
-    case FGEMM_BF16: return launch_fused_type<__nv_bfloat16>(g, x, ldx, plan.nt, plan.ranks, stream);
-    default: return launch_fused_type<__half>(g, x, ldx, plan.nt, plan.ranks, stream);
+    case FGEMM_F32: return launch_fused_type<float>(g, x, ldx, ranks, stream);
+    case FGEMM_BF16: return launch_fused_type<__nv_bfloat16>(g, x, ldx, ranks, stream);
+    default: return launch_fused_type<__half>(g, x, ldx, ranks, stream);
     }
 }
 

@@ -11,10 +11,16 @@
 //
 // A stage is 256 deep: 128 bytes of codes a row, the 128-byte swizzle's row, and two atoms of
 // scales (512 bytes, 128 rows x 4 blocks), which lie in memory as tcgen05.cp wants them.  One
-// warp's lane streams stages by TMA, another's copies each stage's scales to tensor memory
-// and issues four MMAs of depth 64; eight warps store the accumulators of the previous tile
-// meanwhile.  Few tiles with a long K are split over a cluster of CTAs, each with a range of
-// stages; their sums meet in shared memory and are added in rank order.
+// warp streams stages by TMA, another copies each stage's scales to tensor memory and issues
+// four MMAs of depth 64; eight warps store the accumulators of the previous tile meanwhile.
+//
+// What bounds it (one GB300): large products by the power limit -- 8192 x 8192 x 32768 runs at
+// 7.3 PFLOP/s with the SMs held at 1.54 GHz, 96 % of four 128-cycle MMAs a stage at that
+// clock; with K = 4096 by the boundaries of tiles and the writing of C; few rows by reading
+// B, 3.4 us after the launch and the joining of sums (16 x 11008 x 4096: 7.1 us, 3.5 at the
+// memory's rate).  Both loops below are walked by whole warps, one elected lane issuing: from
+// a branch on the lane number an MMA took 128 cycles to issue, whatever its width
+// (8192 x 8192 x 32768: 1198 us, against 683 with the whole warps).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -41,18 +47,15 @@ struct TcTile {
     static constexpr bool FUSED = MODE == SPLIT_FUSED;
     static constexpr int W_BYTES = TC_ROWS * 128;
     static constexpr int X_BYTES = NT * 128;
-    static constexpr int GROUPS = NT > 128 ? 2 : 1;  // 128-row groups of A's scales
-    static constexpr int X_SF_BYTES = 2 * ATOM_BYTES * GROUPS;
-    static constexpr int STAGE_BYTES = W_BYTES + 2 * ATOM_BYTES + (FUSED ? 0 : X_BYTES + X_SF_BYTES);
-    static constexpr int STAGES = NT > 64 && NT <= 128 ? 6 : 4;
+    static constexpr int SF_BYTES = 2 * ATOM_BYTES;  // of either operand: NT divides a group of 128 rows
+    static constexpr int STAGE_BYTES = W_BYTES + SF_BYTES + (FUSED ? 0 : X_BYTES + SF_BYTES);
+    // (80 KB for the narrow tiles, so that two CTAs share an SM; eight stages measured no faster.)
+    static constexpr int STAGES = NT == 128 ? 6 : 4;
     // Fused: A's codes and scales of each of this CTA's stages follow the ring and the barriers.
-    static constexpr int FUSED_BYTES = FUSED ? X_BYTES + X_SF_BYTES : 0;
-    // Tensor memory: two accumulators of NT columns, then two buffers of scales (4 columns an
-    // atom).  At NT = 256 those are 560 columns of the 512: the accumulators overlap by 64,
-    // and the epilogue reads the shared columns first.
-    static constexpr int ACC_STEP = NT == 256 ? 192 : NT;
-    static constexpr int SF_COLS = 8 * (1 + GROUPS);
-    static constexpr int SF_BASE = ACC_STEP + NT;
+    static constexpr int FUSED_BYTES = FUSED ? X_BYTES + SF_BYTES : 0;
+    // Tensor memory: two accumulators of NT columns, then two buffers of scales (4 columns an atom).
+    static constexpr int SF_COLS = 16;
+    static constexpr int SF_BASE = 2 * NT;
     static constexpr int TMEM_USED = SF_BASE + 2 * SF_COLS;
     static constexpr int TMEM_COLS = TMEM_USED > 256 ? 512 : TMEM_USED > 128 ? 256 : TMEM_USED > 64 ? 128 : 64;
     static_assert(TMEM_USED <= 512, "tensor memory");
@@ -352,43 +355,37 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     if (warp == 0) {
         // ---- producer: the whole warp walks along, one lane issues ----
         // A stage: B's codes and scales, then A's codes and scales.
-        auto load_w = [&](int k, int s, int w0, uint32_t x_bytes) {
+        auto load_w = [&](int k, int s, int w0) {
             const uint32_t at = sbase + s * L::STAGE_BYTES;
             const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;  // the last may be alone
-            tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + sf_bytes + x_bytes);
+            tc::mbar_arrive_expect_tx(full_bar(s), L::W_BYTES + sf_bytes + (FUSED ? 0 : L::X_BYTES + sf_bytes));
             tma_load_2d(at, &p.w, full_bar(s), k * 128, w0);
             bulk_load(at + L::W_BYTES, p.w_scales + ((long long)(w0 / 128) * p.atoms + 2ll * k) * ATOM_BYTES, sf_bytes,
                       full_bar(s));
         };
-        auto x_bytes_of = [&](int k, int groups) -> uint32_t {
-            return FUSED ? 0u : (uint32_t)(L::X_BYTES + groups * (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES);
-        };
-        auto load_x = [&](int k, int s, int x0, int groups) {
-            const uint32_t xc = sbase + s * L::STAGE_BYTES + L::W_BYTES + 2 * ATOM_BYTES, xf = xc + L::X_BYTES;
+        auto load_x = [&](int k, int s, int x0) {
+            const uint32_t xc = sbase + s * L::STAGE_BYTES + L::W_BYTES + L::SF_BYTES;
             const uint32_t sf_bytes = (p.atoms - 2ll * k > 1 ? 2 : 1) * ATOM_BYTES;
-            const uint8_t *const xs = p.x_scales + ((long long)(x0 / 128) * p.atoms + 2ll * k) * ATOM_BYTES;
             tma_load_2d(xc, &p.x, full_bar(s), k * 128, x0);
-            bulk_load(xf, xs, sf_bytes, full_bar(s));
-            if (groups == 2) bulk_load(xf + 2 * ATOM_BYTES, xs + p.atoms * ATOM_BYTES, sf_bytes, full_bar(s));
+            bulk_load(xc + L::X_BYTES, p.x_scales + ((long long)(x0 / 128) * p.atoms + 2ll * k) * ATOM_BYTES, sf_bytes,
+                      full_bar(s));
         };
         int g = 0;
         bool ok = true;
         for (long long t = first_tile; ok && t < tiles; t += tile_step) {
             int x0, w0, k = k_first;
             tile_at(t, x0, w0);
-            // The second group of A's scales, where the tile reaches into it.
-            const int groups = L::GROUPS == 2 && x0 + 128 < p.M ? 2 : 1;
             if (MODE == SPLIT && p.dependent) {
                 // Launched while the kernel that writes A may still run: B's part of the first
                 // stages, then the wait for that kernel, then A's.
                 int n = min(S, k_last - k_first);
                 if (p.withhold >= 0) n = min(n, p.withhold);
                 if (elect_one())
-                    for (int i = 0; i < n; ++i) load_w(k_first + i, i, w0, x_bytes_of(k_first + i, groups));
+                    for (int i = 0; i < n; ++i) load_w(k_first + i, i, w0);
                 __syncwarp();
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 if (elect_one())
-                    for (int i = 0; i < n; ++i) load_x(k_first + i, i, x0, groups);
+                    for (int i = 0; i < n; ++i) load_x(k_first + i, i, x0);
                 __syncwarp();
                 k += n;
                 g = n;
@@ -399,8 +396,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                      g != p.withhold;  // (testing: as if this copy never arrived)
                 if (!ok) break;
                 if (elect_one()) {
-                    load_w(k, s, w0, x_bytes_of(k, groups));
-                    if constexpr (!FUSED) load_x(k, s, x0, groups);
+                    load_w(k, s, w0);
+                    if constexpr (!FUSED) load_x(k, s, x0);
                 }
                 __syncwarp();
             }
@@ -411,18 +408,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA: the whole warp walks along, one lane issues ----
-        // (Inside a branch on the lane number, the operands of each tcgen05 instruction have to be
-        // moved to uniform registers one by one, and issuing took 128 cycles an MMA.)
         int g = 0, j = 0;
         bool ok = true;
         for (long long t = first_tile; ok && t < tiles; t += tile_step, ++j) {
             int x0, w0;
             tile_at(t, x0, w0);
             const int acc = j & 1;
-            // Tile j - 2's accumulator has been read; where the two overlap, the shared
-            // columns of tile j - 1's too.
-            const int before = NT == 256 ? j - 1 : j - 2;
-            if (before >= 0 && !warp_wait(acc_free_bar(before & 1), (before >> 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
+            // Tile j - 2's sums have been read.
+            if (j >= 2 && !warp_wait(acc_free_bar(acc), ((j >> 1) - 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
                 ok = false;
                 break;
             }
@@ -431,7 +424,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 break;
             }
             tc::tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)(acc * L::ACC_STEP);
+            const uint32_t d = tmem + (uint32_t)(acc * NT);
             for (int k = k_first; k < k_last; ++k, ++g) {
                 const int s = g % S;
                 ok = warp_wait(full_bar(s), (g / S) & 1, err, tc::ERR_MMA_WAIT, lim);
@@ -439,10 +432,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 tc::tc_fence_after();
                 if (elect_one()) {
                     const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES;
-                    uint32_t xc = sf + 2 * ATOM_BYTES, xf = xc + L::X_BYTES;
+                    uint32_t xc = sf + L::SF_BYTES, xf = xc + L::X_BYTES;
                     if constexpr (FUSED) {
                         xc = sbase + L::X_OFFSET + (k - k_first) * L::X_BYTES;
-                        xf = sbase + L::X_OFFSET + (k_last - k_first) * L::X_BYTES + (k - k_first) * L::X_SF_BYTES;
+                        xf = sbase + L::X_OFFSET + (k_last - k_first) * L::X_BYTES + (k - k_first) * L::SF_BYTES;
                     }
                     const uint32_t sfw = tmem + L::SF_BASE + (uint32_t)((g & 1) * L::SF_COLS), sfx = sfw + 8;
                     const int left = p.blocks - k * TC_BLOCKS;  // blocks from here on
@@ -455,16 +448,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                     for (int a = 0; a < 2; ++a) {
                         if (left > 4 * a) {
                             copy_atom(sfw + 4 * a, sf + a * ATOM_BYTES);
-#pragma unroll
-                            for (int i = 0; i < L::GROUPS; ++i)
-                                copy_atom(sfx + 4 * (a * L::GROUPS + i), xf + (2 * i + a) * ATOM_BYTES);
+                            copy_atom(sfx + 4 * a, xf + a * ATOM_BYTES);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (left > 2 * i)
                             mma_mxf4(d, wd + 2u * i, xd + 2u * i, mxf4_idesc(NT, 2 * (i & 1)), sfw + 4 * (i >> 1),
-                                     sfx_at + 4 * L::GROUPS * (i >> 1), k > k_first || i > 0);
+                                     sfx_at + 4 * (i >> 1), k > k_first || i > 0);
                     tc::umma_commit(empty_bar(s));
                     if (k + 1 == k_last) tc::umma_commit(acc_full_bar(acc));
                 }
@@ -496,7 +487,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             const int acc = j & 1;
             if (!tc::mbar_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
             tc::tc_fence_after();
-            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::ACC_STEP);
+            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NT);
             const int n = w0 + 32 * q + lane;
             const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
             T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
@@ -505,11 +496,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             constexpr int CHUNKS = NT / L::CHUNK;
 #pragma unroll 1
             for (int i = set; i < CHUNKS; i += 2) {
-                // The first accumulator's last columns are the second one's first: those first.
-                const int c0 = (NT == 256 && acc == 0 ? CHUNKS - 1 - i : i) * L::CHUNK;
+                const int c0 = i * L::CHUNK;
                 uint32_t r[L::CHUNK];
                 tmem_load(src + (uint32_t)c0, r);
-                if (NT == 256 && i == set) {
+                if (i + 2 >= CHUNKS) {  // this warp has read its part
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(acc_free_bar(acc));
@@ -522,11 +512,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 } else {
                     store_chunk(p, out + c0 * p.ldc, r, bias, p.M - x0 - c0, n < p.N, pairs);
                 }
-            }
-            if (NT != 256) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(acc_free_bar(acc));
             }
         }
         __syncwarp();

@@ -4,9 +4,8 @@
 namespace fgemm {
 namespace mx {
 
-template fgemm_status launch_tc_type<float>(const GemmArgs &g, int nt, int ranks, cudaStream_t stream);
-template fgemm_status launch_fused_type<float>(const GemmArgs &g, const void *x, long long ldx, int nt, int ranks,
-                                            cudaStream_t stream);
+template fgemm_status launch_tc_type<float>(const GemmArgs &g, GemmPlan plan, cudaStream_t stream);
+template fgemm_status launch_fused_type<float>(const GemmArgs &g, const void *x, long long ldx, int ranks, cudaStream_t stream);
 
 }  // namespace mx
 }  // namespace fgemm

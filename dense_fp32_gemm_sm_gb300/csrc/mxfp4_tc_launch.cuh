@@ -160,32 +160,24 @@ static fgemm_status launch_instance(const GemmArgs &g, const void *x, long long 
     return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
 }
 
-// The product with tiles of `nt` rows of A, each over a cluster of `ranks` CTAs (0: whole
-// tiles; 384 and 512: by pairs, of 192 and 256).
+// The product as planned (see GemmPlan).
 template <class T>
-fgemm_status launch_tc_type(const GemmArgs &g, int nt, int ranks, cudaStream_t stream)
+fgemm_status launch_tc_type(const GemmArgs &g, GemmPlan plan, cudaStream_t stream)
 {
-    if (ranks == 0) {
-        switch (nt) {
-        case 512: return launch_pairs<256, T>(g, stream);
-        case 384: return launch_pairs<192, T>(g, stream);
-        case 256: return launch_instance<256, T, WHOLE>(g, nullptr, 0, 0, stream);
-        default: return launch_instance<128, T, WHOLE>(g, nullptr, 0, 0, stream);
-        }
-    }
-    switch (nt) {
-    case 16: return launch_instance<16, T, SPLIT>(g, nullptr, 0, ranks, stream);
-    case 32: return launch_instance<32, T, SPLIT>(g, nullptr, 0, ranks, stream);
-    case 64: return launch_instance<64, T, SPLIT>(g, nullptr, 0, ranks, stream);
-    default: return launch_instance<128, T, SPLIT>(g, nullptr, 0, ranks, stream);
+    switch (plan.nt) {
+    case PAIRS_256: return launch_pairs<256, T>(g, stream);
+    case PAIRS_192: return launch_pairs<192, T>(g, stream);
+    case 128: return launch_instance<128, T, WHOLE>(g, nullptr, 0, 0, stream);
+    case 64: return launch_instance<64, T, SPLIT>(g, nullptr, 0, plan.ranks, stream);
+    case 32: return launch_instance<32, T, SPLIT>(g, nullptr, 0, plan.ranks, stream);
+    default: return launch_instance<16, T, SPLIT>(g, nullptr, 0, plan.ranks, stream);
     }
 }
 
 // The same with A as x (M x K, unquantised, element type T, at most LINEAR_ROWS rows).
 template <class T>
-fgemm_status launch_fused_type(const GemmArgs &g, const void *x, long long ldx, int nt, int ranks, cudaStream_t stream)
+fgemm_status launch_fused_type(const GemmArgs &g, const void *x, long long ldx, int ranks, cudaStream_t stream)
 {
-    (void)nt;  // 16
     return launch_instance<16, T, SPLIT_FUSED>(g, x, ldx, ranks, stream);
 }
 

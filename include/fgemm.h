@@ -513,6 +513,14 @@ fgemm_status fgemm_mxfp4_gemm(fgemm_dtype type, int M, int N, int K, float alpha
                               cudaStream_t stream);
 
 /*
+ * How fgemm_mxfp4_gemm runs a product with products to form on a GPU with `num_sms` SMs, as
+ * 16 * tile + ranks: tile 16, 32 or 64: that many rows of A by 128 of B a tile, whose K is
+ * divided among `ranks` CTAs; 128: 128 x 128 tiles; 384, 512: 192 or 256 rows of A by 256 of
+ * B, by pairs of CTAs (ranks 0).  -1 for arguments out of range.  Host-only: no CUDA call.
+ */
+int fgemm_mxfp4_plan(fgemm_dtype type, int M, int N, int K, int num_sms);
+
+/*
  * A layer on unquantised tokens: Y (M x N) = act(Q(X) W^T + bias), Q(X) being X (M x K)
  * quantised along its rows as fgemm_mxfp4_quantize does and W (N x K) a quantised matrix.
  * X and Y have element type `type`.

@@ -103,6 +103,15 @@ SHAPES = [(1, 1, 1), (1, 1000, 4096), (2, 128, 32), (5, 130, 64), (8, 128, 40), 
           (31, 640, 1030), (32, 128, 512), (33, 129, 320), (63, 127, 2048), (64, 256, 768), (65, 1000, 100),
           (127, 128, 129), (128, 128, 128), (129, 130, 1000), (255, 500, 544), (256, 256, 256), (257, 300, 33),
           (300, 2000, 700), (1000, 1001, 999), (2600, 1400, 320)]
+# Products that run by pairs of CTAs: one round and several, ragged in every size.
+PAIRS = [(2400, 1700, 4100), (1700, 2900, 4100), (5000, 5001, 2100), (769, 9990, 2305)]
+
+
+def test_the_shapes_reach_every_kernel():
+    tiles = {fg.mxfp4_plan(fg.F32, *s, 152) // 16 for s in SHAPES + PAIRS}
+    assert tiles == {16, 32, 64, 128, 384, 512}
+    ranks = {fg.mxfp4_plan(fg.F32, *s, 152) % 16 for s in SHAPES + [(130, 300, 40001), (40, 200, 11008)]}
+    assert ranks >= {0, 1, 4}
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -111,14 +120,20 @@ def test_exact_sums(M, N, K):
     check_exact("f32", M, N, K, seed=M + N + K)
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES[::3])
+@pytest.mark.parametrize("M,N,K", PAIRS)
+def test_exact_sums_by_pairs(M, N, K):
+    # (K * 144 < 2^20: as above)
+    check_exact("f32", M, N, K, bias=True, pad=1, seed=M + N + K)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES[::3] + PAIRS[:1])
 @pytest.mark.parametrize("t", TYPES)
 def test_epilogue(t, M, N, K):
     check(t, M, N, K, alpha=1.5 * 2.0**-7, beta=-0.75, bias=True, relu=True, pad=3, offset=1, seed=1)
     check(t, M, N, K, alpha=-2.0**-8, bias=True, pad=8, seed=2, c_nan=True)
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES[1::4])
+@pytest.mark.parametrize("M,N,K", SHAPES[1::4] + PAIRS[:1])
 @pytest.mark.parametrize("t", TYPES)
 def test_scales_of_many_sizes(t, M, N, K):
     # scales over 2^-12 .. 2^11; padded rows of codes

@@ -132,6 +132,26 @@ def test_binding_checks_tensor_types():
         _gemm(A_codes=torch.zeros(4, 32, dtype=torch.uint8))
 
 
+def test_plan():
+    plan = lambda *a: divmod(fg.mxfp4_plan(*a), 16)  # noqa: E731
+    # few rows: narrow tiles, a long K over a few tiles divided, one or two B tiles an SM not
+    assert plan(fg.F32, 1, 11008, 4096, 152) == (16, 1)
+    assert plan(fg.F32, 20, 4096, 11008, 152) == (32, 4)
+    assert plan(fg.F32, 130, 1001, 11013, 152) == (64, 4)
+    assert plan(fg.F32, 256, 256, 256, 152) == (64, 1)
+    # a rank never goes without stages of 256
+    for K in (1, 256, 257, 600, 1025):
+        for M in (1, 17, 33):
+            assert 1 <= plan(fg.BF16, M, 128, K, 152)[1] <= -(-K // 256)
+    # large products: pairs of CTAs, in the tile that wastes less of the last round
+    assert plan(fg.BF16, 8192, 11008, 4096, 152) in ((384, 0), (512, 0))
+    assert plan(fg.BF16, 2048, 4096, 11008, 152) == (512, 0)
+    assert plan(fg.F32, 8000, 1000, 4000, 152) == (512, 0)
+    assert plan(fg.F32, 4096, 4096, 1024, 152) == (128, 0)
+    for bad in ((3, 4, 4, 4, 152), (0, 0, 4, 4, 152), (0, 4, 4, 0, 152), (0, 4, 4, 4, 1), (0, 2**31 - 1, 4, 4, 152)):
+        assert fg.mxfp4_plan(*bad) == -1
+
+
 def test_definition_by_hand():
     # largest 7: floor(log2 7) = 2, scale 2^0; 7 saturates to 6; ties go to the even code
     x = [7.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -5.0, 0.26, -0.0]
