@@ -37,7 +37,6 @@ struct QuantParams {
     long long ld_col;
     float *bias_grad;  // or null
     float *partial;    // one partial column sum per 128 rows
-    int early;         // let the next kernel of the stream start (it waits before it reads)
 };
 fgemm_status launch_quantize(fgemm_dtype type, const QuantParams &p, cudaStream_t stream);
 
@@ -59,7 +58,7 @@ struct GemmArgs {
     long long ldc;
     const float *bias;
     int relu;
-    int dependent;  // A is written by the quantising kernel launched just before, with `early`
+    int dependent;  // A is written by the quantising kernel launched just before, B is not
 };
 fgemm_status launch_gemm(fgemm_dtype type, const GemmArgs &g, cudaStream_t stream);
 

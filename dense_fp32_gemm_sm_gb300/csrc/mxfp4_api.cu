@@ -245,9 +245,8 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
     uint8_t *const codes = static_cast<uint8_t *>(workspace);
     uint8_t *const scales = codes + round256(codes_bytes(M, K));
     const int ld = (int)(16 * blocks_of(K));
-    QuantParams q = quant_params(M, K, X, ldx, Direction{codes, ld, scales}, Direction{nullptr, 0, nullptr});
-    q.early = 1;
-    const fgemm_status st = launch_quantize(type, q, stream);
+    const fgemm_status st = launch_quantize(
+        type, quant_params(M, K, X, ldx, Direction{codes, ld, scales}, Direction{nullptr, 0, nullptr}), stream);
     if (st != FGEMM_OK) return st;
     g.a = codes;
     g.a_scales = scales;

@@ -11,6 +11,13 @@
 namespace fgemm {
 namespace mx {
 
+// See mxfp4_launch.h: wait for the kernel before this one, then let the next one come.
+__device__ __forceinline__ void after_previous_kernel()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }

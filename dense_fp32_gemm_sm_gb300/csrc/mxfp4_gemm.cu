@@ -6,6 +6,7 @@
 
 #include "fgemm_internal.h"
 #include "mxfp4_device.cuh"
+#include "mxfp4_launch.h"
 
 namespace fgemm {
 namespace mx {
@@ -31,6 +32,7 @@ constexpr long long FUSED_STAGES = FUSED_SMEM / (16 * 128 + 2 * ATOM_BYTES);
 template <class T>
 __global__ void __launch_bounds__(256) no_products_kernel(const GemmArgs g)
 {
+    after_previous_kernel();
     const long long total = (long long)g.M * g.N;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
         const long long r = i / g.N, c = i - r * g.N;
@@ -53,8 +55,8 @@ fgemm_status run_gemm(const GemmArgs &g, cudaStream_t stream)
     }
     if (g.K == 0) {
         const long long total = (long long)g.M * g.N;
-        no_products_kernel<T><<<(unsigned)std::min<long long>((total + 255) / 256, 8ll * sms), 256, 0, stream>>>(g);
-        return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+        const dim3 grid((unsigned)std::min<long long>((total + 255) / 256, 8ll * sms));
+        return launch(no_products_kernel<T>, grid, 256, 0, stream, 1, g) == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
     }
     return launch_tc_type<T>(g, plan_gemm(g.M, g.N, g.K, (int)sizeof(T), sms), stream);
 }

@@ -10,6 +10,7 @@
 #include "ctx_id.h"
 #include "fgemm_internal.h"
 #include "mxfp4_device.cuh"
+#include "mxfp4_launch.h"
 
 namespace fgemm {
 namespace mx {
@@ -192,8 +193,7 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
     const long long row_blocks = blocks_of(p.N), col_blocks = blocks_of(p.M);
     const T *const X = static_cast<const T *>(p.x);
     const T *const Y = static_cast<const T *>(p.gate);
-    // (Whatever comes next and was told that it may start waits before it reads.)
-    if (p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_previous_kernel();
 
     // Start the copies of tile w into a stage (asynchronous modes); beyond the matrix: zeros.
     // (A thread's pieces lie in one column of pieces, a whole number of rows apart.)
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *partial, in
 {
     __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partial sums are being formed
+    after_previous_kernel();
     for (long long j0 = blockIdx.x * 32ll; j0 < N; j0 += gridDim.x * 32ll) {
         const long long j = j0 + lane;
         float s = 0.0f;
@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
 {
     constexpr int V = 16 / (int)sizeof(T), SPAN = 32 * V;  // elements a lane, a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    after_previous_kernel();
     const long long atoms = atoms_of(blocks_of(p.N)), k0 = (long long)blockIdx.x * SPAN;
     // A CTA: 8 * ROWS rows of a span; a warp: rows warp, warp + 8, ...
     for (long long r0 = (long long)blockIdx.y * (8 * ROWS) + warp; r0 < p.M; r0 += (long long)gridDim.y * (8 * ROWS)) {
@@ -580,9 +581,10 @@ fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int
         }
         ready.store(current_context_id(), std::memory_order_release);
     }
-    quantize_kernel<T, GATED, ELEMENTS><<<(unsigned)std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms), L::THREADS,
-                                          smem, stream>>>(p, mode);
-    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    const dim3 grid((unsigned)std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms));
+    return launch(quantize_kernel<T, GATED, ELEMENTS>, grid, L::THREADS, smem, stream, 1, p, mode) == cudaSuccess
+               ? FGEMM_OK
+               : FGEMM_ERR_LAUNCH;
 }
 
 template <class T, bool GATED>
@@ -593,35 +595,22 @@ fgemm_status run_quantize(const QuantParams &p, cudaStream_t stream)
         (void)cudaGetLastError();
         return FGEMM_ERR_LAUNCH;
     }
-    QuantParams q = p;
     const long long es = sizeof(T), tiles_m = (p.M + TILE - 1) / TILE, tiles = tiles_m * ((p.N + TILE - 1) / TILE);
     const int mode = aligned_to(p.x, p.ldx * es, 16) && (!GATED || aligned_to(p.gate, p.ldgate * es, 16)) ? COPY_16
                      : aligned_to(p.x, p.ldx * es, 4)                                                    ? COPY_4
                                                                                                          : COPY_ELEMENTS;
-    if (p.bias_grad && tiles_m > 1) q.early = 1;
     fgemm_status st;
     if constexpr (sizeof(T) == 2) {
-        st = mode == COPY_ELEMENTS ? start_quantize<T, GATED, true>(q, mode, tiles, sms, stream)
-                                   : start_quantize<T, GATED, false>(q, mode, tiles, sms, stream);
+        st = mode == COPY_ELEMENTS ? start_quantize<T, GATED, true>(p, mode, tiles, sms, stream)
+                                   : start_quantize<T, GATED, false>(p, mode, tiles, sms, stream);
     } else {
-        st = start_quantize<T, GATED, false>(q, mode, tiles, sms, stream);  // (FP32 is always 4-byte aligned)
+        st = start_quantize<T, GATED, false>(p, mode, tiles, sms, stream);  // (FP32 is always 4-byte aligned)
     }
     if (st != FGEMM_OK) return st;
     if (p.bias_grad && tiles_m > 1) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)std::min<long long>(((long long)p.N + 31) / 32, 8ll * sms));
-        cfg.blockDim = dim3(256);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, bias_grad_kernel, (const float *)p.partial, (int)tiles_m, p.N, p.bias_grad) !=
-            cudaSuccess) {
-            (void)cudaGetLastError();
+        const dim3 grid((unsigned)std::min<long long>(((long long)p.N + 31) / 32, 8ll * sms));
+        if (launch(bias_grad_kernel, grid, 256, 0, stream, 1, p.partial, (int)tiles_m, p.N, p.bias_grad) != cudaSuccess)
             return FGEMM_ERR_LAUNCH;
-        }
     }
     return FGEMM_OK;
 }
@@ -637,21 +626,18 @@ fgemm_status run_dequantize(const DequantParams &p, cudaStream_t stream)
     constexpr int SPAN = 512 / (int)sizeof(T);
     const long long spans = ((long long)p.N + SPAN - 1) / SPAN, groups = ((long long)p.M + 31) / 32;
     const bool vec = aligned_to(p.x, p.ldx * (long long)sizeof(T), 16);
+    cudaError_t e;
     // Few rows of work: one a warp, over more CTAs.
     if (spans * groups < 2ll * sms) {
         const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(((long long)p.M + 7) / 8, 65535));
-        if (vec)
-            dequantize_kernel<T, true, 1><<<grid, 256, 0, stream>>>(p);
-        else
-            dequantize_kernel<T, false, 1><<<grid, 256, 0, stream>>>(p);
+        e = vec ? launch(dequantize_kernel<T, true, 1>, grid, 256, 0, stream, 1, p)
+                : launch(dequantize_kernel<T, false, 1>, grid, 256, 0, stream, 1, p);
     } else {
         const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(groups, 65535));
-        if (vec)
-            dequantize_kernel<T, true, 4><<<grid, 256, 0, stream>>>(p);
-        else
-            dequantize_kernel<T, false, 4><<<grid, 256, 0, stream>>>(p);
+        e = vec ? launch(dequantize_kernel<T, true, 4>, grid, 256, 0, stream, 1, p)
+                : launch(dequantize_kernel<T, false, 4>, grid, 256, 0, stream, 1, p);
     }
-    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    return e == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -96,6 +96,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -328,6 +333,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     };
 
     if (warp == 0 && lane == 0) {
+        prefetch_map(&p.w);
+        if constexpr (!FUSED) prefetch_map(&p.x);
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(full_bar(s), 1);
             tc::mbar_init(empty_bar(s), 1);
@@ -351,6 +358,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
+    // (The producer of a dependent product waits below, after it has asked for B.)
+    if (!(MODE == SPLIT && p.dependent && warp == 0)) after_previous_kernel();
 
     if (warp == 0) {
         // ---- producer: the whole warp walks along, one lane issues ----
@@ -376,14 +385,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
             int x0, w0, k = k_first;
             tile_at(t, x0, w0);
             if (MODE == SPLIT && p.dependent) {
-                // Launched while the kernel that writes A may still run: B's part of the first
-                // stages, then the wait for that kernel, then A's.
+                // The kernel before this one, which may still run, writes A and has itself waited for
+                // all before it: B's part of the first stages, then the wait for it, then A's.
                 int n = min(S, k_last - k_first);
                 if (p.withhold >= 0) n = min(n, p.withhold);
                 if (elect_one())
                     for (int i = 0; i < n; ++i) load_w(k_first + i, i, w0);
                 __syncwarp();
-                asm volatile("griddepcontrol.wait;" ::: "memory");
+                after_previous_kernel();
                 if (elect_one())
                     for (int i = 0; i < n; ++i) load_x(k_first + i, i, x0);
                 __syncwarp();
@@ -654,7 +663,7 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
 }
 
 template <int NT, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(TC_THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ PairArgs args, unsigned *err)
 {
     using L = PairTile<NT>;
@@ -685,6 +694,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     };
 
     if (warp == 0 && lane == 0) {
+        prefetch_map(&args.w);
+        prefetch_map(&args.x);
+        prefetch_map(&args.sw);
+        prefetch_map(&args.sx);
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(full_bar(s), 1);
             tc::mbar_init(empty_bar(s), 1);
@@ -706,6 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     cluster.sync();
     tc::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
+    after_previous_kernel();
 
     if (warp == 0) {
         // ---- producer, one in each CTA ----

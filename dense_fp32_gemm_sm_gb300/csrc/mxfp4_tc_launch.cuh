@@ -7,6 +7,7 @@
 
 #include "ctx_id.h"
 #include "fgemm_internal.h"
+#include "mxfp4_launch.h"
 #include "mxfp4_tc.cuh"
 #include "tc_host.h"
 
@@ -101,8 +102,8 @@ static fgemm_status launch_pairs(const GemmArgs &g, cudaStream_t stream)
         !make_scales_map(&p.sw, g.b_scales, g.N, p.t.atoms, 1) || !make_scales_map(&p.sx, g.a_scales, g.M, p.t.atoms, 2))
         return FGEMM_ERR_NOT_SUPPORTED;
     const long long tiles = (long long)p.t.tiles_x * p.t.tiles_w, most = sms / 2;
-    kernel<<<(unsigned)(2 * (tiles < most ? tiles : most)), TC_THREADS, L::SMEM_BYTES, stream>>>(p, err);
-    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    const dim3 grid((unsigned)(2 * (tiles < most ? tiles : most)));
+    return launch(kernel, grid, TC_THREADS, L::SMEM_BYTES, stream, 2, p, err) == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
 }
 
 // One CTA a tile (WHOLE), or a cluster of `ranks`.  x, ldx: the unquantised A of SPLIT_FUSED.
@@ -135,29 +136,11 @@ static fgemm_status launch_instance(const GemmArgs &g, const void *x, long long 
         return FGEMM_ERR_NOT_SUPPORTED;
     }
     const long long tiles = (long long)p.tiles_x * p.tiles_w;
-    if (MODE == WHOLE) {
-        kernel<<<(unsigned)(tiles < sms ? tiles : sms), TC_THREADS, smem, stream>>>(p, err);
-    } else {
-        if (tiles * ranks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(tiles * ranks));
-        cfg.blockDim = dim3(TC_THREADS);
-        cfg.dynamicSmemBytes = (size_t)smem;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ranks;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = p.dependent ? 2 : 1;
-        if (cudaLaunchKernelEx(&cfg, kernel, p, err) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return FGEMM_ERR_LAUNCH;
-        }
-    }
-    return cudaGetLastError() == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
+    if (MODE != WHOLE && tiles * ranks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
+    const dim3 grid((unsigned)(MODE != WHOLE ? tiles * ranks : tiles < sms ? tiles : sms));
+    return launch(kernel, grid, TC_THREADS, (size_t)smem, stream, MODE != WHOLE ? (unsigned)ranks : 1u, p, err) == cudaSuccess
+               ? FGEMM_OK
+               : FGEMM_ERR_LAUNCH;
 }
 
 // The product as planned (see GemmPlan).
