@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI declared in ``include/fgemm.h``.
+"""Binding of the C ABI declared in ``include/fgemm.h``: ctypes, and a small C module for the
+MXFP4 calls.
 
 Argument marshalling only: every call goes straight to ``libfgemm.so`` and the
 work runs in its CUDA kernels.  Matrices may be given as CUDA float32 torch
@@ -13,6 +14,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import sys
 import threading
 
 from . import _build
@@ -107,19 +109,9 @@ def library() -> ctypes.CDLL:
             for name, argtypes, restype in (
                     ("codes_size", [_c_int] * 2, _sz),
                     ("scales_size", [_c_int] * 2, _sz),
-                    ("quantize", [_c_int] * 3 + [_c_vp, _c_int] * 2 + [_c_vp, _c_vp, _c_int, _c_vp,
-                                                                       _c_vp], _c_int),
                     ("quantize_grad_workspace_size", [_c_int] * 2, _sz),
-                    ("quantize_grad", [_c_int] * 3 + [_c_vp, _c_int] * 3 +
-                     [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _sz, _c_vp], _c_int),
-                    ("dequantize", [_c_int] * 3 + [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp],
-                     _c_int),
-                    ("gemm", [_c_int] * 4 + [_c_float] + [_c_vp, _c_int, _c_vp] * 2 +
-                     [_c_float, _c_vp, _c_int, _c_vp, _c_int, _c_vp], _c_int),
                     ("plan", [_c_int] * 5, _c_int),
-                    ("linear_workspace_size", [_c_int] * 3, _sz),
-                    ("linear", [_c_int] * 4 + [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
-                                               _c_vp, _c_int, _c_vp, _sz, _c_vp], _c_int)):
+                    ("linear_workspace_size", [_c_int] * 3, _sz)):
                 fn = getattr(lib, "fgemm_mxfp4_" + name)
                 fn.argtypes = argtypes
                 fn.restype = restype
@@ -382,54 +374,42 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
 
 # ---- MXFP4 (see "MXFP4" in include/fgemm.h) -------------------------------------------
 
-# Element types of unquantised matrices, by fgemm_dtype value; torch's own types join them as
-# they are met (this module does not import torch).
+# The calls' arguments are converted by a small C module (csrc/py_calls.c); it takes tensors or
+# addresses like the functions above.
+
 _TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
-_types = {}
+_calls = None
 
 
 def _type_of(dtype):
+    """fgemm_dtype value of a torch dtype (this module does not import torch), or -1."""
     name = str(dtype)
-    t = _types[dtype] = _TYPE_NAMES.index(name) if name in _TYPE_NAMES else -1
-    return t
+    return _TYPE_NAMES.index(name) if name in _TYPE_NAMES else -1
 
 
-try:  # the current stream's handle without building a Stream object (2 us a call)
-    from torch._C import _cuda_getCurrentRawStream as _raw_stream
-except ImportError:
-    _raw_stream = None
+def _current_stream(device):
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _on(stream, x):
-    """Handle of the stream a call runs on: the given one, or torch's current one on x's device."""
-    if stream is None and _raw_stream is not None and not isinstance(x, int) and x is not None:
-        return _raw_stream(x.get_device()) or None
-    return _stream(stream, x)
-
-
-def _mat(x, type):
-    """Address of an unquantised matrix: a CUDA tensor of the call's type, or an address."""
-    if x is None or x.__class__ is int:
-        return x or None
-    dtype = x.dtype
-    if not x.is_cuda or (_types[dtype] if dtype in _types else _type_of(dtype)) != type:
-        raise TypeError("fgemm type %r takes a CUDA tensor of that type (got %s on %s)"
-                        % (type, dtype, x.device))
-    return x.data_ptr()
-
-
-def _bytes(x):
-    """Address of codes, scales or a workspace: a CUDA tensor of any type, or an address."""
-    if x is None or x.__class__ is int:
-        return x or None
-    if not x.is_cuda:
-        raise TypeError("expected a CUDA tensor (got one on %s)" % (x.device,))
-    return x.data_ptr()
-
-
-def _vector(x):
-    """Address of a float vector (a bias or its gradient), or None."""
-    return None if x is None else _mat(x, F32)
+def _native():
+    """Load the C module and give it the library's entries."""
+    global _calls
+    lib = library()
+    with _lock:
+        if _calls is None:
+            from . import _calls as module
+            raw_stream = _current_stream
+            if "torch" in sys.modules:
+                try:  # the handle without a Stream object, which takes 2 us
+                    from torch._C import _cuda_getCurrentRawStream as raw_stream
+                except ImportError:
+                    pass
+            module.bind(_type_of, raw_stream,
+                        *(ctypes.cast(getattr(lib, "fgemm_mxfp4_" + name), _c_vp).value
+                          for name in ("quantize", "quantize_grad", "dequantize", "gemm", "linear")))
+            _calls = module
+    return _calls
 
 
 def mxfp4_codes_size(rows, cols) -> int:
@@ -446,9 +426,8 @@ def mxfp4_quantize(type, M, N, X, ldx, row_codes, ld_row_codes, row_scales, col_
                    ld_col_codes, col_scales, stream=None, check=True) -> int:
     """``fgemm_mxfp4_quantize``: X along its rows, its columns (the quantised X^T) or both;
     None for the codes and scales of a direction that is not wanted."""
-    st = (_lib or library()).fgemm_mxfp4_quantize(
-        type, M, N, _mat(X, type), ldx, _bytes(row_codes), ld_row_codes, _bytes(row_scales),
-        _bytes(col_codes), ld_col_codes, _bytes(col_scales), _on(stream, X))
+    st = (_calls or _native()).quantize(type, M, N, X, ldx, row_codes, ld_row_codes, row_scales,
+                                       col_codes, ld_col_codes, col_scales, stream)
     if check:
         _check(st, "fgemm_mxfp4_quantize")
     return st
@@ -464,10 +443,9 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
                         workspace_bytes, stream=None, check=True) -> int:
     """``fgemm_mxfp4_quantize_grad``: G where Y > 0 (Y None: G), quantised as by
     ``mxfp4_quantize``, and its column sums (bias_grad None: not wanted)."""
-    st = (_lib or library()).fgemm_mxfp4_quantize_grad(
-        type, M, N, _mat(G, type), ldg, _mat(Y, type), ldy, _bytes(row_codes), ld_row_codes,
-        _bytes(row_scales), _bytes(col_codes), ld_col_codes, _bytes(col_scales), _vector(bias_grad),
-        _bytes(workspace), workspace_bytes, _on(stream, bias_grad if G is None else G))
+    st = (_calls or _native()).quantize_grad(
+        type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row_scales, col_codes, ld_col_codes,
+        col_scales, bias_grad, workspace, workspace_bytes, stream)
     if check:
         _check(st, "fgemm_mxfp4_quantize_grad")
     return st
@@ -475,8 +453,7 @@ def mxfp4_quantize_grad(type, M, N, G, ldg, Y, ldy, row_codes, ld_row_codes, row
 
 def mxfp4_dequantize(type, M, N, codes, ld_codes, scales, X, ldx, stream=None, check=True) -> int:
     """``fgemm_mxfp4_dequantize``: X = the values of a quantised matrix."""
-    st = (_lib or library()).fgemm_mxfp4_dequantize(type, M, N, _bytes(codes), ld_codes, _bytes(scales),
-                                          _mat(X, type), ldx, _on(stream, X))
+    st = (_calls or _native()).dequantize(type, M, N, codes, ld_codes, scales, X, ldx, stream)
     if check:
         _check(st, "fgemm_mxfp4_dequantize")
     return st
@@ -486,10 +463,8 @@ def mxfp4_gemm(type, M, N, K, alpha, A_codes, ld_A_codes, A_scales, B_codes, ld_
                B_scales, beta, C, ldc, bias=None, apply_relu=False, stream=None,
                check=True) -> int:
     """``fgemm_mxfp4_gemm``: C = relu?(alpha*A*B^T + beta*C + bias[col]), A and B quantised."""
-    st = (_lib or library()).fgemm_mxfp4_gemm(
-        type, M, N, K, alpha, _bytes(A_codes), ld_A_codes, _bytes(A_scales), _bytes(B_codes),
-        ld_B_codes, _bytes(B_scales), beta, _mat(C, type), ldc, _vector(bias), 1 if apply_relu else 0,
-        _on(stream, C))
+    st = (_calls or _native()).gemm(type, M, N, K, alpha, A_codes, ld_A_codes, A_scales, B_codes,
+                                   ld_B_codes, B_scales, beta, C, ldc, bias, apply_relu, stream)
     if check:
         _check(st, "fgemm_mxfp4_gemm")
     return st
@@ -508,10 +483,8 @@ def mxfp4_linear_workspace_size(M, N, K) -> int:
 def mxfp4_linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias, apply_relu, Y, ldy,
                  workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
     """``fgemm_mxfp4_linear``: Y = relu?(Q(X)*W^T + bias[col]), X quantised on the way."""
-    st = (_lib or library()).fgemm_mxfp4_linear(
-        type, M, N, K, _mat(X, type), ldx, _bytes(W_codes), ld_W_codes, _bytes(W_scales),
-        _vector(bias), 1 if apply_relu else 0, _mat(Y, type), ldy, _bytes(workspace),
-        workspace_bytes, _on(stream, Y))
+    st = (_calls or _native()).linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias,
+                                     apply_relu, Y, ldy, workspace, workspace_bytes, stream)
     if check:
         _check(st, "fgemm_mxfp4_linear")
     return st

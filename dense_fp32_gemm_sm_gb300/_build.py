@@ -1,4 +1,5 @@
-"""Build ``libfgemm.so`` in-tree from ``csrc/`` with nvcc for sm_103a.
+"""Build ``libfgemm.so`` in-tree from ``csrc/`` with nvcc for sm_103a, and ``_calls.so``, the
+Python side of the MXFP4 entries, from ``csrc/py_calls.c``.
 
 Each translation unit is compiled in parallel, then linked into one shared
 object beside this file.  A rebuild happens only when a source or header is
@@ -12,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfgemm.so")
+CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "py_calls.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
               "-I" + os.path.join(ROOT, "include")]
@@ -48,7 +52,27 @@ def stale() -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def build_calls(force: bool = False) -> str:
+    """``_calls.so``, a CPython extension module (plain C, no CUDA code)."""
+    header = os.path.join(ROOT, "include", "fgemm.h")
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(
+            os.path.getmtime(f) for f in (CALLS_SRC, header, __file__)):
+        return CALLS
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = CALLS + ".tmp.%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include"),
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           CALLS_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("gcc failed on %s" % CALLS_SRC)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and not stale():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)

@@ -1,0 +1,134 @@
+"""A fully-connected layer Y = ReLU(X W + b) in MXFP4, trained and served.
+
+The package's MXFP4 calls as they go together: the master weight W (K x N) is quantised both
+ways in one pass, along its columns for the product forward and along its rows for the
+gradient of X; tokens X (M x K) along their rows forward and their columns for the gradient
+of W; the output's gradient both ways behind ReLU's gate, with the bias's gradient.  A few
+tokens at a time go through ``decode``, which quantises them on the way.
+
+Buffers belong to the layer and are made for the sizes met; nothing else is allocated.
+``python -m dense_fp32_gemm_sm_gb300.mxfp4_layer`` fits a small layer to another one's outputs.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import _binding as fg
+
+_TYPES = {torch.float32: fg.F32, torch.bfloat16: fg.BF16, torch.float16: fg.F16}
+
+
+class Quantised:
+    """Codes and scales of a quantised matrix of rows x cols."""
+
+    def __init__(self, rows: int, cols: int, device):
+        self.shape = (rows, cols)
+        self.ld = 16 * max(1, -(-cols // 32))
+        self.codes = torch.empty(rows, self.ld, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(fg.mxfp4_scales_size(rows, cols), dtype=torch.uint8, device=device)
+
+    @property
+    def args(self):
+        return self.codes, self.ld, self.scales
+
+
+class Mxfp4Layer:
+    """``weight`` (K x N) and ``bias`` (N floats, or None) stay the caller's; call ``update`` after
+    changing the weight.  The element type of weight, tokens and gradients is the weight's."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, relu: bool = True):
+        if weight.dtype not in _TYPES or weight.dim() != 2 or weight.stride(1) != 1:
+            raise ValueError("weight: a K x N matrix of float32, bfloat16 or float16, rows contiguous")
+        self.weight, self.bias, self.relu = weight, bias, relu
+        self.type = _TYPES[weight.dtype]
+        self.K, self.N = weight.shape
+        self.w_rows = Quantised(self.K, self.N, weight.device)
+        self.w_cols = Quantised(self.N, self.K, weight.device)
+        self._sized, self._spaces = {}, {}
+        self.update()
+
+    def update(self) -> None:
+        """Quantise the weight both ways."""
+        fg.mxfp4_quantize(self.type, self.K, self.N, self.weight, self.weight.stride(0), *self.w_rows.args,
+                          *self.w_cols.args)
+
+    def _buffers(self, M: int):
+        if M not in self._sized:
+            dev, K, N = self.weight.device, self.K, self.N
+            self._sized[M] = dict(
+                x_rows=Quantised(M, K, dev), x_cols=Quantised(K, M, dev), g_rows=Quantised(M, N, dev), g_cols=Quantised(N, M, dev),
+                workspace=torch.empty(fg.mxfp4_quantize_grad_workspace_size(M, N), dtype=torch.uint8, device=dev))
+        return self._sized[M]
+
+    def _tokens(self, x: torch.Tensor, cols: int):
+        if x.dtype != self.weight.dtype or x.dim() != 2 or x.shape[1] != cols or (x.shape[0] and x.stride(1) != 1):
+            raise ValueError("a matrix of %s with %d contiguous columns" % (self.weight.dtype, cols))
+        return x.shape[0], max(x.stride(0), cols)
+
+    def decode(self, x: torch.Tensor) -> torch.Tensor:
+        """Y for tokens x (M x K): quantised on the way, nothing kept."""
+        M, ldx = self._tokens(x, self.K)
+        y = torch.empty(M, self.N, dtype=x.dtype, device=x.device)
+        need = fg.mxfp4_linear_workspace_size(M, self.N, self.K)  # 0 for a few tokens
+        if need and M not in self._spaces:
+            self._spaces[M] = torch.empty(need, dtype=torch.uint8, device=x.device)
+        fg.mxfp4_linear(self.type, M, self.N, self.K, x, ldx, *self.w_cols.args, self.bias, self.relu, y, self.N,
+                        self._spaces.get(M) if need else None, need)
+        return y
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        """Y for tokens x (M x K), which stay quantised both ways for ``backward``."""
+        M, ldx = self._tokens(x, self.K)
+        y = torch.empty(M, self.N, dtype=x.dtype, device=x.device)
+        if M:
+            b = self._buffers(M)
+            fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *b["x_rows"].args, *b["x_cols"].args)
+            fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *b["x_rows"].args, *self.w_cols.args, 0.0, y, self.N, self.bias,
+                          self.relu)
+        return y
+
+    def backward(self, g: torch.Tensor, y: torch.Tensor):
+        """(dX, dW, db) for the gradient g of the output y of the last ``forward`` with as many tokens."""
+        M, ldg = self._tokens(g, self.N)
+        dev, dt = g.device, g.dtype
+        dx = torch.empty(M, self.K, dtype=dt, device=dev)
+        dw = torch.zeros(self.K, self.N, dtype=dt, device=dev) if M == 0 else torch.empty(self.K, self.N, dtype=dt, device=dev)
+        db = torch.empty(self.N, device=dev) if M else torch.zeros(self.N, device=dev)
+        if M:
+            b = self._buffers(M)
+            gate, ldy = (y, self._tokens(y, self.N)[1]) if self.relu else (None, 0)
+            ws = b["workspace"]
+            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, gate, ldy, *b["g_rows"].args, *b["g_cols"].args, db, ws, ws.numel())
+            fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *b["g_rows"].args, *self.w_rows.args, 0.0, dx, self.K)
+            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *b["x_cols"].args, *b["g_cols"].args, 0.0, dw, self.N)
+        return dx, dw, db
+
+
+def main(steps: int = 60, M: int = 512, K: int = 256, N: int = 384) -> list[float]:
+    """Fit a layer to another one's outputs; prints and returns the losses."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    target_w, target_b = rand(K, N) / K**0.5, 0.1 * rand(N)
+    w, b = rand(K, N) / K**0.5, torch.zeros(N, device="cuda")
+    layer, losses = Mxfp4Layer(w, b), []
+    for step in range(steps):
+        x = rand(M, K)
+        want = (x @ target_w + target_b).clamp(min=0)
+        y = layer.forward(x)
+        diff = y - want
+        losses.append(float(diff.square().mean()))
+        _, dw, db = layer.backward(diff * (2.0 / M), y)
+        w -= 0.25 * dw
+        b -= 0.25 * db
+        layer.update()
+        if step % 10 == 0 or step + 1 == steps:
+            print("step %d: loss %.4f" % (step, losses[-1]))
+    x = rand(3, K)
+    print("three tokens through decode: largest difference from forward %.2g"
+          % float((layer.decode(x) - layer.forward(x)).abs().max()))
+    return losses
+
+
+if __name__ == "__main__":
+    main()

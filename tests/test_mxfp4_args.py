@@ -170,3 +170,22 @@ def test_definition_by_hand():
     assert s.tolist() == [[255, 125]] and code[0, :32].max() == 0 and code[0, 32] == 6
     v = ref.values(code, s)
     assert np.isnan(v[0, :32]).all() and (v[0, 32:] == 1).all()
+
+
+def test_calls_convert_what_they_are_given():
+    # NULL for None and 0, a truth value for the ReLU, floats or whole numbers for alpha and beta
+    assert _gemm(M=0, alpha=1, beta=0, bias=0, apply_relu=1) == OK
+    assert _gemm(A_codes=0) == INVALID
+    assert _quantize(M=0, stream=1) == OK
+    for wrong in (dict(M=2**40), dict(ldx="40"), dict(M=1.5)):
+        with pytest.raises((TypeError, OverflowError)):
+            _quantize(**wrong)
+    with pytest.raises(TypeError):
+        _quantize(X=object())
+    with pytest.raises(TypeError):
+        _gemm(alpha="1")
+    with pytest.raises((TypeError, OverflowError)):
+        _linear(workspace_bytes=-1)
+    with pytest.raises(fg.FgemmError) as e:
+        fg.mxfp4_dequantize(fg.F32, -1, 5, FAKE, 16, FAKE, FAKE, 5)
+    assert e.value.status == INVALID
