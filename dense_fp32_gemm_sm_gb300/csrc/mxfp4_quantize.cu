@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *partial, in
 }
 
 // Values from codes, 16 bytes of them a lane: a warp writes 512 consecutive bytes of a row.
-// Bound by the writes.  VEC: X allows 16-byte stores; otherwise a lane's elements are 32 apart,
+// Bound by the writes, which go past L2's other contents (__stcs: 8192 x 11008 FP32 69 -> 65 us,
+// 0.93 of the measured copy rate; BF16 44 -> 39, 0.86).  VEC: X allows 16-byte stores; otherwise a lane's elements are 32 apart,
 // so that each store of a warp still falls on consecutive addresses.
 template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
                 for (int e = 0; e < V; ++e) v[e] = from_float<T>(x[e] * f);
                 T *const dst = static_cast<T *>(p.x) + r * p.ldx + k;
                 if (k + V <= p.N) {
-                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(v);
+                    __stcs(reinterpret_cast<uint4 *>(dst), *reinterpret_cast<const uint4 *>(v));
                 } else {
 #pragma unroll
                     for (int e = 0; e < V; ++e)
@@ -624,7 +625,8 @@ fgemm_status run_dequantize(const DequantParams &p, cudaStream_t stream)
         return FGEMM_ERR_LAUNCH;
     }
     constexpr int SPAN = 512 / (int)sizeof(T);
-    const long long spans = ((long long)p.N + SPAN - 1) / SPAN, groups = ((long long)p.M + 31) / 32;
+    constexpr int ROWS = sizeof(T) == 2 ? 8 : 4;  // a warp: 4 KB or 2 KB of X in flight
+    const long long spans = ((long long)p.N + SPAN - 1) / SPAN, groups = ((long long)p.M + 8 * ROWS - 1) / (8 * ROWS);
     const bool vec = aligned_to(p.x, p.ldx * (long long)sizeof(T), 16);
     cudaError_t e;
     // Few rows of work: one a warp, over more CTAs.
@@ -633,8 +635,8 @@ fgemm_status run_dequantize(const DequantParams &p, cudaStream_t stream)
         e = vec ? launch(dequantize_kernel<T, true, 1>, grid, 256, 0, stream, 1, p)
                 : launch(dequantize_kernel<T, false, 1>, grid, 256, 0, stream, 1, p);
     } else {
-        const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(groups, 65535));
-        e = vec ? launch(dequantize_kernel<T, true, 4>, grid, 256, 0, stream, 1, p)
+        const dim3 grid((unsigned)spans, (unsigned)std::min<long long>(vec ? groups : ((long long)p.M + 31) / 32, 65535));
+        e = vec ? launch(dequantize_kernel<T, true, ROWS>, grid, 256, 0, stream, 1, p)
                 : launch(dequantize_kernel<T, false, 4>, grid, 256, 0, stream, 1, p);
     }
     return e == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH;
