@@ -121,12 +121,13 @@ bool linear_fused(long long M, long long K)
 
 int linear_ranks(long long N, long long K, int sms)
 {
-    // As many ranks as two CTAs an SM allow: they divide the quantising too.  (A cluster of
-    // eight costs more than it saves, and is for a K whose tokens need their shared memory.)
+    // Up to four ranks as two CTAs an SM allow: they divide the quantising too (one token through
+    // 4096 x 11008 took 8.5, 7.8, 7.5 and 10.7 us with 1, 2, 3 and 4).  A cluster of eight costs
+    // more than it saves, and is for a K whose tokens need its shared memory.
     const long long stages = (blocks_of(K) + 7) / 8, tiles = (N + 127) / 128;
     int ranks = 1;
-    while (ranks < 8 && 2 * ranks <= stages && (stages > ranks * FUSED_STAGES || (ranks < 4 && 2 * ranks * tiles <= 2 * sms)))
-        ranks *= 2;
+    while (ranks < 4 && ranks < stages && (ranks + 1) * tiles <= 2 * sms) ++ranks;
+    while (ranks < 8 && stages > ranks * FUSED_STAGES) ++ranks;
     return ranks;
 }
 
