@@ -582,8 +582,10 @@ fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int
         }
         ready.store(current_context_id(), std::memory_order_release);
     }
-    const dim3 grid((unsigned)std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms));
-    return launch(quantize_kernel<T, GATED, ELEMENTS>, grid, L::THREADS, smem, stream, 1, p, mode) == cudaSuccess
+    const long long ctas = std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms);
+    // (Stages that no tile of a CTA reaches are left out: the next kernel finds room beside this one.)
+    const size_t used = (size_t)std::min<long long>(smem, (tiles + ctas - 1) / ctas * L::TILE_BYTES);
+    return launch(quantize_kernel<T, GATED, ELEMENTS>, dim3((unsigned)ctas), L::THREADS, used, stream, 1, p, mode) == cudaSuccess
                ? FGEMM_OK
                : FGEMM_ERR_LAUNCH;
 }

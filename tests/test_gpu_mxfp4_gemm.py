@@ -250,6 +250,13 @@ def test_linear_types(t, M, N, K, pad):
     assert not outside(*linear(t, M, N, K, bias=M != 4, pad=pad, seed=9)).any()
 
 
+@pytest.mark.parametrize("M,K", [(1, 30000), (4, 43008), (4, 43009), (2, 60001)])
+def test_linear_long_sums(M, K):
+    # quantised tokens of up to 168 stages of 256 fit in a cluster's shared memory
+    assert (fg.mxfp4_linear_workspace_size(M, 200, K) == 0) == (K <= 43008)
+    assert not outside(*linear("f32", M, 200, K, seed=K)).any()
+
+
 @pytest.mark.parametrize("M", [1, 3, 40, 200])
 def test_linear_without_anything_to_sum(M):
     y = torch.full((M, 9), float("nan"), device="cuda")

@@ -235,6 +235,40 @@ def test_on_another_stream_after_its_producer():
     assert (r.codes == 0x66).all() and set(r.scales[:-16].unique().tolist()) == {129, 0}
 
 
+@pytest.mark.parametrize("M,N", [(5_000_001, 3), (2, 4_000_033)])
+def test_very_tall_and_very_wide(M, N):
+    # more rows than a grid dimension holds CTAs, and as many columns; every row (or column of
+    # 32) repeats one of a few
+    rng = np.random.default_rng(9)
+    if M > N:
+        pool = draw(rng, 64, N)  # (a column's blocks repeat every 64 rows)
+        x = torch.from_numpy(pool).float().cuda()[torch.arange(M, device="cuda") % 64]
+        r, c = Quantised(M, N), Quantised(N, M)
+        fg.mxfp4_quantize(fg.F32, M, N, x, N, r.codes, r.ld, r.scales, c.codes, c.ld, c.scales)
+        back, back_t = torch.empty_like(x), torch.empty(N, M, device="cuda")
+        fg.mxfp4_dequantize(fg.F32, M, N, r.codes, r.ld, r.scales, back, N)
+        fg.mxfp4_dequantize(fg.F32, N, M, c.codes, c.ld, c.scales, back_t, M)
+        pool = x[:64].double().cpu().numpy()
+        want = torch.from_numpy(ref.through(pool)).float().cuda()
+        assert torch.equal(back, want[torch.arange(M, device="cuda") % 64])
+        whole = torch.from_numpy(ref.through(np.concatenate([pool, pool[:M % 64]]).T)).float().cuda()
+        full = M // 64 * 64
+        assert torch.equal(back_t[:, :full].view(N, -1, 64), whole[:, None, :64].expand(N, full // 64, 64))
+        tail = torch.from_numpy(ref.through(pool[:M % 64].T)).float().cuda()
+        assert torch.equal(back_t[:, full:], tail)
+    else:
+        _, ptr, ld, x = hold = on_gpu(draw(rng, M, N), torch.float32)
+        r, c = Quantised(M, N), Quantised(N, M)
+        fg.mxfp4_quantize(fg.F32, M, N, ptr, ld, r.codes, r.ld, r.scales, c.codes, c.ld, c.scales)
+        torch.cuda.synchronize()
+        r.check(x)
+        back = torch.empty(N, M, device="cuda")
+        fg.mxfp4_dequantize(fg.F32, N, M, c.codes, c.ld, c.scales, back, M)
+        pick = rng.integers(0, N, 2000)
+        assert np.array_equal(back.cpu().numpy()[pick], ref.through(x.T[pick]))
+        del hold
+
+
 def test_offsets_beyond_32_bits():
     # more than 2^31 elements, and codes at byte offsets beyond 2^31
     M, N = 2**31 // 8192 + 129, 16384
