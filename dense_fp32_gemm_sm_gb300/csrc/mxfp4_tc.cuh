@@ -493,12 +493,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
         for (long long t = first_tile; t < tiles; t += tile_step, ++j) {
             int x0, w0;
             tile_at(t, x0, w0);
-            const int acc = j & 1;
-            if (!tc::mbar_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
+            const int acc = j & 1, n = w0 + 32 * q + lane;
+            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;  // (on its way during the wait)
+            if (!warp_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
             tc::tc_fence_after();
             const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NT);
-            const int n = w0 + 32 * q + lane;
-            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
             T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
             // (N even: a pair is inside or outside as a whole)
             const bool pairs = p.c_pairs && (p.N & 1) == 0;
@@ -811,12 +810,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (long long t = first_tile; t < tiles; t += tile_step, ++j) {
             int x0, w0;
             tile_at(t, x0, w0);
-            const int acc = j & 1;
+            const int acc = j & 1, n = w0 + 128 * rank + 32 * q + lane;
+            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;  // (on its way during the wait)
             if (!warp_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
             tc::tc_fence_after();
             const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::ACC_STEP);
-            const int n = w0 + 128 * rank + 32 * q + lane;
-            const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
             T *const out = static_cast<T *>(p.c) + (long long)x0 * p.ldc + n;
 #pragma unroll 1
             for (int i = set; i < NT / 32; i += 2) {
