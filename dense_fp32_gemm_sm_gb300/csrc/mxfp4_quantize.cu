@@ -182,7 +182,7 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
 // CTAs; while a tile is worked on, the next two are copied.
 // ELEMENTS: mode is COPY_ELEMENTS (an instance of its own, for the registers that its loads take).
 template <class T, bool GATED, bool ELEMENTS>
-__global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantShape<sizeof(T), GATED>::CTAS_PER_SM)
+__global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T), GATED>::CTAS_PER_SM)
     quantize_kernel(const QuantParams p, int mode)
 {
     using L = QuantShape<sizeof(T), GATED>;
@@ -233,10 +233,24 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // The gate of this thread's own 16-byte pieces of tile w.
+    // This thread's elements one by one: a column's, OWN_STEP rows apart.
+    constexpr int OWN = TILE * TILE / L::THREADS, OWN_STEP = L::THREADS / TILE;
+    [[maybe_unused]] const int own_row = t / TILE, own_col = t % TILE;
+    // The gate of this thread's own 16-byte pieces of tile w ...
     uint4 gate[GATED && !ELEMENTS ? L::CHUNKS : 1];
     auto fetch_gate = [&](long long w) {
-        if (!GATED || ELEMENTS || w >= tiles || mode != COPY_16) return;
+        if (!GATED || ELEMENTS || w >= tiles) return;
+        if (mode == COPY_4) {
+            // ... or of its own elements, in words of one or two.
+            const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
+            const int rows = c0 + own_col < p.N ? (int)min((long long)TILE, p.M - r0) : 0;
+            const T *src = Y + (r0 + own_row) * p.ldgate + c0 + own_col;
+            T *const to = reinterpret_cast<T *>(gate);
+#pragma unroll
+            for (int j = 0; j < OWN; ++j, src += OWN_STEP * p.ldgate)
+                to[j] = own_row + j * OWN_STEP < rows ? __ldcs(src) : from_float<T>(0.0f);
+            return;
+        }
         const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
         if (r0 + TILE <= p.M && c0 + TILE <= p.N) {
             const T *src = Y + (r0 + t / L::CHUNKS_PER_ROW) * p.ldgate + c0 + t % L::CHUNKS_PER_ROW * V;
@@ -260,6 +274,18 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
         }
     };
 
+    // Elements through registers: a tile's are loaded while the one before is worked on.
+    T ahead[ELEMENTS && !GATED ? OWN : 1];
+    [[maybe_unused]] auto load_ahead = [&](long long w) {
+        if (w >= tiles) return;
+        const long long tm = w / tiles_n, r0 = tm * TILE, c0 = (w - tm * tiles_n) * TILE;
+        const int rows = c0 + own_col < p.N ? (int)min((long long)TILE, p.M - r0) : 0;
+        const T *src = X + (r0 + own_row) * p.ldx + c0 + own_col;
+#pragma unroll
+        for (int j = 0; j < OWN; ++j, src += OWN_STEP * p.ldx)
+            ahead[j] = own_row + j * OWN_STEP < rows ? *src : from_float<T>(0.0f);
+    };
+    if constexpr (ELEMENTS && !GATED) load_ahead(blockIdx.x);
     if constexpr (!ELEMENTS) {
         for (int s = 0; s + 1 < L::STAGES; ++s) start(blockIdx.x + (long long)s * gridDim.x, s);
         fetch_gate(blockIdx.x);
@@ -269,14 +295,14 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
         const long long tm = w / tiles_n, tn = w - tm * tiles_n;
         const long long r0 = tm * TILE, c0 = tn * TILE;
         uint8_t *const tile = smem + stage * L::TILE_BYTES;
-        // This thread's elements one by one: a column's, OWN_STEP rows apart.
-        constexpr int OWN = TILE * TILE / L::THREADS, OWN_STEP = L::THREADS / TILE;
-        [[maybe_unused]] const int own_row = t / TILE, own_col = t % TILE;
         [[maybe_unused]] const int own_rows = c0 + own_col < p.N ? (int)min((long long)TILE, p.M - r0) : 0;
-        [[maybe_unused]] uint32_t open[OWN / 32];  // COPY_4: gates of this thread's elements
-        if constexpr (ELEMENTS) {
+        if constexpr (ELEMENTS && !GATED) {
+            // Two stages: what the previous round loaded is written behind the reads of the tile before.
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) *reinterpret_cast<T *>(tile + element_at<ES>(own_row + j * OWN_STEP, own_col)) = ahead[j];
+        } else if constexpr (ELEMENTS) {
             __syncthreads();  // the previous tile has been read (one stage)
-            constexpr int BATCH = GATED ? 16 : 32;  // loads in flight
+            constexpr int BATCH = 16;  // loads in flight
             const T *src = X + (r0 + own_row) * p.ldx + c0 + own_col;
             const T *gsrc = GATED ? Y + (r0 + own_row) * p.ldgate + c0 + own_col : nullptr;
             for (int j = 0; j < OWN; j += BATCH) {
@@ -297,22 +323,6 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
                     *reinterpret_cast<T *>(tile + element_at<ES>(own_row + (j + i) * OWN_STEP, own_col)) = e[i];
             }
         } else {
-            // (The gates, a bit an element, while the copies are on their way.)
-            if constexpr (GATED) {
-                if (mode == COPY_4) {
-                    const T *gsrc = Y + (r0 + own_row) * p.ldgate + c0 + own_col;
-#pragma unroll
-                    for (int h = 0; h < OWN / 32; ++h) {
-                        T y[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i, gsrc += OWN_STEP * p.ldgate)
-                            y[i] = own_row + (32 * h + i) * OWN_STEP < own_rows ? *gsrc : from_float<T>(0.0f);
-                        open[h] = 0;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) open[h] |= (uint32_t)(to_float(y[i]) > 0.0f) << i;
-                    }
-                }
-            }
             // This tile's copies are this thread's oldest group; at most stages - 2 follow it.
             if (L::STAGES == 3)
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -342,11 +352,12 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < OWN; ++j)
-                    if (!(open[j / 32] >> (j % 32) & 1u))
+                    if (!(to_float(reinterpret_cast<const T *>(gate)[j]) > 0.0f))
                         *reinterpret_cast<T *>(tile + element_at<ES>(own_row + j * OWN_STEP, own_col)) = from_float<T>(0.0f);
             }
         }
         __syncthreads();
+        if constexpr (ELEMENTS && !GATED) load_ahead(w + gridDim.x);
         if constexpr (!ELEMENTS) {
             // Into the stage that the previous tile has left (the barrier above: all have read it).
             start(w + (L::STAGES - 1ll) * gridDim.x, stage == 0 ? L::STAGES - 1 : stage - 1);
@@ -451,6 +462,7 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, QuantSh
             }
         }
         if constexpr (!ELEMENTS) stage = stage + 1 == L::STAGES ? 0 : stage + 1;
+        if constexpr (ELEMENTS && !GATED) stage ^= 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -480,10 +492,18 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *partial, in
     }
 }
 
+// Elements of row r before X comes to a multiple of 16 bytes.
+template <class T>
+__device__ __forceinline__ int head_of(const DequantParams &p, long long r)
+{
+    return (int)((16u - ((uint32_t)reinterpret_cast<uintptr_t>(static_cast<const T *>(p.x) + r * p.ldx) & 15u)) & 15u) /
+           (int)sizeof(T);
+}
+
 // Values from codes, 16 bytes of them a lane: a warp writes 512 consecutive bytes of a row.
 // Bound by the writes, which go past L2's other contents (__stcs: 8192 x 11008 FP32 69 -> 65 us,
-// 0.93 of the measured copy rate; BF16 44 -> 39, 0.86).  VEC: X allows 16-byte stores; otherwise a lane's elements are 32 apart,
-// so that each store of a warp still falls on consecutive addresses.
+// 0.93 of the measured copy rate; BF16 44 -> 39, 0.86).  VEC: all rows of X start on
+// 16 bytes.
 template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
 {
@@ -525,7 +545,10 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
                         if (k + e < p.N) dst[e] = v[e];
                 }
             }
-        } else {
+        } else if constexpr (V == 4) {
+            // FP32 rows that start anywhere: a lane's elements are 32 apart, so that each store of a
+            // warp falls on consecutive addresses.  (Shifted 16-byte stores as below measured
+            // 39 us at 4096 x 4096, this 24: the shifts cost more than four times the stores.)
             const uint8_t *const scales = p.scales + k0 / 128 * ATOM_BYTES;
             uint32_t c[ROWS][V], s[ROWS][V];
 #pragma unroll
@@ -537,7 +560,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
                 for (int e = 0; e < V; ++e)
                     if (k0 + 32 * e + lane < p.N) {
                         c[i][e] = src[16 * e];
-                        s[i][e] = sr[e / 4 * ATOM_BYTES + e % 4];
+                        s[i][e] = sr[e];
                     }
             }
 #pragma unroll
@@ -551,6 +574,54 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantParams p)
                         const float2 x = decode2(c[i][e]);  // (the element is odd where the lane is)
                         dst[32 * e] = from_float<T>((lane & 1 ? x.y : x.x) * scale_value(s[i][e]));
                     }
+            }
+        } else {
+            // 16-bit rows that start anywhere: a lane's 16 bytes start `head` elements further, where a
+            // row of X has come to a multiple of 16 bytes, at any nibble and in up to two blocks.
+            const int left = (int)min((long long)SPAN + 8, p.N - k0);  // elements of a row from k0 on
+            const int words = (left + 31) / 32 * 4;                     // and words of their codes
+            uint32_t lo[ROWS], hi[ROWS], s0[ROWS], s1[ROWS];
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const long long r = r0 + 8 * i;
+                if (r >= p.M) break;
+                const int k = head_of<T>(p, r) + lane * V, b0 = k / 32, b1 = (k + V - 1) / 32;
+                lo[i] = hi[i] = s0[i] = s1[i] = 0;
+                if (k < left) {
+                    const uint32_t *const src = reinterpret_cast<const uint32_t *>(p.codes + r * p.ld + k0 / 2) + k / 8;
+                    const uint8_t *const sr = p.scales + k0 / 128 * ATOM_BYTES + scale_offset(r, 0, atoms);
+                    lo[i] = src[0];
+                    s0[i] = sr[b0 / 4 * ATOM_BYTES + b0 % 4];
+                    if (k / 8 + 1 < words) hi[i] = src[1];
+                    if (32 * b1 < left) s1[i] = sr[b1 / 4 * ATOM_BYTES + b1 % 4];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const long long r = r0 + 8 * i;
+                if (r >= p.M) break;
+                const int head = head_of<T>(p, r), k = head + lane * V;
+                T *const row = static_cast<T *>(p.x) + r * p.ldx + k0;
+                if (k < left) {
+                    float x[8];
+                    decode8(__funnelshift_r(lo[i], hi[i], 4 * (k & 7)), x);
+                    const int first = 32 - (k & 31);  // elements before the second block
+                    const float f0 = scale_value(s0[i]), f1 = scale_value(s1[i]);
+                    T v[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] = from_float<T>(x[e] * (e < first ? f0 : f1));
+                    if (k + V <= left) {
+                        __stcs(reinterpret_cast<uint4 *>(row + k), *reinterpret_cast<const uint4 *>(v));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            if (k + e < left) row[k + e] = v[e];
+                    }
+                }
+                if (k0 == 0 && lane < head && lane < p.N) {  // the elements before that
+                    const float2 x = decode2((p.codes + r * p.ld)[lane / 2]);
+                    row[lane] = from_float<T>((lane & 1 ? x.y : x.x) * scale_value(p.scales[scale_offset(r, 0, atoms)]));
+                }
             }
         }
     }
@@ -566,7 +637,7 @@ fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int
 {
     using L = QuantShape<sizeof(T), GATED>;
     static std::atomic<unsigned long long> ready_ctx[64];
-    constexpr int smem = ELEMENTS ? L::TILE_BYTES : L::SMEM_BYTES;
+    constexpr int smem = !ELEMENTS ? L::SMEM_BYTES : GATED ? L::TILE_BYTES : 2 * L::TILE_BYTES;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -582,7 +653,7 @@ fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int
         }
         ready.store(current_context_id(), std::memory_order_release);
     }
-    const long long ctas = std::min<long long>(tiles, (long long)L::CTAS_PER_SM * sms);
+    const long long ctas = std::min<long long>(tiles, (ELEMENTS ? 2ll : (long long)L::CTAS_PER_SM) * sms);
     // (Stages that no tile of a CTA reaches are left out: the next kernel finds room beside this one.)
     const size_t used = (size_t)std::min<long long>(smem, (tiles + ctas - 1) / ctas * L::TILE_BYTES);
     return launch(quantize_kernel<T, GATED, ELEMENTS>, dim3((unsigned)ctas), L::THREADS, used, stream, 1, p, mode) == cudaSuccess
