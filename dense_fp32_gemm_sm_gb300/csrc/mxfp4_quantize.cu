@@ -20,11 +20,15 @@ constexpr int TILE = 128;  // a tile is 128 x 128: one scale atom in each direct
 
 // The kernel's shape by element size.  A thread takes one block of a row and one of a column
 // (FP32), or two blocks of rows and the same block of two neighbouring columns (16 bits).
-template <int ES, bool GATED>
+template <int ES>
 struct QuantShape {
     static constexpr int THREADS = ES == 4 ? 512 : 256;
-    static constexpr int CTAS_PER_SM = ES == 4 ? 1 : GATED ? 2 : 3;  // (a gate's pieces wait in 32 registers)
-    static constexpr int STAGES = ES == 4 || GATED ? 3 : 2;          // 192 KB an SM in all
+    static constexpr int CTAS_PER_SM = ES == 4 ? 1 : 3;
+    static constexpr int STAGES = ES == 4 ? 3 : 2;  // 192 KB an SM in both
+    // FP32: the gates of a tile come while the one before is worked on, in 32 registers; 16 bits:
+    // while its own copies arrive, and three CTAs an SM fit (8192 x 11008 BF16: 91 -> 88 us,
+    // 2048 x 11008 31 -> 27; FP32 8192 x 4096 would go from 58 to 65).
+    static constexpr bool GATES_AHEAD = ES == 4;
     static constexpr int TILE_BYTES = TILE * TILE * ES;
     static constexpr int SMEM_BYTES = STAGES * TILE_BYTES;
     static constexpr int CHUNKS_PER_ROW = TILE * ES / 16;
@@ -182,10 +186,10 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
 // CTAs; while a tile is worked on, the next two are copied.
 // ELEMENTS: mode is COPY_ELEMENTS (an instance of its own, for the registers that its loads take).
 template <class T, bool GATED, bool ELEMENTS>
-__global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T), GATED>::CTAS_PER_SM)
+__global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T)>::CTAS_PER_SM)
     quantize_kernel(const QuantParams p, int mode)
 {
-    using L = QuantShape<sizeof(T), GATED>;
+    using L = QuantShape<sizeof(T)>;
     constexpr int ES = (int)sizeof(T), V = 16 / ES;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENT
     if constexpr (ELEMENTS && !GATED) load_ahead(blockIdx.x);
     if constexpr (!ELEMENTS) {
         for (int s = 0; s + 1 < L::STAGES; ++s) start(blockIdx.x + (long long)s * gridDim.x, s);
-        fetch_gate(blockIdx.x);
+        if constexpr (L::GATES_AHEAD) fetch_gate(blockIdx.x);
     }
     int stage = 0;
     for (long long w = blockIdx.x; w < tiles; w += gridDim.x) {
@@ -296,6 +300,7 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENT
         const long long r0 = tm * TILE, c0 = tn * TILE;
         uint8_t *const tile = smem + stage * L::TILE_BYTES;
         [[maybe_unused]] const int own_rows = c0 + own_col < p.N ? (int)min((long long)TILE, p.M - r0) : 0;
+        if constexpr (!L::GATES_AHEAD) fetch_gate(w);
         if constexpr (ELEMENTS && !GATED) {
             // Two stages: what the previous round loaded is written behind the reads of the tile before.
 #pragma unroll
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENT
         if constexpr (!ELEMENTS) {
             // Into the stage that the previous tile has left (the barrier above: all have read it).
             start(w + (L::STAGES - 1ll) * gridDim.x, stage == 0 ? L::STAGES - 1 : stage - 1);
-            fetch_gate(w + gridDim.x);
+            if constexpr (L::GATES_AHEAD) fetch_gate(w + gridDim.x);
         }
 
         if (p.row_codes) {
@@ -635,7 +640,7 @@ bool aligned_to(const void *ptr, long long ld_bytes, int to)
 template <class T, bool GATED, bool ELEMENTS>
 fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int sms, cudaStream_t stream)
 {
-    using L = QuantShape<sizeof(T), GATED>;
+    using L = QuantShape<sizeof(T)>;
     static std::atomic<unsigned long long> ready_ctx[64];
     constexpr int smem = !ELEMENTS ? L::SMEM_BYTES : GATED ? L::TILE_BYTES : 2 * L::TILE_BYTES;
     int dev = 0;
