@@ -65,7 +65,7 @@ fgemm_status run_gemm(const GemmArgs &g, cudaStream_t stream)
 
 // Estimated microseconds of the ways a product can run, fitted to measurements on one GB300 (30
 // shapes from 96 x 300 x 2000 to 8192 x 11008 x 4096, FP32 and BF16: the way with the least
-// estimate took 0.3 % longer than the fastest on average, 8 % at most).  Tiles over CTAs (or
+// estimate took 0.3 % longer than the fastest on average, 10 % at most).  Tiles over CTAs (or
 // pairs) come in rounds, each of so many stages and a boundary; C is written beside them.
 static double rounds(long long M, long long tile_m, long long N, long long tile_n, long long units)
 {

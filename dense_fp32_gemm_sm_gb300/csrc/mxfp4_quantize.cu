@@ -20,11 +20,12 @@ constexpr int TILE = 128;  // a tile is 128 x 128: one scale atom in each direct
 
 // The kernel's shape by element size.  A thread takes one block of a row and one of a column
 // (FP32), or two blocks of rows and the same block of two neighbouring columns (16 bits).
-template <int ES>
+template <int ES, bool GATED>
 struct QuantShape {
     static constexpr int THREADS = ES == 4 ? 512 : 256;
     static constexpr int CTAS_PER_SM = ES == 4 ? 1 : 3;
-    static constexpr int STAGES = ES == 4 ? 3 : 2;  // 192 KB an SM in both
+    // 192 KB an SM; gated FP32 128, as the gates' loads want room in L1 (8192 x 4096: 58 -> 56 us).
+    static constexpr int STAGES = ES == 4 && !GATED ? 3 : 2;
     // FP32: the gates of a tile come while the one before is worked on, in 32 registers; 16 bits:
     // while its own copies arrive, and three CTAs an SM fit (8192 x 11008 BF16: 91 -> 88 us,
     // 2048 x 11008 31 -> 27; FP32 8192 x 4096 would go from 58 to 65).
@@ -186,10 +187,10 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
 // CTAs; while a tile is worked on, the next two are copied.
 // ELEMENTS: mode is COPY_ELEMENTS (an instance of its own, for the registers that its loads take).
 template <class T, bool GATED, bool ELEMENTS>
-__global__ void __launch_bounds__(QuantShape<sizeof(T)>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T)>::CTAS_PER_SM)
+__global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T), GATED>::CTAS_PER_SM)
     quantize_kernel(const QuantParams p, int mode)
 {
-    using L = QuantShape<sizeof(T)>;
+    using L = QuantShape<sizeof(T), GATED>;
     constexpr int ES = (int)sizeof(T), V = 16 / ES;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -640,7 +641,7 @@ bool aligned_to(const void *ptr, long long ld_bytes, int to)
 template <class T, bool GATED, bool ELEMENTS>
 fgemm_status start_quantize(const QuantParams &p, int mode, long long tiles, int sms, cudaStream_t stream)
 {
-    using L = QuantShape<sizeof(T)>;
+    using L = QuantShape<sizeof(T), GATED>;
     static std::atomic<unsigned long long> ready_ctx[64];
     constexpr int smem = !ELEMENTS ? L::SMEM_BYTES : GATED ? L::TILE_BYTES : 2 * L::TILE_BYTES;
     int dev = 0;
