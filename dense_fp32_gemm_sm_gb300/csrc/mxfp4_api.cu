@@ -46,6 +46,11 @@ size_t scales_bytes(long long rows, long long cols)
 
 size_t round256(size_t n) { return sat_add(n, 255) / 256 * 256; }
 
+// The layer's quantised tokens: rows of whole blocks, and where there are many, rows that start on
+// 64 bytes, as the product reads them faster (4096 x 4096 x 4000 with both operands' rows on
+// 16: 36 us, on 64: 27; 32 x 4096 x 11000: 7.2 both ways).
+long long tokens_ld(long long M, long long K) { return M > 64 ? 64 * ((K + 127) / 128) : 16 * blocks_of(K); }
+
 struct Direction {
     void *codes;
     int ld;
@@ -210,7 +215,7 @@ int fgemm_mxfp4_plan(fgemm_dtype type, int M, int N, int K, int num_sms)
 size_t fgemm_mxfp4_linear_workspace_size(int M, int N, int K)
 {
     if (M < 1 || N < 1 || K < 1 || linear_fused(M, K)) return 0;
-    return sat_add(round256(codes_bytes(M, K)), scales_bytes(M, K));
+    return sat_add(round256(sat_mul((size_t)M, (size_t)tokens_ld(M, K))), scales_bytes(M, K));
 }
 
 fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const void *X, int ldx,
@@ -243,8 +248,8 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
     if (K == 0) return launch_gemm(type, g, stream);
     if (linear_fused(M, K)) return launch_linear(type, X, ldx, g, stream);
     uint8_t *const codes = static_cast<uint8_t *>(workspace);
-    uint8_t *const scales = codes + round256(codes_bytes(M, K));
-    const int ld = (int)(16 * blocks_of(K));
+    const int ld = (int)tokens_ld(M, K);
+    uint8_t *const scales = codes + round256((size_t)M * (size_t)ld);
     const fgemm_status st = launch_quantize(
         type, quant_params(M, K, X, ldx, Direction{codes, ld, scales}, Direction{nullptr, 0, nullptr}), stream);
     if (st != FGEMM_OK) return st;

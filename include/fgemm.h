@@ -439,7 +439,8 @@ fgemm_status fgemm_gemm_explicit(int config, fgemm_op transa, fgemm_op transb, i
  *   codes:  row r starts at byte r * ld; element k is in byte k/2 of the row, the low
  *           nibble for even k.  ld (bytes) is a multiple of 16 and at least
  *           16 * ceil(L/32); the pointer is 16-byte aligned.  A row is written up to
- *           byte 16 * ceil(L/32); the codes beyond L are 0.
+ *           byte 16 * ceil(L/32); the codes beyond L are 0.  Products read rows in pieces
+ *           of 128 bytes and are fastest with rows that start on 64 (pointer and ld).
  *   scales: with nb = ceil(L/32), the byte of row r and block b is at
  *           512 * ((r/128) * ceil(nb/4) + b/4) + 16 * (r%32) + 4 * ((r%128)/32) + b%4:
  *           atoms of 128 rows x 4 blocks, as the tensor cores take them.  16-byte
