@@ -76,3 +76,20 @@ def test_training_lowers_the_loss():
     losses = mxfp4_layer.main(steps=60)
     # (4-bit gradients do not vanish at the optimum, so it does not reach 0)
     assert losses[-1] < 0.25 * losses[0]
+
+
+def test_decoding_on_two_streams_at_once():
+    from dense_fp32_gemm_sm_gb300.mxfp4_layer import Mxfp4Layer
+
+    layer = Mxfp4Layer(torch.randn(1000, 520, device="cuda"))
+    x = [torch.randn(40, 1000, device="cuda") for _ in range(2)]
+    want = [layer.decode(v) for v in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(50):
+        for s, v, out in zip(streams, x, got):
+            with torch.cuda.stream(s):
+                out.append(layer.decode(v))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for w, ys in zip(want, got) for y in ys)
