@@ -64,9 +64,13 @@ class Mxfp4Layer:
         return self._sized[M]
 
     def _tokens(self, x: torch.Tensor, cols: int):
+        """Rows and leading dimension of a matrix given to a call."""
         if x.dtype != self.weight.dtype or x.dim() != 2 or x.shape[1] != cols or (x.shape[0] and x.stride(1) != 1):
             raise ValueError("a matrix of %s with %d contiguous columns" % (self.weight.dtype, cols))
-        return x.shape[0], max(x.stride(0), cols)
+        M = x.shape[0]
+        if M > 1 and x.stride(0) < cols:  # expanded rows, windows: the kernels read rows of their own
+            raise ValueError("rows that overlap (row stride %d for %d columns): pass .contiguous()" % (x.stride(0), cols))
+        return M, max(x.stride(0) if M > 1 else cols, 1)
 
     def decode(self, x: torch.Tensor) -> torch.Tensor:
         """Y for tokens x (M x K): quantised on the way, nothing kept."""

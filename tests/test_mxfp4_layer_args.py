@@ -1,0 +1,55 @@
+"""What the MXFP4 layer refuses and passes on, without a GPU: its calls are replaced by ones that
+only look at their arguments, so that no bad argument ever reaches a kernel."""
+
+import pytest
+import torch
+
+from dense_fp32_gemm_sm_gb300 import mxfp4_layer
+from dense_fp32_gemm_sm_gb300.mxfp4_layer import Mxfp4Layer
+
+K, N = 64, 32
+
+
+class Calls(list):
+    """(name, arguments) of the calls made, in order."""
+
+    def named(self, name):
+        return [args for n, args in self if n == name]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    made = Calls()
+    for name in ("quantize", "quantize_grad", "gemm", "linear"):
+        monkeypatch.setattr(mxfp4_layer.fg, "mxfp4_" + name, lambda *a, name=name: made.append((name, a)))
+    return made
+
+
+def overlapping(rows, cols):
+    """Matrices of rows x cols whose rows share elements: a row repeated, and a sliding window."""
+    row = torch.randn(cols)
+    return [row.expand(rows, cols), row[None].expand(rows, cols), torch.randn(rows + cols).as_strided((rows, cols), (1, 1)),
+            torch.randn(rows * cols).as_strided((rows, cols), (cols - 1, 1))]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_rows_that_overlap_are_refused(calls, which):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    x, g, y = overlapping(5, K)[which], overlapping(5, N)[which], torch.ones(5, N)
+    layer.forward(torch.randn(5, K))
+    del calls[:]
+    for call in (lambda: layer.forward(x), lambda: layer.decode(x), lambda: layer.backward(g, y),
+                 lambda: layer.backward(y, g)):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls
+
+
+def test_leading_dimensions(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    for x, ld in ((torch.randn(3, K), K), (torch.randn(3, K + 5)[:, :K], K + 5), (torch.randn(6, K)[::2], 2 * K),
+                  (torch.randn(K).expand(1, K), K)):
+        del calls[:]
+        layer.decode(x)
+        (args,) = calls.named("linear")
+        assert args[4] is x and args[5] == ld
