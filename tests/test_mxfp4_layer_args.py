@@ -53,3 +53,13 @@ def test_leading_dimensions(calls):
         layer.decode(x)
         (args,) = calls.named("linear")
         assert args[4] is x and args[5] == ld
+
+
+@pytest.mark.parametrize("rows", [0, 1, 4, 6])
+def test_backward_wants_as_many_outputs_as_gradients(calls, rows):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    layer.forward(torch.randn(5, K))
+    del calls[:]
+    with pytest.raises(ValueError):
+        layer.backward(torch.randn(5, N), torch.ones(rows, N))
+    assert not calls
