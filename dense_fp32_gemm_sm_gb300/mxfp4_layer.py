@@ -43,7 +43,7 @@ class Mxfp4Layer:
         if weight.dtype not in _TYPES or weight.dim() != 2 or weight.stride(1) != 1:
             raise ValueError("weight: a K x N matrix of float32, bfloat16 or float16, rows contiguous")
         if bias is not None and not (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32 and bias.is_contiguous()
-                                     and bias.shape == weight.shape[1:] and bias.device == weight.device):
+                                     and bias.numel() == weight.shape[1] and bias.device == weight.device):
             raise ValueError("bias: %d consecutive float32 on %s" % (weight.shape[1], weight.device))
         self.weight, self.bias, self.relu = weight, bias, relu
         self.type = _TYPES[weight.dtype]

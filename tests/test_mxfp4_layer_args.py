@@ -65,7 +65,7 @@ def test_backward_wants_as_many_outputs_as_gradients(calls, rows):
     assert not calls
 
 
-@pytest.mark.parametrize("bias", [torch.zeros(N - 1), torch.zeros(N + 1), torch.zeros(1, N), torch.zeros(N, 1), torch.zeros(2 * N)[::2],
+@pytest.mark.parametrize("bias", [torch.zeros(N - 1), torch.zeros(N + 1), torch.zeros(2 * N)[::2], torch.zeros(2, N), torch.zeros(N, 2)[:, :1],
                                   torch.zeros(1).expand(N), torch.zeros(N).double(), torch.zeros(N).half(),
                                   torch.zeros(N, device="meta"), [0.0] * N])
 def test_bias_is_n_consecutive_floats(calls, bias):
@@ -75,7 +75,7 @@ def test_bias_is_n_consecutive_floats(calls, bias):
 
 
 def test_a_good_bias_goes_to_the_calls(calls):
-    for b in (None, torch.zeros(N), torch.zeros(3, N)[1], torch.zeros(N, dtype=torch.float32)):
+    for b in (None, torch.zeros(N), torch.zeros(3, N)[1], torch.zeros(1, N), torch.zeros(N, 1)):
         layer = Mxfp4Layer(torch.randn(K, N).bfloat16(), b)
         del calls[:]
         layer.decode(torch.randn(2, K).bfloat16())
