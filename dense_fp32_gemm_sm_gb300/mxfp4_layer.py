@@ -102,6 +102,8 @@ class Mxfp4Layer:
         rows, ldy = self._tokens(y, self.N) if self.relu else (M, 0)
         if rows != M:  # y is read as the gate of every row of g
             raise ValueError("%d outputs for %d gradients" % (rows, M))
+        if M and M not in self._sized:  # there are no tokens to multiply the gradient with
+            raise ValueError("no forward with %d tokens before this backward" % M)
         dev, dt = g.device, g.dtype
         dx = torch.empty(M, self.K, dtype=dt, device=dev)
         dw = torch.zeros(self.K, self.N, dtype=dt, device=dev) if M == 0 else torch.empty(self.K, self.N, dtype=dt, device=dev)
@@ -109,7 +111,8 @@ class Mxfp4Layer:
         if M:
             b = self._buffers(M)
             ws = b["workspace"]
-            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *b["g_rows"].args, *b["g_cols"].args, db, ws, ws.numel())
+            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *b["g_rows"].args,
+                                   *b["g_cols"].args, db, ws, ws.numel())
             fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *b["g_rows"].args, *self.w_rows.args, 0.0, dx, self.K)
             fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *b["x_cols"].args, *b["g_cols"].args, 0.0, dw, self.N)
         return dx, dw, db

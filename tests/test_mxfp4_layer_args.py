@@ -80,3 +80,17 @@ def test_a_good_bias_goes_to_the_calls(calls):
         del calls[:]
         layer.decode(torch.randn(2, K).bfloat16())
         assert calls.named("linear")[0][9] is b
+
+
+def test_backward_without_its_forward_is_refused(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    del calls[:]
+    with pytest.raises(ValueError):
+        layer.backward(torch.randn(5, N), torch.ones(5, N))
+    y = layer.forward(torch.randn(5, K))
+    del calls[:]
+    with pytest.raises(ValueError):
+        layer.backward(torch.randn(4, N), y[:4])
+    assert not calls
+    layer.backward(torch.randn(5, N), y)
+    assert [name for name, _ in calls] == ["quantize_grad", "gemm", "gemm"]
