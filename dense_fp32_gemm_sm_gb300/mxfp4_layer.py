@@ -6,8 +6,8 @@ gradient of X; tokens X (M x K) along their rows forward and their columns for t
 of W; the output's gradient both ways behind ReLU's gate, with the bias's gradient.  A few
 tokens at a time go through ``decode``, which quantises them on the way.
 
-The buffers of ``forward`` and ``backward`` belong to the layer and are made for the sizes met, so those
-are used on one stream at a time.
+``forward`` and ``backward`` work in buffers of the layer (those of the last size met, and the tokens of
+a few forwards), so they are used on one stream at a time.
 ``python -m dense_fp32_gemm_sm_gb300.mxfp4_layer`` fits a small layer to another one's outputs.
 """
 
@@ -16,6 +16,8 @@ from __future__ import annotations
 import torch
 
 from . import _binding as fg
+
+SIZES = 4  # numbers of tokens whose last forward may wait for its backward
 
 _TYPES = {torch.float32: fg.F32, torch.bfloat16: fg.BF16, torch.float16: fg.F16}
 
@@ -50,7 +52,8 @@ class Mxfp4Layer:
         self.K, self.N = weight.shape
         self.w_rows = Quantised(self.K, self.N, weight.device)
         self.w_cols = Quantised(self.N, self.K, weight.device)
-        self._sized = {}
+        self._scratch = (0, {})  # rows, buffers of the last size met
+        self._tokens_of = {}     # rows -> the tokens that backward needs, the latest last
         self.update()
 
     def update(self) -> None:
@@ -58,13 +61,14 @@ class Mxfp4Layer:
         fg.mxfp4_quantize(self.type, self.K, self.N, self.weight, self.weight.stride(0), *self.w_rows.args,
                           *self.w_cols.args)
 
-    def _buffers(self, M: int):
-        if M not in self._sized:
-            dev, K, N = self.weight.device, self.K, self.N
-            self._sized[M] = dict(
-                x_rows=Quantised(M, K, dev), x_cols=Quantised(K, M, dev), g_rows=Quantised(M, N, dev), g_cols=Quantised(N, M, dev),
-                workspace=torch.empty(fg.mxfp4_quantize_grad_workspace_size(M, N), dtype=torch.uint8, device=dev))
-        return self._sized[M]
+    def _buffer(self, M: int, name: str, make):
+        """What only lives during a call, kept while calls have M rows."""
+        if self._scratch[0] != M:
+            self._scratch = (M, {})
+        made = self._scratch[1]
+        if name not in made:
+            made[name] = make()
+        return made[name]
 
     def _tokens(self, x: torch.Tensor, cols: int):
         """Rows and leading dimension of a matrix given to a call."""
@@ -86,14 +90,19 @@ class Mxfp4Layer:
         return y
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """Y for tokens x (M x K), which stay quantised both ways for ``backward``."""
+        """Y for tokens x (M x K), which stay quantised along their columns for ``backward``: those of the last
+        forward for each of the last ``SIZES`` numbers of tokens."""
         M, ldx = self._tokens(x, self.K)
+        dev = self.weight.device
         y = torch.empty(M, self.N, dtype=x.dtype, device=x.device)
         if M:
-            b = self._buffers(M)
-            fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *b["x_rows"].args, *b["x_cols"].args)
-            fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *b["x_rows"].args, *self.w_cols.args, 0.0, y, self.N, self.bias,
-                          self.relu)
+            rows = self._buffer(M, "x_rows", lambda: Quantised(M, self.K, dev))
+            cols = self._tokens_of.pop(M, None) or Quantised(self.K, M, dev)
+            fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *rows.args, *cols.args)
+            self._tokens_of[M] = cols
+            if len(self._tokens_of) > SIZES:
+                del self._tokens_of[next(iter(self._tokens_of))]
+            fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *rows.args, *self.w_cols.args, 0.0, y, self.N, self.bias, self.relu)
         return y
 
     def backward(self, g: torch.Tensor, y: torch.Tensor):
@@ -102,19 +111,22 @@ class Mxfp4Layer:
         rows, ldy = self._tokens(y, self.N) if self.relu else (M, 0)
         if rows != M:  # y is read as the gate of every row of g
             raise ValueError("%d outputs for %d gradients" % (rows, M))
-        if M and M not in self._sized:  # there are no tokens to multiply the gradient with
+        if M and M not in self._tokens_of:  # there are no tokens to multiply the gradient with
             raise ValueError("no forward with %d tokens before this backward" % M)
         dev, dt = g.device, g.dtype
         dx = torch.empty(M, self.K, dtype=dt, device=dev)
         dw = torch.zeros(self.K, self.N, dtype=dt, device=dev) if M == 0 else torch.empty(self.K, self.N, dtype=dt, device=dev)
         db = torch.empty(self.N, device=dev) if M else torch.zeros(self.N, device=dev)
         if M:
-            b = self._buffers(M)
-            ws = b["workspace"]
-            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *b["g_rows"].args,
-                                   *b["g_cols"].args, db, ws, ws.numel())
-            fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *b["g_rows"].args, *self.w_rows.args, 0.0, dx, self.K)
-            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *b["x_cols"].args, *b["g_cols"].args, 0.0, dw, self.N)
+            here = self.weight.device
+            rows = self._buffer(M, "g_rows", lambda: Quantised(M, self.N, here))
+            cols = self._buffer(M, "g_cols", lambda: Quantised(self.N, M, here))
+            ws = self._buffer(M, "workspace", lambda: torch.empty(fg.mxfp4_quantize_grad_workspace_size(M, self.N),
+                                                                  dtype=torch.uint8, device=here))
+            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *rows.args, *cols.args, db,
+                                   ws, ws.numel())
+            fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *rows.args, *self.w_rows.args, 0.0, dx, self.K)
+            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *self._tokens_of[M].args, *cols.args, 0.0, dw, self.N)
         return dx, dw, db
 
 

@@ -94,3 +94,44 @@ def test_backward_without_its_forward_is_refused(calls):
     assert not calls
     layer.backward(torch.randn(5, N), y)
     assert [name for name, _ in calls] == ["quantize_grad", "gemm", "gemm"]
+
+
+def held(layer):
+    """Bytes of the tensors that the layer keeps, besides what it was given."""
+    seen, stack, total = set(), [layer], 0
+    while stack:
+        o = stack.pop()
+        if id(o) in seen or o is layer.weight or o is layer.bias:
+            continue
+        seen.add(id(o))
+        if isinstance(o, torch.Tensor):
+            total += o.numel() * o.element_size()
+        elif isinstance(o, dict):
+            stack.extend(o.values())
+        elif isinstance(o, (list, tuple)):
+            stack.extend(o)
+        elif type(o).__module__ == mxfp4_layer.__name__:
+            stack.extend(getattr(o, n, None) for n in (*vars(o), *getattr(type(o), "__slots__", ())))
+    return total
+
+
+def test_many_sizes_do_not_fill_the_memory(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    weights = held(layer)
+    most = 0
+    layer.backward(torch.randn(200, N), layer.forward(torch.randn(200, K)))  # the largest size
+    one = held(layer) - weights
+    for M in range(1, 201):
+        layer.backward(torch.randn(M, N), layer.forward(torch.randn(M, K)))
+        most = max(most, held(layer) - weights)
+    assert 0 < one and most <= 4 * one
+
+
+def test_a_few_sizes_may_be_under_way_at_once(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    sizes = (5, 17, 130, 40)
+    outs = [layer.forward(torch.randn(M, K)) for M in sizes]
+    for y in outs:
+        del calls[:]
+        layer.backward(torch.randn(len(y), N), y)
+        assert calls.named("gemm")[1][3] == len(y)
