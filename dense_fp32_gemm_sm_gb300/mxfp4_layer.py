@@ -6,12 +6,14 @@ gradient of X; tokens X (M x K) along their rows forward and their columns for t
 of W; the output's gradient both ways behind ReLU's gate, with the bias's gradient.  A few
 tokens at a time go through ``decode``, which quantises them on the way.
 
-``forward`` and ``backward`` work in buffers of the layer (those of the last size met, and the tokens of
-a few forwards), so they are used on one stream at a time.
+``forward`` and ``backward`` work in buffers of the layer (those of the last size met), so they are used on one
+stream at a time.
 ``python -m dense_fp32_gemm_sm_gb300.mxfp4_layer`` fits a small layer to another one's outputs.
 """
 
 from __future__ import annotations
+
+import weakref
 
 import torch
 
@@ -37,6 +39,14 @@ class Quantised:
         return self.codes, self.ld, self.scales
 
 
+class Saved:
+    """What a forward leaves for its backward: its tokens, quantised along their columns (a K x M matrix), and
+    where its output is."""
+
+    def __init__(self, layer: "Mxfp4Layer", tokens: Quantised, output: int):
+        self.of, self.tokens, self.output = weakref.ref(layer), tokens, output
+
+
 class Mxfp4Layer:
     """``weight`` (K x N) and ``bias`` (N floats, or None) stay the caller's; call ``update`` after
     changing the weight.  The element type of weight, tokens and gradients is the weight's."""
@@ -53,7 +63,8 @@ class Mxfp4Layer:
         self.w_rows = Quantised(self.K, self.N, weight.device)
         self.w_cols = Quantised(self.N, self.K, weight.device)
         self._scratch = (0, {})  # rows, buffers of the last size met
-        self._tokens_of = {}     # rows -> the tokens that backward needs, the latest last
+        self._last = {}          # rows -> the last forward's Saved, the latest forward last
+        self.saved = None        # the latest forward's (None for no tokens)
         self.update()
 
     def update(self) -> None:
@@ -90,29 +101,41 @@ class Mxfp4Layer:
         return y
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """Y for tokens x (M x K), which stay quantised along their columns for ``backward``: those of the last
-        forward for each of the last ``SIZES`` numbers of tokens."""
+        """Y for tokens x (M x K), which stay quantised along their columns for ``backward``: the layer keeps
+        those of the last forward for each of the last ``SIZES`` numbers of tokens, and ``saved`` is what
+        the caller keeps where more forwards come before their backwards.  (``decode`` keeps nothing.)"""
         M, ldx = self._tokens(x, self.K)
         dev = self.weight.device
         y = torch.empty(M, self.N, dtype=x.dtype, device=x.device)
+        self.saved = None
         if M:
             rows = self._buffer(M, "x_rows", lambda: Quantised(M, self.K, dev))
-            cols = self._tokens_of.pop(M, None) or Quantised(self.K, M, dev)
+            cols = Quantised(self.K, M, dev)
             fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *rows.args, *cols.args)
-            self._tokens_of[M] = cols
-            if len(self._tokens_of) > SIZES:
-                del self._tokens_of[next(iter(self._tokens_of))]
             fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *rows.args, *self.w_cols.args, 0.0, y, self.N, self.bias, self.relu)
+            self._last.pop(M, None)
+            self._last[M] = self.saved = Saved(self, cols, y.data_ptr())
+            if len(self._last) > SIZES:
+                del self._last[next(iter(self._last))]
         return y
 
-    def backward(self, g: torch.Tensor, y: torch.Tensor):
-        """(dX, dW, db) for the gradient g of the output y of the last ``forward`` with as many tokens."""
+    def backward(self, g: torch.Tensor, y: torch.Tensor | None, saved: Saved | None = None):
+        """(dX, dW, db) for the gradient g of the output y (None will do without ReLU) of the forward that left
+        ``saved``, or else of the last forward with as many tokens, whose output y then has to be."""
         M, ldg = self._tokens(g, self.N)
         rows, ldy = self._tokens(y, self.N) if self.relu else (M, 0)
         if rows != M:  # y is read as the gate of every row of g
             raise ValueError("%d outputs for %d gradients" % (rows, M))
-        if M and M not in self._tokens_of:  # there are no tokens to multiply the gradient with
-            raise ValueError("no forward with %d tokens before this backward" % M)
+        if saved is not None:
+            if not isinstance(saved, Saved) or saved.of() is not self or saved.tokens.shape[1] != M:
+                raise ValueError("saved: what a forward of this layer with %d tokens left" % M)
+        elif M:
+            saved = self._last.get(M)
+            if saved is None:  # there are no tokens to multiply the gradient with
+                raise ValueError("no forward with %d tokens before this backward" % M)
+            if y is not None and y.data_ptr() != saved.output:  # another forward's tokens have taken its place
+                raise ValueError("y is not the output of the last forward with %d tokens: keep the layer's `saved` after "
+                                 "its forward and pass it" % M)
         dev, dt = g.device, g.dtype
         dx = torch.empty(M, self.K, dtype=dt, device=dev)
         dw = torch.zeros(self.K, self.N, dtype=dt, device=dev) if M == 0 else torch.empty(self.K, self.N, dtype=dt, device=dev)
@@ -126,7 +149,7 @@ class Mxfp4Layer:
             fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *rows.args, *cols.args, db,
                                    ws, ws.numel())
             fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *rows.args, *self.w_rows.args, 0.0, dx, self.K)
-            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *self._tokens_of[M].args, *cols.args, 0.0, dw, self.N)
+            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *saved.tokens.args, *cols.args, 0.0, dw, self.N)
         return dx, dw, db
 
 

@@ -135,3 +135,58 @@ def test_a_few_sizes_may_be_under_way_at_once(calls):
         del calls[:]
         layer.backward(torch.randn(len(y), N), y)
         assert calls.named("gemm")[1][3] == len(y)
+
+
+def test_an_output_whose_tokens_were_replaced_is_refused(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    first = layer.forward(torch.randn(5, K))
+    second = layer.forward(torch.randn(5, K))
+    del calls[:]
+    with pytest.raises(ValueError):
+        layer.backward(torch.randn(5, N), first)
+    assert not calls
+    layer.backward(torch.randn(5, N), second)
+    layer.backward(torch.randn(5, N), second.detach())
+    assert len(calls) == 6
+
+
+def test_forwards_kept_by_the_caller(calls):
+    # several forwards of one size before their backwards, each with tokens of its own
+    layer = Mxfp4Layer(torch.randn(K, N))
+    outs, saved = [], []
+    for M in (5, 5, 9, 5):
+        outs.append(layer.forward(torch.randn(M, K)))
+        saved.append(layer.saved)
+    addresses = []
+    for y, s in zip(outs, saved):
+        del calls[:]
+        layer.backward(torch.randn(len(y), N), y.clone(), s)  # (a copy of the output will do then)
+        addresses.append(calls.named("gemm")[1][5].data_ptr())
+    assert len(set(addresses)) == 4
+    del calls[:]
+    layer.forward(torch.randn(5, K))
+    assert calls.named("quantize")[0][8].data_ptr() not in addresses
+    for wrong in (saved[2], object()):
+        with pytest.raises(ValueError):
+            layer.backward(torch.randn(5, N), outs[0], wrong)
+    other = Mxfp4Layer(torch.randn(K, N))
+    with pytest.raises(ValueError):  # another layer's tokens
+        other.backward(torch.randn(5, N), outs[0], saved[0])
+
+
+def test_without_relu_no_output_is_needed(calls):
+    layer = Mxfp4Layer(torch.randn(K, N), relu=False)
+    first = layer.forward(torch.randn(5, K))
+    layer.backward(torch.randn(5, N), None)
+    layer.forward(torch.randn(5, K))
+    with pytest.raises(ValueError):
+        layer.backward(torch.randn(5, N), first)
+
+
+def test_no_tokens_leave_nothing(calls):
+    layer = Mxfp4Layer(torch.randn(K, N))
+    layer.forward(torch.randn(5, K))
+    y = layer.forward(torch.empty(0, K))
+    assert layer.saved is None
+    dx, dw, db = layer.backward(torch.empty(0, N), y, layer.saved)
+    assert dx.shape == (0, K) and not dw.any() and not db.any()
