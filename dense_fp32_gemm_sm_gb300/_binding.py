@@ -375,7 +375,8 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
 # ---- MXFP4 (see "MXFP4" in include/fgemm.h) -------------------------------------------
 
 # The calls' arguments are converted by a small C module (csrc/py_calls.c); it takes tensors or
-# addresses like the functions above.
+# addresses like the functions above.  Tensors have to be on the current device (ValueError): the
+# library launches there.
 
 _TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
 _calls = None
@@ -392,6 +393,11 @@ def _current_stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
 def _native():
     """Load the C module and give it the library's entries."""
     global _calls
@@ -399,13 +405,13 @@ def _native():
     with _lock:
         if _calls is None:
             from . import _calls as module
-            raw_stream = _current_stream
+            raw_stream, device = _current_stream, _current_device
             if "torch" in sys.modules:
                 try:  # the handle without a Stream object, which takes 2 us
-                    from torch._C import _cuda_getCurrentRawStream as raw_stream
+                    from torch._C import _cuda_getCurrentRawStream as raw_stream, _cuda_getDevice as device
                 except ImportError:
                     pass
-            module.bind(_type_of, raw_stream,
+            module.bind(_type_of, raw_stream, device,
                         *(ctypes.cast(getattr(lib, "fgemm_mxfp4_" + name), _c_vp).value
                           for name in ("quantize", "quantize_grad", "dequantize", "gemm", "linear")))
             _calls = module

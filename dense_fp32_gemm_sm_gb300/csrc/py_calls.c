@@ -3,8 +3,8 @@
  * in Python took 3; here they take under 1.)
  *
  * A matrix may be a CUDA tensor (its data_ptr() is passed) or an address; an unquantised one
- * must have the call's element type.  Nothing of the library is linked: bind() is given the
- * entries' addresses. */
+ * must have the call's element type.  A call's tensors have to be on the current device, where the
+ * library launches.  Nothing of the library is linked: bind() is given the entries' addresses. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <cuda_runtime_api.h>
@@ -23,7 +23,8 @@ static struct {
 } entry;
 static PyObject *type_of;     /* Python: torch dtype -> fgemm_dtype value or -1 */
 static PyObject *raw_stream;  /* torch's (device index) -> current stream's handle, or None */
-static PyObject *s_is_cuda, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_cuda_stream;
+static PyObject *current_device;  /* torch's () -> current device's index */
+static PyObject *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_cuda_stream;
 /* Types met so far (borrowed for good: torch's dtypes live as long as the process). */
 static PyObject *known_type[8];
 static long known_value[8];
@@ -45,8 +46,9 @@ static long element_type(PyObject *dtype)
     return t;
 }
 
-/* The address of a tensor or number; type: the element type it must have (-1: any). */
-static int address(PyObject *x, long type, void **out)
+/* The address of a tensor or number; type: the element type it must have (-1: any).  device: that of
+ * the call's tensors, -1 before the first one. */
+static int address(PyObject *x, long type, long *device, void **out)
 {
     if (x == Py_None) {
         *out = NULL;
@@ -56,13 +58,16 @@ static int address(PyObject *x, long type, void **out)
         *out = PyLong_AsVoidPtr(x);
         return *out != NULL || !PyErr_Occurred();
     }
-    PyObject *cuda = PyObject_GetAttr(x, s_is_cuda);
-    if (!cuda) {
-        PyErr_Format(PyExc_TypeError, "expected a CUDA tensor or a device address, got %R", (PyObject *)Py_TYPE(x));
+    PyObject *index = PyObject_CallMethodNoArgs(x, s_get_device);
+    if (!index) {
+        if (PyErr_ExceptionMatches(PyExc_AttributeError))
+            PyErr_Format(PyExc_TypeError, "expected a CUDA tensor or a device address, got %R", (PyObject *)Py_TYPE(x));
         return 0;
     }
-    int ok = cuda == Py_True;
-    Py_DECREF(cuda);
+    const long on = PyLong_AsLong(index);  /* -1: on the host */
+    Py_DECREF(index);
+    if (on == -1 && PyErr_Occurred()) return 0;
+    const int ok = on >= 0;
     if (type >= 0 || !ok) {
         PyObject *dtype = PyObject_GetAttr(x, s_dtype);
         if (!dtype) return 0;
@@ -86,6 +91,12 @@ static int address(PyObject *x, long type, void **out)
         }
         Py_DECREF(dtype);
     }
+    if (*device < 0) {
+        *device = on;
+    } else if (*device != on) {
+        PyErr_Format(PyExc_ValueError, "tensors on several devices (cuda:%ld and cuda:%ld)", *device, on);
+        return 0;
+    }
     PyObject *ptr = PyObject_CallMethodNoArgs(x, s_data_ptr);
     if (!ptr) return 0;
     *out = PyLong_AsVoidPtr(ptr);
@@ -94,10 +105,22 @@ static int address(PyObject *x, long type, void **out)
 }
 
 /* The stream a call runs on: the one given (a handle or an object with cuda_stream), else the
- * current one of tensor x's device, else the default stream. */
-static int stream_of(PyObject *s, PyObject *x, cudaStream_t *out)
+ * current one of tensor x's device, else the default stream.  device: that of the call's tensors (-1:
+ * there are none), which has to be the current one. */
+static int stream_of(PyObject *s, PyObject *x, long device, cudaStream_t *out)
 {
     PyObject *v;
+    if (device >= 0) {
+        v = PyObject_CallNoArgs(current_device);
+        if (!v) return 0;
+        const long current = PyLong_AsLong(v);
+        Py_DECREF(v);
+        if (current == -1 && PyErr_Occurred()) return 0;
+        if (current != device) {
+            PyErr_Format(PyExc_ValueError, "tensors on cuda:%ld, but the current device is cuda:%ld", device, current);
+            return 0;
+        }
+    }
     if (s != Py_None) {
         if (PyLong_Check(s)) {
             Py_INCREF(s);
@@ -109,7 +132,7 @@ static int stream_of(PyObject *s, PyObject *x, cudaStream_t *out)
         *out = NULL;
         return 1;
     } else {
-        PyObject *d = PyObject_CallMethodNoArgs(x, s_get_device);
+        PyObject *d = PyLong_FromLong(device);
         if (!d) return 0;
         v = PyObject_CallOneArg(raw_stream, d);
         Py_DECREF(d);
@@ -162,9 +185,9 @@ static int count(const char *name, Py_ssize_t n, Py_ssize_t want)
     } while (0)
 
 #define INT(i, v) integer(a[i], &v)
-#define MATRIX(i, v) address(a[i], type, (void **)&v)
-#define RAW(i, v) address(a[i], -1, (void **)&v)
-#define FLOATS(i, v) address(a[i], FGEMM_F32, (void **)&v)
+#define MATRIX(i, v) address(a[i], type, &device, (void **)&v)
+#define RAW(i, v) address(a[i], -1, &device, (void **)&v)
+#define FLOATS(i, v) address(a[i], FGEMM_F32, &device, (void **)&v)
 
 /* (type, M, N, X, ldx, row_codes, ld, row_scales, col_codes, ld, col_scales, stream) */
 static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -172,9 +195,10 @@ static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     int type, M, N, ldx, ldr, ldc;
     void *x, *rc, *rs, *cc, *cs;
     cudaStream_t stream;
+    long device = -1;
     if (!count("mxfp4_quantize", n, 12) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !MATRIX(3, x) || !INT(4, ldx) ||
         !RAW(5, rc) || !INT(6, ldr) || !RAW(7, rs) || !RAW(8, cc) || !INT(9, ldc) || !RAW(10, cs) ||
-        !stream_of(a[11], a[3], &stream))
+        !stream_of(a[11], a[3], device, &stream))
         return NULL;
     RETURN_CALL(entry.quantize((fgemm_dtype)type, M, N, x, ldx, rc, ldr, rs, cc, ldc, cs, stream));
 }
@@ -187,10 +211,11 @@ static PyObject *quantize_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
     float *bias;
     size_t size;
     cudaStream_t stream;
+    long device = -1;
     if (!count("mxfp4_quantize_grad", n, 17) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !MATRIX(3, g) || !INT(4, ldg) ||
         !MATRIX(5, y) || !INT(6, ldy) || !RAW(7, rc) || !INT(8, ldr) || !RAW(9, rs) || !RAW(10, cc) || !INT(11, ldc) ||
         !RAW(12, cs) || !FLOATS(13, bias) || !RAW(14, ws) || !bytes(a[15], &size) ||
-        !stream_of(a[16], a[3] == Py_None ? a[13] : a[3], &stream))
+        !stream_of(a[16], a[3] == Py_None ? a[13] : a[3], device, &stream))
         return NULL;
     RETURN_CALL(entry.quantize_grad((fgemm_dtype)type, M, N, g, ldg, y, ldy, rc, ldr, rs, cc, ldc, cs, bias, ws, size, stream));
 }
@@ -201,8 +226,9 @@ static PyObject *dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     int type, M, N, ld, ldx;
     void *codes, *scales, *x;
     cudaStream_t stream;
+    long device = -1;
     if (!count("mxfp4_dequantize", n, 9) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !RAW(3, codes) || !INT(4, ld) ||
-        !RAW(5, scales) || !MATRIX(6, x) || !INT(7, ldx) || !stream_of(a[8], a[6], &stream))
+        !RAW(5, scales) || !MATRIX(6, x) || !INT(7, ldx) || !stream_of(a[8], a[6], device, &stream))
         return NULL;
     RETURN_CALL(entry.dequantize((fgemm_dtype)type, M, N, codes, ld, scales, x, ldx, stream));
 }
@@ -215,10 +241,11 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t n)
     void *ac, *as, *bc, *bs, *c;
     float *bias;
     cudaStream_t stream;
+    long device = -1;
     if (!count("mxfp4_gemm", n, 17) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !INT(3, K) || !number(a[4], &alpha) ||
         !RAW(5, ac) || !INT(6, lda) || !RAW(7, as) || !RAW(8, bc) || !INT(9, ldb) || !RAW(10, bs) || !number(a[11], &beta) ||
         !MATRIX(12, c) || !INT(13, ldc) || !FLOATS(14, bias) || (relu = PyObject_IsTrue(a[15])) < 0 ||
-        !stream_of(a[16], a[12], &stream))
+        !stream_of(a[16], a[12], device, &stream))
         return NULL;
     RETURN_CALL(entry.gemm((fgemm_dtype)type, M, N, K, alpha, ac, lda, as, bc, ldb, bs, beta, c, ldc, bias, relu, stream));
 }
@@ -231,25 +258,27 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n)
     float *bias;
     size_t size;
     cudaStream_t stream;
+    long device = -1;
     if (!count("mxfp4_linear", n, 16) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !INT(3, K) || !MATRIX(4, x) ||
         !INT(5, ldx) || !RAW(6, wc) || !INT(7, ldw) || !RAW(8, ws) || !FLOATS(9, bias) ||
         (relu = PyObject_IsTrue(a[10])) < 0 || !MATRIX(11, y) || !INT(12, ldy) || !RAW(13, space) || !bytes(a[14], &size) ||
-        !stream_of(a[15], a[11], &stream))
+        !stream_of(a[15], a[11], device, &stream))
         return NULL;
     RETURN_CALL(entry.linear((fgemm_dtype)type, M, N, K, x, ldx, wc, ldw, ws, bias, relu, y, ldy, space, size, stream));
 }
 
-/* (type_of, raw_stream, addresses of quantize, quantize_grad, dequantize, gemm, linear) */
+/* (type_of, raw_stream, current_device, addresses of quantize, quantize_grad, dequantize, gemm, linear) */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     void *p[5];
-    if (!count("bind", n, 7)) return NULL;
+    long device = -1;
+    if (!count("bind", n, 8)) return NULL;
     for (int i = 0; i < 5; ++i)
-        if (!address(a[2 + i], -1, &p[i])) return NULL;
-    Py_INCREF(a[0]);
-    Py_INCREF(a[1]);
+        if (!address(a[3 + i], -1, &device, &p[i])) return NULL;
+    for (int i = 0; i < 3; ++i) Py_INCREF(a[i]);
     Py_XSETREF(type_of, a[0]);
     Py_XSETREF(raw_stream, a[1]);
+    Py_XSETREF(current_device, a[2]);
     *(void **)&entry.quantize = p[0];
     *(void **)&entry.quantize_grad = p[1];
     *(void **)&entry.dequantize = p[2];
@@ -265,12 +294,11 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "MXFP4 call
 
 PyMODINIT_FUNC PyInit__calls(void)
 {
-    s_is_cuda = PyUnicode_InternFromString("is_cuda");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_device = PyUnicode_InternFromString("device");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_get_device = PyUnicode_InternFromString("get_device");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    if (!s_is_cuda || !s_dtype || !s_device || !s_data_ptr || !s_get_device || !s_cuda_stream) return NULL;
+    if (!s_dtype || !s_device || !s_data_ptr || !s_get_device || !s_cuda_stream) return NULL;
     return PyModule_Create(&module);
 }
