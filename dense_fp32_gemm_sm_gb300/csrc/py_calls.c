@@ -22,7 +22,7 @@ static struct {
                            void *, int, void *, size_t, cudaStream_t);
 } entry;
 static PyObject *type_of;     /* Python: torch dtype -> fgemm_dtype value or -1 */
-static PyObject *raw_stream;  /* torch's (device index) -> current stream's handle, or None */
+static PyObject *raw_stream;  /* torch's (device index) -> current stream's handle */
 static PyObject *current_device;  /* torch's () -> current device's index */
 static PyObject *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_cuda_stream;
 /* Types met so far (borrowed for good: torch's dtypes live as long as the process). */
@@ -105,9 +105,9 @@ static int address(PyObject *x, long type, long *device, void **out)
 }
 
 /* The stream a call runs on: the one given (a handle or an object with cuda_stream), else the
- * current one of tensor x's device, else the default stream.  device: that of the call's tensors (-1:
+ * current one of its tensors' device, else the default stream.  device: that of the call's tensors (-1:
  * there are none), which has to be the current one. */
-static int stream_of(PyObject *s, PyObject *x, long device, cudaStream_t *out)
+static int stream_of(PyObject *s, long device, cudaStream_t *out)
 {
     PyObject *v;
     if (device >= 0) {
@@ -128,7 +128,7 @@ static int stream_of(PyObject *s, PyObject *x, long device, cudaStream_t *out)
         } else {
             v = PyObject_GetAttr(s, s_cuda_stream);
         }
-    } else if (x == Py_None || PyLong_Check(x) || raw_stream == Py_None) {
+    } else if (device < 0) {
         *out = NULL;
         return 1;
     } else {
@@ -198,7 +198,7 @@ static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     long device = -1;
     if (!count("mxfp4_quantize", n, 12) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !MATRIX(3, x) || !INT(4, ldx) ||
         !RAW(5, rc) || !INT(6, ldr) || !RAW(7, rs) || !RAW(8, cc) || !INT(9, ldc) || !RAW(10, cs) ||
-        !stream_of(a[11], a[3], device, &stream))
+        !stream_of(a[11], device, &stream))
         return NULL;
     RETURN_CALL(entry.quantize((fgemm_dtype)type, M, N, x, ldx, rc, ldr, rs, cc, ldc, cs, stream));
 }
@@ -215,7 +215,7 @@ static PyObject *quantize_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (!count("mxfp4_quantize_grad", n, 17) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !MATRIX(3, g) || !INT(4, ldg) ||
         !MATRIX(5, y) || !INT(6, ldy) || !RAW(7, rc) || !INT(8, ldr) || !RAW(9, rs) || !RAW(10, cc) || !INT(11, ldc) ||
         !RAW(12, cs) || !FLOATS(13, bias) || !RAW(14, ws) || !bytes(a[15], &size) ||
-        !stream_of(a[16], a[3] == Py_None ? a[13] : a[3], device, &stream))
+        !stream_of(a[16], device, &stream))
         return NULL;
     RETURN_CALL(entry.quantize_grad((fgemm_dtype)type, M, N, g, ldg, y, ldy, rc, ldr, rs, cc, ldc, cs, bias, ws, size, stream));
 }
@@ -228,7 +228,7 @@ static PyObject *dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     cudaStream_t stream;
     long device = -1;
     if (!count("mxfp4_dequantize", n, 9) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !RAW(3, codes) || !INT(4, ld) ||
-        !RAW(5, scales) || !MATRIX(6, x) || !INT(7, ldx) || !stream_of(a[8], a[6], device, &stream))
+        !RAW(5, scales) || !MATRIX(6, x) || !INT(7, ldx) || !stream_of(a[8], device, &stream))
         return NULL;
     RETURN_CALL(entry.dequantize((fgemm_dtype)type, M, N, codes, ld, scales, x, ldx, stream));
 }
@@ -245,7 +245,7 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (!count("mxfp4_gemm", n, 17) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !INT(3, K) || !number(a[4], &alpha) ||
         !RAW(5, ac) || !INT(6, lda) || !RAW(7, as) || !RAW(8, bc) || !INT(9, ldb) || !RAW(10, bs) || !number(a[11], &beta) ||
         !MATRIX(12, c) || !INT(13, ldc) || !FLOATS(14, bias) || (relu = PyObject_IsTrue(a[15])) < 0 ||
-        !stream_of(a[16], a[12], device, &stream))
+        !stream_of(a[16], device, &stream))
         return NULL;
     RETURN_CALL(entry.gemm((fgemm_dtype)type, M, N, K, alpha, ac, lda, as, bc, ldb, bs, beta, c, ldc, bias, relu, stream));
 }
@@ -262,7 +262,7 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (!count("mxfp4_linear", n, 16) || !INT(0, type) || !INT(1, M) || !INT(2, N) || !INT(3, K) || !MATRIX(4, x) ||
         !INT(5, ldx) || !RAW(6, wc) || !INT(7, ldw) || !RAW(8, ws) || !FLOATS(9, bias) ||
         (relu = PyObject_IsTrue(a[10])) < 0 || !MATRIX(11, y) || !INT(12, ldy) || !RAW(13, space) || !bytes(a[14], &size) ||
-        !stream_of(a[15], a[11], device, &stream))
+        !stream_of(a[15], device, &stream))
         return NULL;
     RETURN_CALL(entry.linear((fgemm_dtype)type, M, N, K, x, ldx, wc, ldw, ws, bias, relu, y, ldy, space, size, stream));
 }

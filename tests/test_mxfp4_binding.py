@@ -107,3 +107,12 @@ def test_what_is_no_cuda_tensor_is_a_type_error(gpu):
                 call({n: bad if n == k else make() for n, make in makers.items()})
     with pytest.raises(TypeError):
         call({n: make() for n, make in makers.items()} | dict(X=Tensor(0, torch.float16)))
+
+
+@pytest.mark.parametrize("name,odd", [(n, k) for n, (_, makers) in CALLS.items() for k in makers])
+def test_one_tensor_among_addresses_gives_its_stream(gpu, name, odd):
+    # whichever argument it is: work that made it is on that stream
+    call, makers = CALLS[name]
+    gpu.current = 1
+    assert call({k: make(1) if k == odd else 0x10000 for k, make in makers.items()}) == INVALID
+    assert gpu.asked == [1]
