@@ -399,11 +399,12 @@ def _current_device():
 
 
 def _native():
-    """Load the C module and give it the library's entries."""
+    """Load the C module (building first if its source is newer) and give it the library's entries."""
     global _calls
     lib = library()
     with _lock:
         if _calls is None:
+            _build.build_calls()
             from . import _calls as module
             raw_stream, device = _current_stream, _current_device
             if "torch" in sys.modules:

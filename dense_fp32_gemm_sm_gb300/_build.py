@@ -1,4 +1,4 @@
-"""Build ``libfgemm.so`` in-tree from ``csrc/`` with nvcc for sm_103a, and ``_calls.so``, the
+"""Build ``libfgemm.so`` in-tree from ``csrc/`` with nvcc for sm_103a, and ``_calls``, the
 Python side of the MXFP4 entries, from ``csrc/py_calls.c``.
 
 Each translation unit is compiled in parallel, then linked into one shared
@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfgemm.so")
-CALLS = os.path.join(HERE, "_calls.so")
+CALLS = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALLS_SRC = os.path.join(CSRC, "py_calls.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
@@ -53,7 +53,8 @@ def stale() -> bool:
 
 
 def build_calls(force: bool = False) -> str:
-    """``_calls.so``, a CPython extension module (plain C, no CUDA code)."""
+    """``_calls``, a CPython extension module (plain C, no CUDA code) for the running interpreter; wanted by
+    the MXFP4 calls alone."""
     header = os.path.join(ROOT, "include", "fgemm.h")
     if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(
             os.path.getmtime(f) for f in (CALLS_SRC, header, __file__)):
@@ -72,7 +73,6 @@ def build_calls(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_calls(force)
     if not force and not stale():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -109,3 +109,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True)
+    build_calls(force="--force" in sys.argv)
