@@ -27,6 +27,14 @@ template <> __device__ __forceinline__ float from_float<float>(float x) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
 
+// max(0, x); a NaN stays, as what a spoiled block reaches is not a number.
+__device__ __forceinline__ float relu(float x)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // A block's scale byte from the bits of its largest magnitude (the exponent field, less
 // the 2 of the largest code's exponent); 255 when the block holds a NaN or an infinity.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t largest_bits)

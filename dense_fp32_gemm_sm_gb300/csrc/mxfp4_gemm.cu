@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256) no_products_kernel(const GemmArgs g)
         float o = 0.0f;
         if (g.beta != 0.0f) o = g.beta * to_float(*out);
         if (g.bias) o += g.bias[c];
-        if (g.relu) o = fmaxf(o, 0.0f);
+        if (g.relu) o = relu(o);
         *out = from_float<T>(o);
     }
 }

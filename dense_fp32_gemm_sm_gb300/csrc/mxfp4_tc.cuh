@@ -187,7 +187,7 @@ __device__ __forceinline__ float finish(const TcArgs &p, const T *out, float sum
 {
     float o = fmaf(p.alpha, sum, bias);
     if constexpr (BETA) o = fmaf(p.beta, to_float(*out), o);
-    if constexpr (RELU) o = fmaxf(o, 0.0f);
+    if constexpr (RELU) o = relu(o);
     return o;
 }
 
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) mxfp4_tc_kernel(const __grid_co
                 const float bias = p.bias ? __ldcg(p.bias + n + e) : 0.0f;
                 float o = p.beta != 0.0f ? finish<T, true, false>(p, out + e, sum[e], bias)
                                          : finish<T, false, false>(p, out + e, sum[e], bias);
-                if (p.relu) o = fmaxf(o, 0.0f);
+                if (p.relu) o = relu(o);
                 out[e] = from_float<T>(o);
             }
         }

@@ -503,9 +503,10 @@ fgemm_status fgemm_mxfp4_dequantize(fgemm_dtype type, int M, int N, const void *
  * Product of quantised matrices, A (M x K) and B (N x K), both with blocks along K:
  *     C[i][j] = act( alpha * sum_k A[i][k] B[j][k] + beta * C[i][j] + bias[j] )
  * C (M x N, leading dimension ldc) has element type `type`; bias: N floats or NULL; a
- * nonzero apply_relu is act(x) = max(0, x).  Products and sums are formed in FP32 and C is
- * rounded once.  alpha, beta, empty sizes: as for fgemm_sgemm (beta == 0 does not read C;
- * alpha == 0 or K == 0 reads neither A nor B).
+ * nonzero apply_relu is act(x) = max(0, x), and a NaN stays NaN (in fgemm_mxfp4_linear too; the FP32
+ * entries make it 0).  Products and sums are formed in FP32 and C is rounded once.  alpha,
+ * beta, empty sizes: as for fgemm_sgemm (beta == 0 does not read C; alpha == 0 or K == 0
+ * reads neither A nor B).
  */
 fgemm_status fgemm_mxfp4_gemm(fgemm_dtype type, int M, int N, int K, float alpha,
                               const void *A_codes, int ld_A_codes, const void *A_scales,
