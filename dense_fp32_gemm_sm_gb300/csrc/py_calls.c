@@ -24,7 +24,8 @@ static struct {
 static PyObject *type_of;     /* Python: torch dtype -> fgemm_dtype value or -1 */
 static PyObject *raw_stream;  /* torch's (device index) -> current stream's handle */
 static PyObject *current_device;  /* torch's () -> current device's index */
-static PyObject *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_cuda_stream;
+static int one_device;            /* torch sees one device: its tensors are on the current one, number 0 */
+static PyObject *s_is_cuda, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_cuda_stream;
 /* Types met so far (borrowed for good: torch's dtypes live as long as the process). */
 static PyObject *known_type[8];
 static long known_value[8];
@@ -58,14 +59,14 @@ static int address(PyObject *x, long type, long *device, void **out)
         *out = PyLong_AsVoidPtr(x);
         return *out != NULL || !PyErr_Occurred();
     }
-    PyObject *index = PyObject_CallMethodNoArgs(x, s_get_device);
-    if (!index) {
+    PyObject *where = one_device ? PyObject_GetAttr(x, s_is_cuda) : PyObject_CallMethodNoArgs(x, s_get_device);
+    if (!where) {
         if (PyErr_ExceptionMatches(PyExc_AttributeError))
             PyErr_Format(PyExc_TypeError, "expected a CUDA tensor or a device address, got %R", (PyObject *)Py_TYPE(x));
         return 0;
     }
-    const long on = PyLong_AsLong(index);  /* -1: on the host */
-    Py_DECREF(index);
+    const long on = one_device ? (where == Py_True) - 1 : PyLong_AsLong(where);  /* -1: on the host */
+    Py_DECREF(where);
     if (on == -1 && PyErr_Occurred()) return 0;
     const int ok = on >= 0;
     if (type >= 0 || !ok) {
@@ -110,7 +111,7 @@ static int address(PyObject *x, long type, long *device, void **out)
 static int stream_of(PyObject *s, long device, cudaStream_t *out)
 {
     PyObject *v;
-    if (device >= 0) {
+    if (device >= 0 && !one_device) {
         v = PyObject_CallNoArgs(current_device);
         if (!v) return 0;
         const long current = PyLong_AsLong(v);
@@ -267,14 +268,17 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n)
     RETURN_CALL(entry.linear((fgemm_dtype)type, M, N, K, x, ldx, wc, ldw, ws, bias, relu, y, ldy, space, size, stream));
 }
 
-/* (type_of, raw_stream, current_device, addresses of quantize, quantize_grad, dequantize, gemm, linear) */
+/* (type_of, raw_stream, current_device, one_device, addresses of quantize, quantize_grad, dequantize, gemm, linear) */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     void *p[5];
     long device = -1;
-    if (!count("bind", n, 8)) return NULL;
+    if (!count("bind", n, 9)) return NULL;
     for (int i = 0; i < 5; ++i)
-        if (!address(a[3 + i], -1, &device, &p[i])) return NULL;
+        if (!address(a[4 + i], -1, &device, &p[i])) return NULL;
+    const int one = PyObject_IsTrue(a[3]);
+    if (one < 0) return NULL;
+    one_device = one;
     for (int i = 0; i < 3; ++i) Py_INCREF(a[i]);
     Py_XSETREF(type_of, a[0]);
     Py_XSETREF(raw_stream, a[1]);
@@ -294,11 +298,12 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "MXFP4 call
 
 PyMODINIT_FUNC PyInit__calls(void)
 {
+    s_is_cuda = PyUnicode_InternFromString("is_cuda");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_device = PyUnicode_InternFromString("device");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_get_device = PyUnicode_InternFromString("get_device");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    if (!s_dtype || !s_device || !s_data_ptr || !s_get_device || !s_cuda_stream) return NULL;
+    if (!s_is_cuda || !s_dtype || !s_device || !s_data_ptr || !s_get_device || !s_cuda_stream) return NULL;
     return PyModule_Create(&module);
 }

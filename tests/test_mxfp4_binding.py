@@ -28,8 +28,9 @@ class Tensor:
 
 @pytest.fixture
 def gpu(monkeypatch):
-    """The current device, and the devices whose current stream was asked for."""
+    """Two devices: the current one, and those whose current stream was asked for."""
     state = type("State", (), dict(current=0, asked=[]))()
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
 
     def stream(index):
         state.asked.append(index)
@@ -42,6 +43,16 @@ def gpu(monkeypatch):
     yield state
     monkeypatch.undo()
     _binding._calls = None
+
+
+@pytest.fixture
+def only_gpu(gpu, monkeypatch):
+    """The same with one device, of which nobody asks whether it is current."""
+    def asked():
+        raise AssertionError("asked for the current device")
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", asked, raising=False)
+    return gpu
 
 
 def u8(index=0):
@@ -75,6 +86,13 @@ def test_tensors_on_the_current_device(gpu, name):
 
 
 @pytest.mark.parametrize("name", CALLS)
+def test_tensors_on_the_only_device(only_gpu, name):
+    call, makers = CALLS[name]
+    assert call({k: make() for k, make in makers.items()}) == INVALID
+    assert only_gpu.asked == [0]
+
+
+@pytest.mark.parametrize("name", CALLS)
 def test_tensors_on_another_device_are_refused(gpu, name):
     # the library launches on the current device, whatever device an address belongs to
     call, makers = CALLS[name]
@@ -99,7 +117,9 @@ def test_addresses_are_taken_as_they_are(gpu):
     assert not gpu.asked
 
 
-def test_what_is_no_cuda_tensor_is_a_type_error(gpu):
+@pytest.mark.parametrize("devices", ["gpu", "only_gpu"])
+def test_what_is_no_cuda_tensor_is_a_type_error(devices, request):
+    request.getfixturevalue(devices)
     call, makers = CALLS["quantize"]
     for bad in (torch.zeros(4, 40), torch.zeros(4, 40, device="meta"), object(), "x", 1.5):
         for k in ("X", "rs"):
