@@ -6,8 +6,8 @@ gradient of X; tokens X (M x K) along their rows forward and their columns for t
 of W; the output's gradient both ways behind ReLU's gate, with the bias's gradient.  A few
 tokens at a time go through ``decode``, which quantises them on the way.
 
-``forward`` and ``backward`` work in buffers of the layer (those of the last size met), so they are used on one
-stream at a time.
+``forward`` and ``backward`` work in buffers of the layer (those of the last few sizes met), so they are used on
+one stream at a time.
 ``python -m dense_fp32_gemm_sm_gb300.mxfp4_layer`` fits a small layer to another one's outputs.
 """
 
@@ -19,7 +19,7 @@ import torch
 
 from . import _binding as fg
 
-SIZES = 4  # numbers of tokens whose last forward may wait for its backward
+SIZES = 4  # numbers of tokens whose buffers a layer keeps
 
 _TYPES = {torch.float32: fg.F32, torch.bfloat16: fg.BF16, torch.float16: fg.F16}
 
@@ -45,6 +45,7 @@ class Saved:
 
     def __init__(self, layer: "Mxfp4Layer", tokens: Quantised, output: int):
         self.of, self.tokens, self.output = weakref.ref(layer), tokens, output
+        self.kept = False  # a caller has it, so later forwards leave its tokens alone
 
 
 class Mxfp4Layer:
@@ -62,9 +63,8 @@ class Mxfp4Layer:
         self.K, self.N = weight.shape
         self.w_rows = Quantised(self.K, self.N, weight.device)
         self.w_cols = Quantised(self.N, self.K, weight.device)
-        self._scratch = (0, {})  # rows, buffers of the last size met
-        self._last = {}          # rows -> the last forward's Saved, the latest forward last
-        self.saved = None        # the latest forward's (None for no tokens)
+        self._sized = {}      # rows -> buffers of the last sizes met, the latest last
+        self._latest = None   # what the latest forward left (None for no tokens)
         self.update()
 
     def update(self) -> None:
@@ -72,14 +72,16 @@ class Mxfp4Layer:
         fg.mxfp4_quantize(self.type, self.K, self.N, self.weight, self.weight.stride(0), *self.w_rows.args,
                           *self.w_cols.args)
 
-    def _buffer(self, M: int, name: str, make):
-        """What only lives during a call, kept while calls have M rows."""
-        if self._scratch[0] != M:
-            self._scratch = (M, {})
-        made = self._scratch[1]
-        if name not in made:
-            made[name] = make()
-        return made[name]
+    def _buffers(self, M: int):
+        b = self._sized.pop(M, None)
+        if b is None:
+            dev, K, N = self.weight.device, self.K, self.N
+            if len(self._sized) == SIZES:
+                del self._sized[next(iter(self._sized))]
+            b = dict(x_rows=Quantised(M, K, dev), g_rows=Quantised(M, N, dev), g_cols=Quantised(N, M, dev), saved=None,
+                     workspace=torch.empty(fg.mxfp4_quantize_grad_workspace_size(M, N), dtype=torch.uint8, device=dev))
+        self._sized[M] = b
+        return b
 
     def _tokens(self, x: torch.Tensor, cols: int):
         """Rows and leading dimension of a matrix given to a call."""
@@ -105,19 +107,24 @@ class Mxfp4Layer:
         those of the last forward for each of the last ``SIZES`` numbers of tokens, and ``saved`` is what
         the caller keeps where more forwards come before their backwards.  (``decode`` keeps nothing.)"""
         M, ldx = self._tokens(x, self.K)
-        dev = self.weight.device
         y = torch.empty(M, self.N, dtype=x.dtype, device=x.device)
-        self.saved = None
+        self._latest = None
         if M:
-            rows = self._buffer(M, "x_rows", lambda: Quantised(M, self.K, dev))
-            cols = Quantised(self.K, M, dev)
-            fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *rows.args, *cols.args)
-            fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *rows.args, *self.w_cols.args, 0.0, y, self.N, self.bias, self.relu)
-            self._last.pop(M, None)
-            self._last[M] = self.saved = Saved(self, cols, y.data_ptr())
-            if len(self._last) > SIZES:
-                del self._last[next(iter(self._last))]
+            b = self._buffers(M)
+            last, b["saved"] = b["saved"], None
+            cols = last.tokens if last and not last.kept else Quantised(self.K, M, self.weight.device)
+            fg.mxfp4_quantize(self.type, M, self.K, x, ldx, *b["x_rows"].args, *cols.args)
+            fg.mxfp4_gemm(self.type, M, self.N, self.K, 1.0, *b["x_rows"].args, *self.w_cols.args, 0.0, y, self.N, self.bias,
+                          self.relu)
+            self._latest = b["saved"] = Saved(self, cols, y.data_ptr())
         return y
+
+    @property
+    def saved(self) -> Saved | None:
+        """What the latest forward left for its backward, the caller's from here on."""
+        if self._latest:
+            self._latest.kept = True
+        return self._latest
 
     def backward(self, g: torch.Tensor, y: torch.Tensor | None, saved: Saved | None = None):
         """(dX, dW, db) for the gradient g of the output y (None will do without ReLU) of the forward that left
@@ -130,7 +137,7 @@ class Mxfp4Layer:
             if not isinstance(saved, Saved) or saved.of() is not self or saved.tokens.shape[1] != M:
                 raise ValueError("saved: what a forward of this layer with %d tokens left" % M)
         elif M:
-            saved = self._last.get(M)
+            saved = self._sized[M]["saved"] if M in self._sized else None
             if saved is None:  # there are no tokens to multiply the gradient with
                 raise ValueError("no forward with %d tokens before this backward" % M)
             if y is not None and y.data_ptr() != saved.output:  # another forward's tokens have taken its place
@@ -141,15 +148,12 @@ class Mxfp4Layer:
         dw = torch.zeros(self.K, self.N, dtype=dt, device=dev) if M == 0 else torch.empty(self.K, self.N, dtype=dt, device=dev)
         db = torch.empty(self.N, device=dev) if M else torch.zeros(self.N, device=dev)
         if M:
-            here = self.weight.device
-            rows = self._buffer(M, "g_rows", lambda: Quantised(M, self.N, here))
-            cols = self._buffer(M, "g_cols", lambda: Quantised(self.N, M, here))
-            ws = self._buffer(M, "workspace", lambda: torch.empty(fg.mxfp4_quantize_grad_workspace_size(M, self.N),
-                                                                  dtype=torch.uint8, device=here))
-            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *rows.args, *cols.args, db,
-                                   ws, ws.numel())
-            fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *rows.args, *self.w_rows.args, 0.0, dx, self.K)
-            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *saved.tokens.args, *cols.args, 0.0, dw, self.N)
+            b = self._buffers(M)
+            ws = b["workspace"]
+            fg.mxfp4_quantize_grad(self.type, M, self.N, g, ldg, y if self.relu else None, ldy, *b["g_rows"].args,
+                                   *b["g_cols"].args, db, ws, ws.numel())
+            fg.mxfp4_gemm(self.type, M, self.K, self.N, 1.0, *b["g_rows"].args, *self.w_rows.args, 0.0, dx, self.K)
+            fg.mxfp4_gemm(self.type, self.K, self.N, M, 1.0, *saved.tokens.args, *b["g_cols"].args, 0.0, dw, self.N)
         return dx, dw, db
 
 
