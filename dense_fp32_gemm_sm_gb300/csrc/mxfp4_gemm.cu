@@ -67,6 +67,9 @@ fgemm_status run_gemm(const GemmArgs &g, cudaStream_t stream)
 // shapes from 96 x 300 x 2000 to 8192 x 11008 x 4096, FP32 and BF16: the way with the least
 // estimate took 0.3 % longer than the fastest on average, 10 % at most).  Tiles over CTAs (or
 // pairs) come in rounds, each of so many stages and a boundary; C is written beside them.
+// For fewer rows than 96, where only the number of ranks is chosen, the same estimate serves
+// unfitted, and it weighs 2, 4 and 8 ranks with one CTA an SM although the kernel takes any
+// number to 8 and two CTAs an SM.
 static double rounds(long long M, long long tile_m, long long N, long long tile_n, long long units)
 {
     const long long tiles = ((M + tile_m - 1) / tile_m) * ((N + tile_n - 1) / tile_n);

@@ -184,7 +184,8 @@ __device__ __forceinline__ uint32_t encode_row_block(const uint8_t *tile, int ro
 }
 
 // Bound by memory: the matrix once in, 17/32 bytes an element and direction out.  Persistent
-// CTAs; while a tile is worked on, the next two are copied.
+// CTAs; while a tile is worked on, the next is copied, and in FP32 without a gate the one after
+// it too (STAGES - 1 tiles ahead).
 // ELEMENTS: mode is COPY_ELEMENTS (an instance of its own, for the registers that its loads take).
 template <class T, bool GATED, bool ELEMENTS>
 __global__ void __launch_bounds__(QuantShape<sizeof(T), GATED>::THREADS, ELEMENTS ? 2 : QuantShape<sizeof(T), GATED>::CTAS_PER_SM)

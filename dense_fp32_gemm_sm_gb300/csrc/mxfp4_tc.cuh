@@ -53,8 +53,8 @@ struct TcTile {
     static constexpr int X_BYTES = NT * 128;
     static constexpr int SF_BYTES = 2 * ATOM_BYTES;  // of either operand: NT divides a group of 128 rows
     static constexpr int STAGE_BYTES = W_BYTES + SF_BYTES + (FUSED ? 0 : X_BYTES + SF_BYTES);
-    // (80 KB for the narrow tiles, so that two CTAs share an SM; eight stages measured no faster, and
-    // three, with three CTAs an SM, 0.1 to 0.8 us slower.)
+    // (80 to 104 KB for the tiles of 16 to 64 rows, so that two CTAs share an SM; eight stages measured
+    // no faster, and three, with three CTAs an SM, 0.1 to 0.8 us slower.)
     static constexpr int STAGES = NT == 128 ? 6 : 4;
     // Fused: A's codes and scales of each of this CTA's stages follow the ring and the barriers.
     static constexpr int FUSED_BYTES = FUSED ? X_BYTES + SF_BYTES : 0;

@@ -439,13 +439,16 @@ fgemm_status fgemm_gemm_explicit(int config, fgemm_op transa, fgemm_op transb, i
  *   codes:  row r starts at byte r * ld; element k is in byte k/2 of the row, the low
  *           nibble for even k.  ld (bytes) is a multiple of 16 and at least
  *           16 * ceil(L/32); the pointer is 16-byte aligned.  A row is written up to
- *           byte 16 * ceil(L/32); the codes beyond L are 0.  Products read rows in pieces
- *           of 128 bytes and are fastest with rows that start on 64 (pointer and ld).
+ *           byte 16 * ceil(L/32); the codes beyond L are 0 (and have to be in a matrix that
+ *           comes from elsewhere).  Products read rows in pieces of 128 bytes and are
+ *           fastest with rows that start on 64 (pointer and ld).
  *   scales: with nb = ceil(L/32), the byte of row r and block b is at
  *           512 * ((r/128) * ceil(nb/4) + b/4) + 16 * (r%32) + 4 * ((r%128)/32) + b%4:
  *           atoms of 128 rows x 4 blocks, as the tensor cores take them.  16-byte
  *           aligned, fgemm_mxfp4_scales_size(R, L) bytes.  Scales of rows and blocks
- *           beyond the matrix are written as 0, and read as 0 by the products.
+ *           beyond the matrix are written as 0.  Products read them: in a matrix that comes
+ *           from elsewhere, those of blocks beyond L have to be 0 too (255, a NaN, there
+ *           spoils its row); those of rows beyond R may hold anything.
  * Quantising a block with largest magnitude a:  s = max(0, floor(log2 a) + 125) (0 when a
  * is 0), codes are the nearest of the values above to x / 2^(s-127), ties to the even
  * code, magnitudes over 6 becoming 6; the sign bit is kept.  A block that holds a NaN or
