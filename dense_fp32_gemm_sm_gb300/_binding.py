@@ -1,5 +1,5 @@
 """Binding of the C ABI declared in ``include/fgemm.h``: ctypes, and a small C module for the
-MXFP4 calls.
+MXFP4 and 16-bit calls.
 
 Argument marshalling only: every call goes straight to ``libfgemm.so`` and the
 work runs in its CUDA kernels.  Matrices may be given as CUDA float32 torch
@@ -23,6 +23,8 @@ OP_N, OP_T = 0, 1
 OK, ERR_INVALID_VALUE, ERR_LAUNCH, ERR_NOT_SUPPORTED, ERR_TIMEOUT = 0, 1, 2, 3, 4
 MATH_FP32, MATH_TF32, MATH_3XTF32 = 0, 1, 2
 F32, BF16, F16 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
+MAX_GROUPS = 1024  # FGEMM_MAX_GROUPS of include/fgemm.h
 
 _lock = threading.Lock()
 _lib = None
@@ -113,6 +115,13 @@ def library() -> ctypes.CDLL:
                     ("plan", [_c_int] * 5, _c_int),
                     ("linear_workspace_size", [_c_int] * 3, _sz)):
                 fn = getattr(lib, "fgemm_mxfp4_" + name)
+                fn.argtypes = argtypes
+                fn.restype = restype
+            for name, argtypes, restype in (
+                    ("copy_workspace_size", [_c_int] * 6, _sz),
+                    ("sums_workspace_size", [_c_int] * 3, _sz),
+                    ("plan", [_c_int] * 7, _c_int)):
+                fn = getattr(lib, "fgemm_gemm16_" + name)
                 fn.argtypes = argtypes
                 fn.restype = restype
             lib.fgemm_config_name.restype = ctypes.c_char_p
@@ -378,12 +387,12 @@ def gemm_math_staged(math, transa, transb, M, N, K, alpha, A, lda, strideA, B, l
 # addresses like the functions above.  Tensors have to be on the current device (ValueError): the
 # library launches there.
 
-_TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16")
+_TYPE_NAMES = ("torch.float32", "torch.bfloat16", "torch.float16", "torch.int32")
 _calls = None
 
 
 def _type_of(dtype):
-    """fgemm_dtype value of a torch dtype (this module does not import torch), or -1."""
+    """fgemm_dtype value of a torch dtype (this module does not import torch), 3 for int32, or -1."""
     name = str(dtype)
     return _TYPE_NAMES.index(name) if name in _TYPE_NAMES else -1
 
@@ -415,8 +424,10 @@ def _native():
                 # Where torch sees one device, the calls need not ask which one is current (0.4 us).
                 one_device = sys.modules["torch"].cuda.device_count() == 1
             module.bind(_type_of, raw_stream, device, one_device,
-                        *(ctypes.cast(getattr(lib, "fgemm_mxfp4_" + name), _c_vp).value
-                          for name in ("quantize", "quantize_grad", "dequantize", "gemm", "linear")))
+                        *(ctypes.cast(getattr(lib, "fgemm_" + name), _c_vp).value
+                          for name in ("mxfp4_quantize", "mxfp4_quantize_grad", "mxfp4_dequantize", "mxfp4_gemm",
+                                       "mxfp4_linear", "gemm16", "gemm16_grad", "gemm16_grouped",
+                                       "gemm16_grouped_grad", "gemm16_weight_grad", "act16_grad")))
             _calls = module
     return _calls
 
@@ -497,3 +508,86 @@ def mxfp4_linear(type, M, N, K, X, ldx, W_codes, ld_W_codes, W_scales, bias, app
     if check:
         _check(st, "fgemm_mxfp4_linear")
     return st
+
+
+# ---- 16-bit layers (see "16-bit layers" in include/fgemm.h) ---------------------------
+
+# A, B, Z, G and D are tensors of `type`, R and Y (C) of `out_type`, bias and col_sums float32, offsets
+# int32 on the device; any of them may be an address.  Through the C module, like the MXFP4 calls.
+
+
+def gemm16_copy_workspace_size(transa, transb, groups, M, N, K) -> int:
+    """``fgemm_gemm16_copy_workspace_size``: bytes for copies of A and B whose rows are not on 16 bytes."""
+    return int(library().fgemm_gemm16_copy_workspace_size(int(transa), int(transb), groups, M, N, K))
+
+
+def gemm16_sums_workspace_size(groups, M, N) -> int:
+    """``fgemm_gemm16_sums_workspace_size``: bytes for the partial column sums of an M x N output."""
+    return int(library().fgemm_gemm16_sums_workspace_size(groups, M, N))
+
+
+def gemm16(type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, bias, act, Z, ldz, beta, R, ldr, Y, ldy,
+           workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_gemm16``: Z = alpha op(A) op(B) + bias (kept unless None), Y = act(Z) + beta R."""
+    st = (_calls or _native()).gemm16(type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, bias, act, Z, ldz,
+                                     beta, R, ldr, Y, ldy, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_gemm16")
+    return st
+
+
+def gemm16_grad(type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, act, Z, ldz, Y, ldy, col_sums=None,
+                workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_gemm16_grad``: Y = (alpha op(A) op(B)) act'(Z), and the sums of its columns."""
+    st = (_calls or _native()).gemm16_grad(type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, act, Z, ldz,
+                                          Y, ldy, col_sums, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_gemm16_grad")
+    return st
+
+
+def gemm16_grouped(type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B, ldb, strideB, bias, act, Z, ldz,
+                   beta, R, ldr, Y, ldy, workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_gemm16_grouped``: ``gemm16`` with B and bias of each group of rows."""
+    st = (_calls or _native()).gemm16_grouped(type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B, ldb,
+                                             strideB, bias, act, Z, ldz, beta, R, ldr, Y, ldy, workspace,
+                                             workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_gemm16_grouped")
+    return st
+
+
+def gemm16_grouped_grad(type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B, ldb, strideB, act, Z, ldz,
+                        Y, ldy, col_sums=None, workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_gemm16_grouped_grad``: ``gemm16_grad`` with B of each group of rows."""
+    st = (_calls or _native()).gemm16_grouped_grad(type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B,
+                                                  ldb, strideB, act, Z, ldz, Y, ldy, col_sums, workspace,
+                                                  workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_gemm16_grouped_grad")
+    return st
+
+
+def gemm16_weight_grad(type, out_type, groups, M, N, K, offsets, alpha, A, lda, G, ldg, beta, C, ldc, strideC,
+                       workspace=None, workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_gemm16_weight_grad``: C_e = alpha A_e^T G_e + beta C_e over each group's rows."""
+    st = (_calls or _native()).gemm16_weight_grad(type, out_type, groups, M, N, K, offsets, alpha, A, lda, G, ldg, beta,
+                                                 C, ldc, strideC, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_gemm16_weight_grad")
+    return st
+
+
+def act16_grad(type, groups, M, N, offsets, act, G, ldg, Z, ldz, D, ldd, col_sums=None, workspace=None,
+               workspace_bytes=0, stream=None, check=True) -> int:
+    """``fgemm_act16_grad``: D = G act'(Z), and the sums of its columns for each group."""
+    st = (_calls or _native()).act16_grad(type, groups, M, N, offsets, act, G, ldg, Z, ldz, D, ldd, col_sums, workspace,
+                                         workspace_bytes, stream)
+    if check:
+        _check(st, "fgemm_act16_grad")
+    return st
+
+
+def gemm16_plan(grouped, groups, M, N, K, sums, num_sms) -> int:
+    """``fgemm_gemm16_plan``: 16 * rows of a tile + ranks (0: pairs) of a product's kernel; host-only."""
+    return library().fgemm_gemm16_plan(grouped, groups, M, N, K, 1 if sums else 0, num_sms)

@@ -1,0 +1,84 @@
+// gemm16.h -- what the units of the 16-bit layers share: the arguments of a product and of the
+// passes around it, and the launchers behind the C entries.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fgemm.h"
+
+namespace fgemm {
+namespace h16 {
+
+// A product, or one a group:  P = alpha op(A) op(B),  then the epilogue.
+//   RAGGED_NONE   one product
+//   RAGGED_ROWS   group e: rows offsets[e] .. offsets[e+1] of A and of the outputs, with B_e
+//   RAGGED_DEPTH  group e: those rows are what is summed over, Y_e is an output of its own
+enum Ragged { RAGGED_NONE = 0, RAGGED_ROWS = 1, RAGGED_DEPTH = 2 };
+
+struct Product {
+    fgemm_dtype type, out_type;
+    int M, N, K;  // of the outputs (all groups' rows for RAGGED_ROWS), and the depth (all groups' for RAGGED_DEPTH)
+    int ta, tb;   // A stored K x M, B stored N x K
+    float alpha;
+    const void *a, *b;
+    long long lda, ldb, stride_b;
+    int ragged, groups;
+    const int *offsets;  // device, groups + 1
+    // Epilogue.  slope == 0: Y = act(P + bias) + beta R, Z (if any) = P + bias.  slope != 0: Y = P act'(Z).
+    int act, slope;
+    const float *bias;  // N floats a group
+    void *z;
+    long long ldz;
+    float beta;
+    const void *r;
+    long long ldr;
+    void *y;
+    long long ldy, stride_y;
+    // Column sums of Y: partial ones, `partials` rows of N floats of room, and the first row of each group.
+    float *partial;
+    int *partial_start;
+    long long partials;
+};
+
+// How a product runs: tiles of 128 (pair: 256) columns of the output by at most nt rows; a tile's
+// depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs).
+struct Plan {
+    int pair, nt, ranks, per_sm;
+};
+Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, int sms);
+
+// Least rows of a tile where column sums are wanted, which bounds their partial sums.
+constexpr int SUMS_ROWS = 32;
+// Partial sums of columns: two of every tile of rows, or one of every 64 rows (act16_grad).
+inline long long partial_rows(long long groups, long long M) { return 2 * ((M + SUMS_ROWS - 1) / SUMS_ROWS + groups); }
+
+fgemm_status launch_product(const Product &q, cudaStream_t stream);
+template <class T> fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream);
+
+// Y (rows x cols, ldy a multiple of 8) = X (ldx), 16-bit elements, for `batch` matrices stride_x
+// elements apart (Y's follow each other).
+fgemm_status launch_realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch,
+                            void *y, long long ldy, cudaStream_t stream);
+
+struct ActGrad {
+    fgemm_dtype type;
+    int act, groups, M, N;
+    const int *offsets;  // or null: one group of all rows
+    const void *g, *z;
+    void *d;
+    long long ldg, ldz, ldd;
+    float *partial;  // or null: no sums
+};
+// Slices of a group's rows, each with a partial sum.
+long long act_slices(long long groups, long long M);
+fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream);
+
+// sums[e][j] = the partial rows start[e] .. start[e+1] of column j, in order (start == null: `each` a group).
+fgemm_status launch_sums(const float *partial, const int *start, long long each, int groups, int N, float *sums,
+                         cudaStream_t stream);
+
+}  // namespace h16
+}  // namespace fgemm

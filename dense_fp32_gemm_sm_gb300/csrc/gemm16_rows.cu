@@ -1,0 +1,176 @@
+// gemm16_rows.cu -- the passes around the 16-bit products: rows copied to 16-byte boundaries, the
+// gradient through an activation with its column sums, and the adding up of partial column sums.
+#include <cuda_runtime.h>
+
+#include "fgemm_internal.h"
+#include "gemm16.h"
+#include "gemm16_device.cuh"
+#include "mxfp4_launch.h"
+
+namespace fgemm {
+namespace h16 {
+namespace {
+
+// ---- rows on 16-byte boundaries ----------------------------------------------------------
+
+// A thread makes 16 bytes of a row.  Bounded by its reads, 2 bytes a lane and instruction, of which eight
+// share their sectors in L1.
+__global__ void __launch_bounds__(256) realign_kernel(const uint16_t *x, long long ldx, long long stride_x, long long rows, int cols,
+                                                      long long total, uint4 *y, int pieces)
+{
+    after_previous_kernel();
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = i / pieces;
+        const int c0 = (int)(i - row * pieces) * 8;
+        const long long m = row / rows;
+        const uint16_t *const src = x + m * stride_x + (row - m * rows) * ldx + c0;
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c0 + j < cols ? src[j] : 0;
+        y[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+
+// ---- the gradient through an activation --------------------------------------------------
+
+constexpr int ACT_COLUMNS = 256;  // of a block: eight a lane
+constexpr int ACT_WARPS = 8;      // rows of a block at a time
+constexpr int SLICE_ROWS = 64;
+
+// D = G act'(Z) for a slice of a group's rows by 256 columns, and its column sums.  VEC: a lane's eight
+// columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(32 * ACT_WARPS) act_grad_kernel(ActGrad p, int strips, int slices)
+{
+    __shared__ float sums[ACT_WARPS][ACT_COLUMNS];
+    after_previous_kernel();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int strip = blockIdx.x % strips, part = blockIdx.x / strips, e = part / slices, slice = part % slices;
+    long long first = 0, rows = p.M;
+    if (p.offsets) {
+        const int a = max(0, min(p.offsets[e], p.M)), b = max(0, min(p.offsets[e + 1], p.M));
+        first = a;
+        rows = max(b - a, 0);
+    }
+    const long long from = first + rows * slice / slices, to = first + rows * (slice + 1) / slices;
+    const int c0 = strip * ACT_COLUMNS;
+    auto column = [&](int j) { return c0 + (VEC ? 8 * lane + j : lane + 32 * j); };
+    float sum[8] = {};
+    const T *const G = static_cast<const T *>(p.g);
+    const T *const Z = static_cast<const T *>(p.z);
+    T *const D = static_cast<T *>(p.d);
+    const bool gated = p.act != FGEMM_ACT_NONE;
+    if (column(0) < p.N) {
+#pragma unroll 2
+        for (long long r = from + warp; r < to; r += ACT_WARPS) {
+            __align__(16) T g[8], z[8];
+            if (VEC) {
+                *reinterpret_cast<uint4 *>(g) = *reinterpret_cast<const uint4 *>(G + r * p.ldg + column(0));
+                if (gated) *reinterpret_cast<uint4 *>(z) = *reinterpret_cast<const uint4 *>(Z + r * p.ldz + column(0));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = column(j) < p.N;
+                    g[j] = in ? G[r * p.ldg + column(j)] : from_float<T>(0.0f);
+                    if (gated) z[j] = in ? Z[r * p.ldz + column(j)] : from_float<T>(0.0f);
+                }
+            }
+            __align__(16) T d[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = to_float(g[j]);
+                if (gated) v = through(v, to_float(z[j]), p.act);
+                sum[j] += v;
+                d[j] = from_float<T>(v);
+            }
+            if (D) {
+                if (VEC) {
+                    *reinterpret_cast<uint4 *>(D + r * p.ldd + column(0)) = *reinterpret_cast<const uint4 *>(d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (column(j) < p.N) D[r * p.ldd + column(j)] = d[j];
+                }
+            }
+        }
+    }
+    if (p.partial) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[warp][column(j) - c0] = sum[j];
+        __syncthreads();
+        const int n = c0 + (int)threadIdx.x;
+        if (n < p.N) {
+            float total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < ACT_WARPS; ++w) total += sums[w][threadIdx.x];
+            p.partial[(long long)part * p.N + n] = total;
+        }
+    }
+}
+
+// ---- partial column sums -----------------------------------------------------------------
+
+// 32 columns of a group by 8 warps, each adding up every eighth row; then the warps' sums, in order.
+__global__ void __launch_bounds__(256) sums_kernel(const float *partial, const int *start, long long each, int strips, int N, float *sums)
+{
+    __shared__ float part[8][32];
+    after_previous_kernel();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int strip = blockIdx.x % strips, e = blockIdx.x / strips, n = strip * 32 + lane;
+    const long long from = start ? start[e] : each * e, to = start ? start[e + 1] : each * (e + 1);
+    float sum = 0.0f;
+    if (n < N) {
+#pragma unroll 4
+        for (long long r = from + warp; r < to; r += 8) sum += partial[r * N + n];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && n < N) {
+#pragma unroll
+        for (int w = 1; w < 8; ++w) sum += part[w][lane];
+        sums[(long long)e * N + n] = sum;
+    }
+}
+
+bool vectors(const void *p, long long ld) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); }
+
+fgemm_status status(cudaError_t e) { return e == cudaSuccess ? FGEMM_OK : FGEMM_ERR_LAUNCH; }
+
+}  // namespace
+
+fgemm_status launch_realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch, void *y,
+                            long long ldy, cudaStream_t stream)
+{
+    const int pieces = (int)(ldy / 8);
+    const long long total = rows * batch * pieces, blocks = (total + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 152 * 64 ? blocks : 152 * 64));
+    return status(mx::launch(realign_kernel, grid, 256, 0, stream, 1, static_cast<const uint16_t *>(x), ldx, stride_x, rows, cols,
+                             total, static_cast<uint4 *>(y), pieces));
+}
+
+long long act_slices(long long groups, long long M)
+{
+    const long long rows = (M + groups - 1) / groups;
+    return rows > SLICE_ROWS ? (rows + SLICE_ROWS - 1) / SLICE_ROWS : 1;
+}
+
+fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream)
+{
+    const int strips = (p.N - 1) / ACT_COLUMNS + 1;
+    const long long slices = act_slices(p.groups, p.M), blocks = strips * slices * p.groups;
+    if (blocks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
+    const bool vec = p.N % 8 == 0 && vectors(p.g, p.ldg) && vectors(p.z, p.ldz) && vectors(p.d, p.ldd);
+    const auto kernel = p.type == FGEMM_BF16 ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
+                                             : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);
+    return status(mx::launch(kernel, dim3((unsigned)blocks), 32 * ACT_WARPS, 0, stream, 1, p, strips, (int)slices));
+}
+
+fgemm_status launch_sums(const float *partial, const int *start, long long each, int groups, int N, float *sums, cudaStream_t stream)
+{
+    const int strips = (N - 1) / 32 + 1;
+    if ((long long)strips * groups > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
+    return status(mx::launch(sums_kernel, dim3((unsigned)(strips * groups)), 256, 0, stream, 1, partial, start, each, strips, N, sums));
+}
+
+}  // namespace h16
+}  // namespace fgemm

@@ -1,4 +1,4 @@
-/* py_calls.c -- the Python side of the MXFP4 entry points: arguments from Python objects to
+/* py_calls.c -- the Python side of the MXFP4 and 16-bit entry points: arguments from Python objects to
  * the C calls of include/fgemm.h.  (Of a small call's 5 us on the host, ctypes and conversions
  * in Python took 3; here they take under 1.)
  *
@@ -20,7 +20,23 @@ static struct {
                          float, void *, int, const float *, int, cudaStream_t);
     fgemm_status (*linear)(fgemm_dtype, int, int, int, const void *, int, const void *, int, const void *, const float *, int,
                            void *, int, void *, size_t, cudaStream_t);
+    fgemm_status (*gemm16)(fgemm_dtype, fgemm_dtype, fgemm_op, fgemm_op, int, int, int, float, const void *, int, const void *, int,
+                           const float *, fgemm_activation, void *, int, float, const void *, int, void *, int, void *, size_t,
+                           cudaStream_t);
+    fgemm_status (*gemm16_grad)(fgemm_dtype, fgemm_dtype, fgemm_op, fgemm_op, int, int, int, float, const void *, int, const void *,
+                                int, fgemm_activation, const void *, int, void *, int, float *, void *, size_t, cudaStream_t);
+    fgemm_status (*gemm16_grouped)(fgemm_dtype, fgemm_dtype, fgemm_op, int, int, int, int, const int *, float, const void *, int,
+                                   const void *, int, long long, const float *, fgemm_activation, void *, int, float, const void *,
+                                   int, void *, int, void *, size_t, cudaStream_t);
+    fgemm_status (*gemm16_grouped_grad)(fgemm_dtype, fgemm_dtype, fgemm_op, int, int, int, int, const int *, float, const void *,
+                                        int, const void *, int, long long, fgemm_activation, const void *, int, void *, int,
+                                        float *, void *, size_t, cudaStream_t);
+    fgemm_status (*gemm16_weight_grad)(fgemm_dtype, fgemm_dtype, int, int, int, int, const int *, float, const void *, int,
+                                       const void *, int, float, void *, int, long long, void *, size_t, cudaStream_t);
+    fgemm_status (*act16_grad)(fgemm_dtype, int, int, int, const int *, fgemm_activation, const void *, int, const void *, int,
+                               void *, int, float *, void *, size_t, cudaStream_t);
 } entry;
+enum { ENTRIES = 11 };
 static PyObject *type_of;     /* Python: torch dtype -> fgemm_dtype value or -1 */
 static PyObject *raw_stream;  /* torch's (device index) -> current stream's handle */
 static PyObject *current_device;  /* torch's () -> current device's index */
@@ -30,6 +46,8 @@ static PyObject *s_is_cuda, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_
 static PyObject *known_type[8];
 static long known_value[8];
 static int known;
+
+enum { TYPE_I32 = 3 };  /* type_of's value for 32-bit integers, behind those of fgemm_dtype */
 
 static long element_type(PyObject *dtype)
 {
@@ -156,6 +174,12 @@ static int integer(PyObject *x, int *out)
     return 1;
 }
 
+static int wide(PyObject *x, long long *out)
+{
+    *out = PyLong_AsLongLong(x);
+    return *out != -1 || !PyErr_Occurred();
+}
+
 static int number(PyObject *x, float *out)
 {
     const double v = PyFloat_AsDouble(x);
@@ -189,6 +213,8 @@ static int count(const char *name, Py_ssize_t n, Py_ssize_t want)
 #define MATRIX(i, v) address(a[i], type, &device, (void **)&v)
 #define RAW(i, v) address(a[i], -1, &device, (void **)&v)
 #define FLOATS(i, v) address(a[i], FGEMM_F32, &device, (void **)&v)
+#define OUT(i, v) address(a[i], out_type, &device, (void **)&v)
+#define INTS(i, v) address(a[i], TYPE_I32, &device, (void **)&v)
 
 /* (type, M, N, X, ldx, row_codes, ld, row_scales, col_codes, ld, col_scales, stream) */
 static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -268,13 +294,135 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n)
     RETURN_CALL(entry.linear((fgemm_dtype)type, M, N, K, x, ldx, wc, ldw, ws, bias, relu, y, ldy, space, size, stream));
 }
 
-/* (type_of, raw_stream, current_device, one_device, addresses of quantize, quantize_grad, dequantize, gemm, linear) */
+/* (type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, bias, act, Z, ldz, beta, R, ldr, Y, ldy, workspace, bytes, stream) */
+static PyObject *gemm16(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, out_type, ta, tb, M, N, K, lda, ldb, act, ldz, ldr, ldy;
+    float alpha, beta;
+    void *A, *B, *Z, *R, *Y, *ws;
+    float *bias;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("gemm16", n, 24) || !INT(0, type) || !INT(1, out_type) || !INT(2, ta) || !INT(3, tb) || !INT(4, M) || !INT(5, N) ||
+        !INT(6, K) || !number(a[7], &alpha) || !MATRIX(8, A) || !INT(9, lda) || !MATRIX(10, B) || !INT(11, ldb) ||
+        !FLOATS(12, bias) || !INT(13, act) || !MATRIX(14, Z) || !INT(15, ldz) || !number(a[16], &beta) || !OUT(17, R) ||
+        !INT(18, ldr) || !OUT(19, Y) || !INT(20, ldy) || !RAW(21, ws) || !bytes(a[22], &size) || !stream_of(a[23], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.gemm16((fgemm_dtype)type, (fgemm_dtype)out_type, (fgemm_op)ta, (fgemm_op)tb, M, N, K, alpha, A, lda, B, ldb,
+                             bias, (fgemm_activation)act, Z, ldz, beta, R, ldr, Y, ldy, ws, size, stream));
+}
+
+/* (type, out_type, transa, transb, M, N, K, alpha, A, lda, B, ldb, act, Z, ldz, Y, ldy, col_sums, workspace, bytes, stream) */
+static PyObject *gemm16_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, out_type, ta, tb, M, N, K, lda, ldb, act, ldz, ldy;
+    float alpha;
+    void *A, *B, *Z, *Y, *ws;
+    float *sums;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("gemm16_grad", n, 21) || !INT(0, type) || !INT(1, out_type) || !INT(2, ta) || !INT(3, tb) || !INT(4, M) ||
+        !INT(5, N) || !INT(6, K) || !number(a[7], &alpha) || !MATRIX(8, A) || !INT(9, lda) || !MATRIX(10, B) || !INT(11, ldb) ||
+        !INT(12, act) || !MATRIX(13, Z) || !INT(14, ldz) || !OUT(15, Y) || !INT(16, ldy) || !FLOATS(17, sums) || !RAW(18, ws) ||
+        !bytes(a[19], &size) || !stream_of(a[20], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.gemm16_grad((fgemm_dtype)type, (fgemm_dtype)out_type, (fgemm_op)ta, (fgemm_op)tb, M, N, K, alpha, A, lda, B,
+                                  ldb, (fgemm_activation)act, Z, ldz, Y, ldy, sums, ws, size, stream));
+}
+
+/* (type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B, ldb, strideB, bias, act, Z, ldz, beta, R, ldr, Y, ldy, workspace,
+ * bytes, stream) */
+static PyObject *gemm16_grouped(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, out_type, tb, groups, M, N, K, lda, ldb, act, ldz, ldr, ldy;
+    float alpha, beta;
+    void *A, *B, *Z, *R, *Y, *ws;
+    int *offsets;
+    long long strideB;
+    float *bias;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("gemm16_grouped", n, 26) || !INT(0, type) || !INT(1, out_type) || !INT(2, tb) || !INT(3, groups) || !INT(4, M) ||
+        !INT(5, N) || !INT(6, K) || !INTS(7, offsets) || !number(a[8], &alpha) || !MATRIX(9, A) || !INT(10, lda) ||
+        !MATRIX(11, B) || !INT(12, ldb) || !wide(a[13], &strideB) || !FLOATS(14, bias) || !INT(15, act) || !MATRIX(16, Z) ||
+        !INT(17, ldz) || !number(a[18], &beta) || !OUT(19, R) || !INT(20, ldr) || !OUT(21, Y) || !INT(22, ldy) || !RAW(23, ws) ||
+        !bytes(a[24], &size) || !stream_of(a[25], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.gemm16_grouped((fgemm_dtype)type, (fgemm_dtype)out_type, (fgemm_op)tb, groups, M, N, K, offsets, alpha, A, lda,
+                                     B, ldb, strideB, bias, (fgemm_activation)act, Z, ldz, beta, R, ldr, Y, ldy, ws, size, stream));
+}
+
+/* (type, out_type, transb, groups, M, N, K, offsets, alpha, A, lda, B, ldb, strideB, act, Z, ldz, Y, ldy, col_sums, workspace, bytes,
+ * stream) */
+static PyObject *gemm16_grouped_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, out_type, tb, groups, M, N, K, lda, ldb, act, ldz, ldy;
+    float alpha;
+    void *A, *B, *Z, *Y, *ws;
+    int *offsets;
+    long long strideB;
+    float *sums;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("gemm16_grouped_grad", n, 23) || !INT(0, type) || !INT(1, out_type) || !INT(2, tb) || !INT(3, groups) || !INT(4, M) ||
+        !INT(5, N) || !INT(6, K) || !INTS(7, offsets) || !number(a[8], &alpha) || !MATRIX(9, A) || !INT(10, lda) ||
+        !MATRIX(11, B) || !INT(12, ldb) || !wide(a[13], &strideB) || !INT(14, act) || !MATRIX(15, Z) || !INT(16, ldz) ||
+        !OUT(17, Y) || !INT(18, ldy) || !FLOATS(19, sums) || !RAW(20, ws) || !bytes(a[21], &size) ||
+        !stream_of(a[22], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.gemm16_grouped_grad((fgemm_dtype)type, (fgemm_dtype)out_type, (fgemm_op)tb, groups, M, N, K, offsets, alpha, A,
+                                          lda, B, ldb, strideB, (fgemm_activation)act, Z, ldz, Y, ldy, sums, ws, size, stream));
+}
+
+/* (type, out_type, groups, M, N, K, offsets, alpha, A, lda, G, ldg, beta, C, ldc, strideC, workspace, bytes, stream) */
+static PyObject *gemm16_weight_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, out_type, groups, M, N, K, lda, ldg, ldc;
+    float alpha, beta;
+    void *A, *G, *C, *ws;
+    int *offsets;
+    long long strideC;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("gemm16_weight_grad", n, 19) || !INT(0, type) || !INT(1, out_type) || !INT(2, groups) || !INT(3, M) || !INT(4, N) ||
+        !INT(5, K) || !INTS(6, offsets) || !number(a[7], &alpha) || !MATRIX(8, A) || !INT(9, lda) || !MATRIX(10, G) ||
+        !INT(11, ldg) || !number(a[12], &beta) || !OUT(13, C) || !INT(14, ldc) || !wide(a[15], &strideC) || !RAW(16, ws) ||
+        !bytes(a[17], &size) || !stream_of(a[18], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.gemm16_weight_grad((fgemm_dtype)type, (fgemm_dtype)out_type, groups, M, N, K, offsets, alpha, A, lda, G, ldg,
+                                         beta, C, ldc, strideC, ws, size, stream));
+}
+
+/* (type, groups, M, N, offsets, act, G, ldg, Z, ldz, D, ldd, col_sums, workspace, bytes, stream) */
+static PyObject *act16_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    int type, groups, M, N, act, ldg, ldz, ldd;
+    void *G, *Z, *D, *ws;
+    int *offsets;
+    float *sums;
+    size_t size;
+    cudaStream_t stream;
+    long device = -1;
+    if (!count("act16_grad", n, 16) || !INT(0, type) || !INT(1, groups) || !INT(2, M) || !INT(3, N) || !INTS(4, offsets) ||
+        !INT(5, act) || !MATRIX(6, G) || !INT(7, ldg) || !MATRIX(8, Z) || !INT(9, ldz) || !MATRIX(10, D) || !INT(11, ldd) ||
+        !FLOATS(12, sums) || !RAW(13, ws) || !bytes(a[14], &size) || !stream_of(a[15], device, &stream))
+        return NULL;
+    RETURN_CALL(entry.act16_grad((fgemm_dtype)type, groups, M, N, offsets, (fgemm_activation)act, G, ldg, Z, ldz, D, ldd, sums, ws,
+                                 size, stream));
+}
+
+/* (type_of, raw_stream, current_device, one_device, the entries' addresses in their order above) */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
-    void *p[5];
+    void *p[ENTRIES];
     long device = -1;
-    if (!count("bind", n, 9)) return NULL;
-    for (int i = 0; i < 5; ++i)
+    if (!count("bind", n, 4 + ENTRIES)) return NULL;
+    for (int i = 0; i < ENTRIES; ++i)
         if (!address(a[4 + i], -1, &device, &p[i])) return NULL;
     const int one = PyObject_IsTrue(a[3]);
     if (one < 0) return NULL;
@@ -288,13 +436,21 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n)
     *(void **)&entry.dequantize = p[2];
     *(void **)&entry.gemm = p[3];
     *(void **)&entry.linear = p[4];
+    *(void **)&entry.gemm16 = p[5];
+    *(void **)&entry.gemm16_grad = p[6];
+    *(void **)&entry.gemm16_grouped = p[7];
+    *(void **)&entry.gemm16_grouped_grad = p[8];
+    *(void **)&entry.gemm16_weight_grad = p[9];
+    *(void **)&entry.act16_grad = p[10];
     Py_RETURN_NONE;
 }
 
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(bind), METHOD(quantize), METHOD(quantize_grad), METHOD(dequantize),
-                                METHOD(gemm), METHOD(linear),   {NULL, NULL, 0, NULL}};
-static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "MXFP4 calls of libfgemm", -1, methods};
+                                METHOD(gemm), METHOD(linear), METHOD(gemm16), METHOD(gemm16_grad), METHOD(gemm16_grouped),
+                                METHOD(gemm16_grouped_grad), METHOD(gemm16_weight_grad), METHOD(act16_grad),
+                                {NULL, NULL, 0, NULL}};
+static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "MXFP4 and 16-bit calls of libfgemm", -1, methods};
 
 PyMODINIT_FUNC PyInit__calls(void)
 {

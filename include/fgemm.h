@@ -539,6 +539,122 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
                                 const float *bias, int apply_relu, void *Y, int ldy,
                                 void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 16-bit layers: products of BF16 or F16 matrices (FP32 sums) with a layer's epilogue, for one
+ * weight or for one of each group of rows (the experts of a mixture), and their gradients.
+ *
+ * With act one of
+ *     FGEMM_ACT_NONE  z            FGEMM_ACT_GELU  z Phi(z), Phi the normal distribution
+ *     FGEMM_ACT_RELU  max(0, z)    FGEMM_ACT_SILU  z / (1 + exp(-z))
+ * a layer is  Z = alpha op(A) op(B) + bias,  Y = act(Z) + beta R,  and the gradient of Z's
+ * layer, through its activation,  Y = (alpha op(A) op(B)) act'(Z).  act and act' are evaluated
+ * in FP32, forward on the unrounded Z; max(0, x) keeps a NaN; behind ReLU's gate (Z > 0 does not
+ * hold) a gradient is 0 whatever it was; act(-inf) is 0, and act' at an infinity its limit.
+ *
+ * `type` (FGEMM_BF16 or FGEMM_F16) is the element type of A, B and Z; `out_type` (the same or
+ * FGEMM_F32) that of Y and R.  bias and col_sums hold FP32.  Sums are formed in FP32 and each
+ * output is rounded once; col_sums are sums of Y before that rounding, in a fixed order.
+ * Matrices are row-major with leading dimensions in elements, as for fgemm_sgemm: A is M x K (K x M
+ * for transa = FGEMM_OP_T), B is K x N (N x K).  Pointers are aligned to an element; any alignment
+ * and leading dimension is accepted:
+ *   - A and B whose pointer, leading dimension (where there is more than one row) and strideB are
+ *     multiples of 16 bytes are read as they are.  Others are copied into the workspace first, at
+ *     each call: lay weights out with rows on 16 bytes.
+ *   - Y, Z, R take any (16-bit ones are fastest on 4 bytes with even leading dimensions and N).
+ * Of a matrix, nothing but its elements is read: what lies between rows does not matter.
+ * The conventions at the top of this file hold (device pointers, nothing allocated, asynchronous
+ * on `stream`, FGEMM_MAX_DIM, invalid arguments refused before anything is launched, graph capture).
+ * Outputs overlap neither inputs nor each other, but R may be Y (with ldr = ldy).  beta == 0 does not
+ * read R; alpha == 0 or K == 0 reads neither A nor B.  M == 0 or N == 0: nothing to do, but col_sums
+ * become 0.
+ *
+ * Workspace: 16-byte aligned device memory, used from the call until its kernels have run; calls that
+ * may run at the same time want one each.  It holds the copies (at most
+ * fgemm_gemm16_copy_workspace_size bytes; none for operands on 16 bytes) behind the partial column
+ * sums (fgemm_gemm16_sums_workspace_size bytes where col_sums is not NULL); where neither is wanted
+ * it may be NULL.
+ * ------------------------------------------------------------------------- */
+typedef enum fgemm_activation {
+    FGEMM_ACT_NONE = 0,
+    FGEMM_ACT_RELU = 1,
+    FGEMM_ACT_GELU = 2,
+    FGEMM_ACT_SILU = 3
+} fgemm_activation;
+
+/* The most groups that a call takes (more: FGEMM_ERR_NOT_SUPPORTED). */
+#define FGEMM_MAX_GROUPS 1024
+
+/* Bytes for the copies of both operands (`groups` matrices B; 1 for fgemm_gemm16), and for the partial
+ * column sums of an M x N output.  0 for a size below 1.  fgemm_gemm16_weight_grad copies as a product
+ * with transa = FGEMM_OP_T, one group, K in place of M, N, and M in place of K. */
+size_t fgemm_gemm16_copy_workspace_size(fgemm_op transa, fgemm_op transb, int groups, int M, int N, int K);
+size_t fgemm_gemm16_sums_workspace_size(int groups, int M, int N);
+
+/* Z = alpha op(A) op(B) + bias (bias: N floats or NULL), kept where Z is not NULL;
+ * Y = act(Z) + beta R.  (beta = 1, R = Y, act none: a product added to what is there.) */
+fgemm_status fgemm_gemm16(fgemm_dtype type, fgemm_dtype out_type, fgemm_op transa, fgemm_op transb,
+                          int M, int N, int K, float alpha, const void *A, int lda, const void *B,
+                          int ldb, const float *bias, fgemm_activation act, void *Z, int ldz,
+                          float beta, const void *R, int ldr, void *Y, int ldy, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* Y = (alpha op(A) op(B)) act'(Z) (Z, M x N, is read unless act is none), and col_sums (N floats or
+ * NULL): the sums of Y's columns.  For a layer Y2 = act(Z1) W2 + b2 with the gradient G of Y2:
+ * A = G, B = W2 (transposed), Z = Z1 give the gradient of Z1, and its column sums that of the bias. */
+fgemm_status fgemm_gemm16_grad(fgemm_dtype type, fgemm_dtype out_type, fgemm_op transa,
+                               fgemm_op transb, int M, int N, int K, float alpha, const void *A,
+                               int lda, const void *B, int ldb, fgemm_activation act, const void *Z,
+                               int ldz, void *Y, int ldy, float *col_sums, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * By groups of rows: rows offsets[e] .. offsets[e+1] - 1 of A (M x K), Z, R and Y (M x N) belong to
+ * group e, which has the matrix B + e strideB and the bias bias + e N; col_sums + e N are the
+ * sums of a group's rows (0 for a group without any).  offsets: groups + 1 ints in device memory,
+ * not decreasing, from 0 to M at most; a group may have no rows.  The host does not read them.  Rows before
+ * offsets[0] and from offsets[groups] on are left as they were.  (Offsets out of that order or range
+ * lead to no access outside the matrices; what the call then computes is not defined.)
+ */
+fgemm_status fgemm_gemm16_grouped(fgemm_dtype type, fgemm_dtype out_type, fgemm_op transb,
+                                  int groups, int M, int N, int K, const int *offsets, float alpha,
+                                  const void *A, int lda, const void *B, int ldb, long long strideB,
+                                  const float *bias, fgemm_activation act, void *Z, int ldz,
+                                  float beta, const void *R, int ldr, void *Y, int ldy,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+fgemm_status fgemm_gemm16_grouped_grad(fgemm_dtype type, fgemm_dtype out_type, fgemm_op transb,
+                                       int groups, int M, int N, int K, const int *offsets,
+                                       float alpha, const void *A, int lda, const void *B, int ldb,
+                                       long long strideB, fgemm_activation act, const void *Z,
+                                       int ldz, void *Y, int ldy, float *col_sums, void *workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/* The weights' gradient:  C_e = alpha A_e^T G_e + beta C_e  for the rows A_e of A (M x K) and G_e of
+ * G (M x N) of each group; C_e, K x N, is at C + e strideC (strideC >= (K - 1) ldc + N).  A group
+ * without rows gets beta C_e (0 for beta == 0). */
+fgemm_status fgemm_gemm16_weight_grad(fgemm_dtype type, fgemm_dtype out_type, int groups, int M,
+                                      int N, int K, const int *offsets, float alpha, const void *A,
+                                      int lda, const void *G, int ldg, float beta, void *C, int ldc,
+                                      long long strideC, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/* The gradient through a layer's own activation:  D = G act'(Z)  (M x N, all of `type`; Z is not read
+ * for act none), rounded once, and col_sums (N floats a group, or NULL), the sums of its columns before
+ * that rounding: the gradient of the bias.  D may be G or Z (with the same leading dimension), or NULL
+ * where only the sums are wanted.  offsets: as above, or NULL for one group of all rows. */
+fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const int *offsets,
+                              fgemm_activation act, const void *G, int ldg, const void *Z, int ldz,
+                              void *D, int ldd, float *col_sums, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * How a product runs on a GPU with `num_sms` SMs, as 16 * rows + ranks: tiles of 128 columns of Y by at
+ * most `rows` rows, each tile's depth divided among `ranks` CTAs; ranks 0: tiles of 256 columns by pairs of
+ * CTAs.  grouped 0: fgemm_gemm16 and its gradient (sums: with col_sums), 1: by groups, 2:
+ * fgemm_gemm16_weight_grad (sizes as that call has them).  -1 for arguments out of range.  Host-only: no CUDA call.
+ */
+int fgemm_gemm16_plan(int grouped, int groups, int M, int N, int K, int sums, int num_sms);
+
 #ifdef __cplusplus
 }
 #endif
