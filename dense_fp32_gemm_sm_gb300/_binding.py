@@ -120,7 +120,7 @@ def library() -> ctypes.CDLL:
             for name, argtypes, restype in (
                     ("copy_workspace_size", [_c_int] * 6, _sz),
                     ("sums_workspace_size", [_c_int] * 3, _sz),
-                    ("plan", [_c_int] * 7, _c_int)):
+                    ("plan", [_c_int] * 8, _c_int)):
                 fn = getattr(lib, "fgemm_gemm16_" + name)
                 fn.argtypes = argtypes
                 fn.restype = restype
@@ -588,6 +588,6 @@ def act16_grad(type, groups, M, N, offsets, act, G, ldg, Z, ldz, D, ldd, col_sum
     return st
 
 
-def gemm16_plan(grouped, groups, M, N, K, sums, num_sms) -> int:
-    """``fgemm_gemm16_plan``: 16 * rows of a tile + ranks (0: pairs) of a product's kernel; host-only."""
-    return library().fgemm_gemm16_plan(grouped, groups, M, N, K, 1 if sums else 0, num_sms)
+def gemm16_plan(out_type, grouped, groups, M, N, K, sums, num_sms) -> int:
+    """``fgemm_gemm16_plan``: 16 * rows of a tile + ranks (+ 8192: pairs, + 16384: in turns); host-only."""
+    return library().fgemm_gemm16_plan(out_type, grouped, groups, M, N, K, 1 if sums else 0, num_sms)

@@ -44,11 +44,12 @@ struct Product {
 };
 
 // How a product runs: tiles of 128 (pair: 256) columns of the output by at most nt rows; a tile's
-// depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs).
+// depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs or pairs); CTAs an
+// SM; and whether sums over a long depth are added up in turns (where they are kept in FP32: `fine`).
 struct Plan {
-    int pair, nt, ranks, per_sm;
+    int pair, nt, ranks, per_sm, in_turns;
 };
-Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, int sms);
+Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, bool fine, int sms);
 
 // Least rows of a tile where column sums are wanted, which bounds their partial sums.
 constexpr int SUMS_ROWS = 32;

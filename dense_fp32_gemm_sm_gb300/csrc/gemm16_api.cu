@@ -330,14 +330,15 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
     return launch_sums(p.partial, nullptr, act_slices(groups, M), groups, N, col_sums, stream);
 }
 
-int fgemm_gemm16_plan(int grouped, int groups, int M, int N, int K, int sums, int num_sms)
+int fgemm_gemm16_plan(fgemm_dtype out_type, int grouped, int groups, int M, int N, int K, int sums, int num_sms)
 {
     if (grouped < 0 || grouped > 2 || groups < 1 || groups > FGEMM_MAX_GROUPS || M < 1 || N < 1 || K < 1 || num_sms < 2 ||
         !dims_supported(M, N, K))
         return -1;
-    const Plan plan = grouped == 2 ? plan_product(K, N, M, RAGGED_DEPTH, groups, false, num_sms)
-                                   : plan_product(M, N, K, grouped ? RAGGED_ROWS : RAGGED_NONE, groups, sums != 0, num_sms);
-    return 16 * plan.nt + (plan.pair ? 0 : plan.ranks);
+    const bool fine = out_type == FGEMM_F32 || sums != 0;
+    const Plan plan = grouped == 2 ? plan_product(K, N, M, RAGGED_DEPTH, groups, false, fine, num_sms)
+                                   : plan_product(M, N, K, grouped ? RAGGED_ROWS : RAGGED_NONE, groups, sums != 0, fine, num_sms);
+    return 16384 * plan.in_turns + 8192 * plan.pair + 16 * plan.nt + plan.ranks;
 }
 
 }  // extern "C"

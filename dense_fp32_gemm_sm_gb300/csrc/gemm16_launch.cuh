@@ -52,10 +52,10 @@ static bool prepare(unsigned **err, int *sms)
 
 static bool paired(const void *p, long long ld, fgemm_dtype t) { return t != FGEMM_F32 && reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
-template <bool PAIR, class T, class O>
+template <bool PAIR, class T, class O, bool LONG>
 static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    constexpr auto kernel = &gemm16_kernel<PAIR, T, O>;
+    constexpr auto kernel = &gemm16_kernel<PAIR, T, O, LONG>;
     unsigned *err = nullptr;
     int sms = 0;
     if (!prepare<decltype(kernel), kernel>(&err, &sms)) {
@@ -63,8 +63,8 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
         return FGEMM_ERR_LAUNCH;
     }
     constexpr int columns = PAIR ? 2 * TILE_F : TILE_F;
-    const int ranks = PAIR ? 2 : plan.ranks;
-    if (ranks < 1 || ranks > 8) return FGEMM_ERR_NOT_SUPPORTED;
+    const int ctas = PAIR ? 2 : plan.ranks;
+    if (ctas < 1 || ctas > 8 || (LONG && !PAIR && plan.nt > 64)) return FGEMM_ERR_NOT_SUPPORTED;
     Args p;
     std::memset(&p, 0, sizeof(p));
     p.q = q;
@@ -78,23 +78,28 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     long long tiles = row_tiles * tiles_f;
     if (q.ragged == RAGGED_DEPTH) tiles *= q.groups;
     if (q.ragged == RAGGED_ROWS) tiles = (row_tiles + (q.groups < q.M ? q.groups : q.M)) * tiles_f;  // at most
-    if (tiles * ranks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
+    if (tiles * ctas > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
     p.tiles_t = (int)row_tiles;
     p.tiles_f = (int)tiles_f;
     const int own = PAIR ? p.nt / 2 : p.nt;  // rows of op(A) that a CTA brings
     // Boxes: a whole tile's where all tiles are alike, else small enough that a short tile brings little more.
     const int own_step = PAIR ? p.step / 2 : p.step;
-    p.x_box = q.ragged == RAGGED_ROWS ? (own < 64 ? own : own % 64 == 0 ? 64 : 16) : (own_step <= 256 ? own_step : 128);
-    const int x_bytes = q.ta ? (own + 63) / 64 * BLOCK_BYTES : (own + p.x_box - 1) / p.x_box * p.x_box * 128;
-    p.stage_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
+    p.x_box = q.ragged == RAGGED_ROWS ? (own < 64 ? own : 64) : own_step;
+    const int x_bytes = q.ta ? (own + 63) / 64 * BOX_BYTES : (own + p.x_box - 1) / p.x_box * p.x_box * 128;
+    p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
-    const int room = (plan.per_sm > 1 ? MOST_SMEM / plan.per_sm - 1024 : MOST_SMEM) - 1024 - table_bytes - bar_bytes(MAX_STAGES);
+    const int join_bytes = !PAIR && plan.ranks > 1 ? (p.nt + plan.ranks) * TILE_F * 4 : 0;  // (shares are rounded up)
+    const int room = (plan.per_sm > 1 ? MOST_SMEM / plan.per_sm - 1024 : MOST_SMEM) - 1024 - table_bytes - join_bytes -
+                     bar_bytes(MAX_STAGES) - 32;
+    p.blocks = room >= 6 * p.block_bytes ? 2 : 1;
+    p.stage_bytes = p.blocks * p.block_bytes;
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     if (p.stages < 2) return FGEMM_ERR_NOT_SUPPORTED;
     p.table = p.stages * p.stage_bytes + (bar_bytes(p.stages) + 15) / 16 * 16;
-    const int smem = 1024 + p.table + table_bytes;
-    p.acc_step = p.nt < 32 ? 32 : p.nt;
-    p.tmem_cols = 64;
+    p.join = p.table + (table_bytes + 15) / 16 * 16;
+    const int smem = 1024 + p.join + join_bytes;
+    p.acc_step = p.nt;
+    p.tmem_cols = 32;
     while (p.tmem_cols < 2 * p.acc_step) p.tmem_cols *= 2;
     if (p.tmem_cols > 512) return FGEMM_ERR_NOT_SUPPORTED;
     p.y_pairs = paired(q.y, q.ldy, q.out_type) && q.stride_y % 2 == 0 && q.N % 2 == 0;
@@ -110,18 +115,23 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
             return FGEMM_ERR_NOT_SUPPORTED;
     }
     const long long most = PAIR ? sms / 2 : (long long)sms * plan.per_sm;
-    const bool split = !PAIR && ranks > 1;
-    const dim3 grid((unsigned)(ranks * (split || tiles < most ? tiles : most)));
-    return mx::launch(kernel, grid, THREADS, (size_t)smem, stream, (unsigned)ranks, p, err) == cudaSuccess ? FGEMM_OK
+    const dim3 grid((unsigned)(ctas * ((!PAIR && plan.ranks > 1) || tiles < most ? tiles : most)));
+    return mx::launch(kernel, grid, threads_of(PAIR), (size_t)smem, stream, (unsigned)ctas, p, err) == cudaSuccess ? FGEMM_OK
                                                                                                         : FGEMM_ERR_LAUNCH;
+}
+
+template <class T, class O, bool LONG>
+static fgemm_status launch_kind(const Product &q, const Plan &plan, cudaStream_t stream)
+{
+    return plan.pair ? launch_instance<true, T, O, LONG>(q, plan, stream) : launch_instance<false, T, O, LONG>(q, plan, stream);
 }
 
 template <class T>
 fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream)
 {
     if (q.out_type == FGEMM_F32)
-        return plan.pair ? launch_instance<true, T, float>(q, plan, stream) : launch_instance<false, T, float>(q, plan, stream);
-    return plan.pair ? launch_instance<true, T, T>(q, plan, stream) : launch_instance<false, T, T>(q, plan, stream);
+        return plan.in_turns ? launch_kind<T, float, true>(q, plan, stream) : launch_kind<T, float, false>(q, plan, stream);
+    return plan.in_turns ? launch_kind<T, T, true>(q, plan, stream) : launch_kind<T, T, false>(q, plan, stream);
 }
 
 }  // namespace h16

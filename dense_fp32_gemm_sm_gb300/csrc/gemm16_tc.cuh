@@ -10,7 +10,9 @@
 // and alignment; a column sum is a sum in one lane; and a short tile (the end of a group, few
 // tokens) takes an MMA of as many columns as it has rows, in steps of 16.
 //
-// A stage is 64 deep: 128 bytes a row, the 128-byte swizzle's row.  Either operand may be stored
+// A stage is one or two blocks of a depth of 64: 128 bytes a row, the 128-byte swizzle's row.  (Two
+// where room for three such stages is left: a stage's way through the barriers takes the producer
+// and the MMA warp some 170 ns, which is what bounds short tiles.)  Either operand may be stored
 // along the depth (K-major boxes of 64 x rows) or across it (boxes of 64 rows x 64 deep); the
 // MMA takes both.  One warp streams stages by TMA, one issues MMAs, eight store the sums of the
 // tile before.
@@ -31,12 +33,15 @@ namespace fgemm {
 namespace h16 {
 
 constexpr int TILE_F = 128;      // columns of Y a CTA: tensor-memory lanes
-constexpr int DEPTH = 64;        // 16-bit elements of a stage: 128 bytes
-constexpr int THREADS = 320;     // producer, MMA, eight epilogue warps
-constexpr int EPI_WARPS = 8;
+constexpr int DEPTH = 64;        // 16-bit elements of a block: 128 bytes
+constexpr int SETS = 2;  // of four epilogue warps: one for 32 lanes of tensor memory each
+__host__ __device__ constexpr int threads_of(bool pair) { return 64 + 128 * SETS + (pair ? 32 : 0); }  // producer, MMA, epilogue; mender
+constexpr int CHUNK = 16;      // accumulator columns that a warp finishes at a time
+constexpr int LONG_DEPTH = 512;  // depth whose products the tensor core adds up, where sums are kept in FP32
 constexpr int MAX_STAGES = 12;
 constexpr int W_BYTES = TILE_F * 128;
-constexpr int BLOCK_BYTES = 64 * 128;  // a box of an operand stored across the depth
+constexpr int BOX_BYTES = 64 * 128;  // a box of an operand stored across the depth
+constexpr int MAX_BOXES = 4;            // of op(A), a stage and CTA
 constexpr int ROWS_SWEPT = 8;          // tiles of rows that are swept along the columns together
 
 struct Args {
@@ -47,20 +52,21 @@ struct Args {
     int tiles_t, tiles_f;    // of one product (RAGGED_ROWS: tiles_t is not known here)
     int x_box;               // rows of a box of A stored along the depth
     int stages, stage_bytes, acc_step, tmem_cols;
-    int table;               // offset in shared memory of the groups' table
+    int blocks, block_bytes;  // 64-deep blocks of a stage (1 or 2), each of op(B), then of op(A)
+    int table, join;         // offsets in shared memory: the groups' table, the sums that ranks send each other
     int y_pairs, z_pairs;    // pairs of columns are aligned
     unsigned long long wait_limit_ns;
     int withhold;
 };
 
 // Offsets in shared memory behind the ring: barriers, then the slot for tensor memory's address.
-__host__ __device__ constexpr int bar_bytes(int stages) { return (3 * stages + 5) * 8 + 8; }
+__host__ __device__ constexpr int bar_bytes(int stages) { return (4 * stages + 5) * 8 + 8; }
 
 // MMA descriptors.  Along the depth: as of the other tensor-core kernels.  Across it: boxes of 64 elements x
 // 64 deep, 128 bytes an entry of depth; 8 of depth are 1024 bytes apart (stride), 64 elements a box (leading).
 __device__ __forceinline__ uint64_t across_desc(uint32_t smem_addr)
 {
-    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(BLOCK_BYTES >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(BOX_BYTES >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
@@ -87,26 +93,53 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
             : "memory");
 }
 
-// A wait for an arrival of the other CTA of a pair, whose writes it makes visible.
-__device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, unsigned *err, unsigned code,
-                                             unsigned long long limit_ns)
+// A value that is the same in all lanes, kept in a register and known to be uniform.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ uint32_t test_wait(uint32_t bar, uint32_t parity)
 {
-    const uint64_t t0 = tc::global_timer();
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
+}
+
+// A bounded wait for a whole warp, with the same answer in all lanes, known to be uniform.  CLUSTER: what
+// another CTA wrote before it arrived is visible.  The clock is read only after some polls: reading it
+// takes longer than most waits.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned *err, unsigned code,
+                                          unsigned long long limit_ns)
+{
+    uint64_t t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
         uint32_t done;
-        asm volatile(
-            "{\n"
-            ".reg .pred p;\n"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n"
-            "}\n"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
+        if constexpr (CLUSTER)
+            asm volatile(
+                "{\n"
+                ".reg .pred p;\n"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                "selp.u32 %0, 1, 0, p;\n"
+                "}\n"
+                : "=r"(done)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            done = tc::mbar_try_wait(bar, parity);
         if (__all_sync(0xFFFFFFFFu, done)) return true;
-        if ((spin & 255u) == 0) {
+        if ((spin & 63u) == 0) {
             bool stop = *(volatile unsigned *)err != 0u;
-            if (!stop && tc::global_timer() - t0 > limit_ns) {
+            const uint64_t now = tc::global_timer();
+            if (t0 == 0) t0 = now;
+            if (!stop && now - t0 > limit_ns) {
                 atomicOr(err, code);
                 stop = true;
             }
@@ -115,46 +148,73 @@ __device__ __forceinline__ bool cluster_wait(uint32_t bar, uint32_t parity, unsi
     }
 }
 
+// Arrive on a barrier of another CTA of the cluster, without releasing writes to it: with
+// .release.cluster the arrival waits for this thread's stores to global memory (3000 cycles a tile).
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
 // A tile: rows t0 .. t0 + valid of the output, columns from f0, group e, depth k0 .. k0 + depth;
 // row_tile: its number among all tiles of rows.
 struct Tile {
     int t0, valid, f0, e, k0, depth, row_tile;
 };
 
-// The tiles of a product, for each role by itself.  Eight tiles of rows are swept along the columns
-// together, so that the tiles in flight share operands in L2.
+// The tiles of a product, for each role (a warp) by itself.  Eight tiles of rows are swept along the
+// columns together, so that the tiles in flight share operands in L2.  Each lane finds one of the CTA's
+// next 32 tiles: found one by one they took every role 1400 cycles a tile, divisions for the most part.
 struct Walk {
     const Args &p;
     const int *begin, *first;  // table: a group's first row, its first tile
-    int tile_f, group;
+    int tile_f, start, step, total, group;
+    Tile mine;
 
-    __device__ Walk(const Args &args, const int *table, int columns)
-        : p(args), begin(table), first(table + args.q.groups + 1), tile_f(columns), group(0)
+    __device__ Walk(const Args &args, const int *table, int columns, int first_tile, int tile_step)
+        : p(args), begin(table), first(table + args.q.groups + 1), tile_f(columns), start(first_tile), step(tile_step), group(0)
     {
+        if (p.q.ragged == RAGGED_ROWS)
+            total = __shfl_sync(0xFFFFFFFFu, first[p.q.groups], 0);
+        else
+            total = p.tiles_t * p.tiles_f * (p.q.ragged == RAGGED_DEPTH ? p.q.groups : 1);
+        mine = Tile{};
     }
 
-    __device__ __forceinline__ int tiles() const
+    // Whether there is a j-th tile of this CTA, and what it is.  j: 0, 1, 2, ...
+    __device__ __forceinline__ bool get(int j, Tile &o)
     {
-        if (p.q.ragged == RAGGED_ROWS) return first[p.q.groups];
-        return p.tiles_t * p.tiles_f * (p.q.ragged == RAGGED_DEPTH ? p.q.groups : 1);
+        if (start + (long long)j * step >= total) return false;
+        if (j % 32 == 0) mine = find((int)min(start + (long long)(j + (int)(threadIdx.x & 31)) * step, total - 1ll));
+        // (Through shuffles, so that loops over a tile are known to be uniform: in others an MMA takes 128
+        // cycles to issue, and 16 of depth of a 128 x 16 tile as long as of a 256 x 256 one.)
+        int *const to = reinterpret_cast<int *>(&o);
+        const int *const from = reinterpret_cast<const int *>(&mine);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Tile) / sizeof(int)); ++i) to[i] = __shfl_sync(0xFFFFFFFFu, from[i], j % 32);
+        return true;
     }
 
-    __device__ __forceinline__ Tile at(int t)
+    // Tile t; a lane asks for ever later ones.
+    __device__ __forceinline__ Tile find(int t)
     {
         Tile o;
-        int tiles_t = p.tiles_t, step = p.step, rows = p.q.M, row0 = 0, row_tile0 = 0;
+        int tiles_t = p.tiles_t, height_t = p.step, rows = p.q.M, row0 = 0, row_tile0 = 0;
         o.e = 0;
         o.k0 = 0;
         o.depth = p.q.K;
         if (p.q.ragged == RAGGED_ROWS) {
-            while (t >= first[group + 1]) ++group;  // (t only grows)
+            while (t >= first[group + 1]) ++group;
             o.e = group;
             tiles_t = (first[group + 1] - first[group]) / p.tiles_f;
             t -= first[group];
             row0 = begin[group];
             rows = begin[group + 1] - row0;
-            step = ((rows + tiles_t - 1) / tiles_t + 31) & ~31;
-            step = min(step, p.nt);
+            height_t = min(((rows + tiles_t - 1) / tiles_t + 31) & ~31, p.nt);
             row_tile0 = first[group] / p.tiles_f;
         } else if (p.q.ragged == RAGGED_DEPTH) {
             const int per = p.tiles_t * p.tiles_f;
@@ -167,8 +227,8 @@ struct Walk {
         const int height = min(tiles_t - sweep * ROWS_SWEPT, ROWS_SWEPT);
         const int i = sweep * ROWS_SWEPT + in % height;
         o.f0 = in / height * tile_f;
-        o.t0 = row0 + i * step;
-        o.valid = min(step, rows - i * step);
+        o.t0 = row0 + i * height_t;
+        o.valid = min(height_t, rows - i * height_t);
         o.row_tile = row_tile0 + i;
         if (p.q.alpha == 0.0f) o.depth = 0;
         return o;
@@ -213,118 +273,120 @@ __device__ __forceinline__ void make_table(const Args &p, int *table, int lane)
 // ---- epilogue ---------------------------------------------------------------------------
 
 // Elements [row c][this lane's column], c < rows, into v.
-template <class T>
-__device__ __forceinline__ void load_rows(float (&v)[32], const T *src, long long ld, int rows, bool in)
+template <class T, int N>
+__device__ __forceinline__ void load_rows(float (&v)[N], const T *src, long long ld, int rows, bool in)
 {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = in && c < rows ? to_float(src[c * ld]) : 0.0f;
+    for (int c = 0; c < N; ++c, src += ld) v[c] = in && c < rows ? to_float(*src) : 0.0f;
 }
 
 // Store v to rows c < rows of this lane's column.  16-bit types, where pairs of columns are aligned:
 // lanes 2i and 2i + 1 exchange their values of two rows, and each stores both columns of one.
-template <class T>
-__device__ __forceinline__ void store_rows(T *out, long long ld, const float (&v)[32], int rows, bool in, bool pairs)
+template <class T, int N>
+__device__ __forceinline__ void store_rows(T *out, long long ld, const float (&v)[N], int rows, bool in, bool pairs)
 {
     if constexpr (sizeof(T) == 2) {
         if (pairs) {
-            const int odd = threadIdx.x & 1;
+            const int odd = threadIdx.x & 1, last = in ? rows - odd : 0;
+            const uint32_t select = odd ? 0x3276u : 0x5410u;
             T *dst = out + (odd ? ld - 1 : 0);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2, dst += 2 * ld) {
-                const T a = from_float<T>(v[c]), b = from_float<T>(v[c + 1]);
-                const uint32_t own = (uint32_t)reinterpret_cast<const uint16_t &>(a) |
-                                     (uint32_t)reinterpret_cast<const uint16_t &>(b) << 16;
-                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-                const uint32_t both = __byte_perm(own, other, odd ? 0x3276u : 0x5410u);
-                if (in && c + odd < rows) *reinterpret_cast<uint32_t *>(dst) = both;
+            for (int c = 0; c < N; c += 2, dst += 2 * ld) {
+                const uint32_t own = pack<T>(v[c], v[c + 1]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                if (c < last) *reinterpret_cast<uint32_t *>(dst) = __byte_perm(own, other, select);
             }
             return;
         }
     }
     if (!in) return;
 #pragma unroll
-    for (int c = 0; c < 32; ++c, out += ld)
+    for (int c = 0; c < N; ++c, out += ld)
         if (c < rows) *out = from_float<T>(v[c]);
 }
 
-// 32 sums of this lane's column (rows from `row` on) to their place (stride_y is 0 unless each group has an output); returns the sum of what Y
-// holds of them, before its rounding.
-template <class T, class O>
-__device__ __forceinline__ float finish_rows(const Args &p, float (&v)[32], long long row, int n, int e, float bias, int rows,
+// What the epilogue needs of the arguments, in registers: from the constant bank each of them would
+// cost a chunk of rows 40 cycles and more (a chunk of 16 rows took 1400 cycles).
+enum { WITH_Z = 16, WITH_R = 32, WITH_SUMS = 64, SLOPE = 128, Y_PAIRS = 256, Z_PAIRS = 512 };
+struct Epilogue {
+    float alpha, beta;
+    int mode;  // act, and the above
+    long long ldy, ldz, ldr;
+
+    __device__ __forceinline__ explicit Epilogue(const Args &p)
+    {
+        const Product &q = p.q;
+        alpha = __shfl_sync(0xFFFFFFFFu, q.alpha, 0);
+        beta = __shfl_sync(0xFFFFFFFFu, q.beta, 0);
+        ldy = __shfl_sync(0xFFFFFFFFu, q.ldy, 0);
+        ldz = __shfl_sync(0xFFFFFFFFu, q.ldz, 0);
+        ldr = __shfl_sync(0xFFFFFFFFu, q.ldr, 0);
+        const int z = q.slope ? q.act != FGEMM_ACT_NONE : q.z != nullptr;
+        mode = uniform(q.act | (z ? WITH_Z : 0) | (!q.slope && q.beta != 0.0f ? WITH_R : 0) | (q.partial ? WITH_SUMS : 0) |
+                       (q.slope ? SLOPE : 0) | (p.y_pairs ? Y_PAIRS : 0) | (p.z_pairs ? Z_PAIRS : 0));
+    }
+    __device__ __forceinline__ int act() const { return mode & 15; }
+    __device__ __forceinline__ bool has(int what) const { return (mode & what) != 0; }
+};
+
+// N sums of this lane's column to `rows` rows of it, the first at y (and z, r); returns the sum of what
+// Y holds of them, before its rounding.
+template <class T, class O, int N>
+__device__ __forceinline__ float finish_rows(const Epilogue &q, float (&v)[N], O *y, T *z, const O *r, float bias, int rows,
                                              bool in)
 {
-    const Product &q = p.q;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = fmaf(q.alpha, v[c], bias);
-    if (q.slope) {
-        if (q.act != FGEMM_ACT_NONE) {
-            float z[32];
-            load_rows(z, static_cast<const T *>(q.z) + row * q.ldz + n, q.ldz, rows, in);
-            if (q.act == FGEMM_ACT_RELU) {
+    for (int c = 0; c < N; ++c) v[c] = fmaf(q.alpha, v[c], bias);
+    const int act = q.act();
+    if (q.has(SLOPE)) {
+        if (q.has(WITH_Z)) {
+            float x[N];
+            load_rows(x, z, q.ldz, rows, in);
+            if (act == FGEMM_ACT_RELU) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = through(v[c], z[c], FGEMM_ACT_RELU);
-            } else if (q.act == FGEMM_ACT_GELU) {
+                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_RELU);
+            } else if (act == FGEMM_ACT_GELU) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = through(v[c], z[c], FGEMM_ACT_GELU);
+                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_GELU);
             } else {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = through(v[c], z[c], FGEMM_ACT_SILU);
+                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_SILU);
             }
         }
     } else {
-        if (q.z) store_rows(static_cast<T *>(q.z) + row * q.ldz + n, q.ldz, v, rows, in, p.z_pairs);
-        if (q.act == FGEMM_ACT_RELU) {
+        if (q.has(WITH_Z)) store_rows(z, q.ldz, v, rows, in, q.has(Z_PAIRS));
+        if (act == FGEMM_ACT_RELU) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = relu(v[c]);
-        } else if (q.act == FGEMM_ACT_GELU) {
+            for (int c = 0; c < N; ++c) v[c] = relu(v[c]);
+        } else if (act == FGEMM_ACT_GELU) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = gelu(v[c]);
-        } else if (q.act == FGEMM_ACT_SILU) {
+            for (int c = 0; c < N; ++c) v[c] = gelu(v[c]);
+        } else if (act == FGEMM_ACT_SILU) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = silu(v[c]);
+            for (int c = 0; c < N; ++c) v[c] = silu(v[c]);
         }
-        if (q.beta != 0.0f) {
-            float r[32];
-            load_rows(r, static_cast<const O *>(q.r) + e * q.stride_y + row * q.ldr + n, q.ldr, rows, in);
+        if (q.has(WITH_R)) {
+            float x[N];
+            load_rows(x, r, q.ldr, rows, in);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = fmaf(q.beta, r[c], v[c]);
+            for (int c = 0; c < N; ++c) v[c] = fmaf(q.beta, x[c], v[c]);
         }
     }
-    store_rows(static_cast<O *>(q.y) + e * q.stride_y + row * q.ldy + n, q.ldy, v, rows, in, p.y_pairs);
+    store_rows(y, q.ldy, v, rows, in, q.has(Y_PAIRS));
     float sum = 0.0f;
-    if (q.partial) {
+    if (q.has(WITH_SUMS)) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) sum += c < rows ? v[c] : 0.0f;
+        for (int c = 0; c < N; ++c) sum += c < rows ? v[c] : 0.0f;
     }
     return sum;
 }
 
-// The same for one element.
-template <class T, class O>
-__device__ __forceinline__ void finish_one(const Args &p, float sum, long long row, int n, int e)
+// Zero rows `from` .. `to` (entries of depth, at most 15) of `boxes` boxes stored across the depth, by a warp.
+__device__ __forceinline__ void zero_depth(uint32_t base, int boxes, int from, int to, int lane)
 {
-    const Product &q = p.q;
-    float v = q.alpha * sum;
-    if (q.slope) {
-        if (q.act != FGEMM_ACT_NONE) v = through(v, to_float(static_cast<const T *>(q.z)[row * q.ldz + n]), q.act);
-    } else {
-        if (q.bias) v += q.bias[(long long)e * q.N + n];
-        if (q.z) static_cast<T *>(q.z)[row * q.ldz + n] = from_float<T>(v);
-        v = activate(v, q.act);
-        if (q.beta != 0.0f) v = fmaf(q.beta, to_float(static_cast<const O *>(q.r)[e * q.stride_y + row * q.ldr + n]), v);
-    }
-    static_cast<O *>(q.y)[e * q.stride_y + row * q.ldy + n] = from_float<O>(v);
-}
-
-// Zero rows `from` .. `to` (entries of depth) of `blocks` boxes stored across the depth, by a warp.
-__device__ __forceinline__ void zero_depth(uint32_t base, int blocks, int from, int to, int lane)
-{
-    const int per = (to - from) * 8;
-    for (int i = lane; i < blocks * per; i += 32) {
-        const int b = i / per, o = i - b * per;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + b * BLOCK_BYTES + from * 128 + o * 16), "r"(0)
-                     : "memory");
-    }
+    for (int b = 0; b < boxes; ++b)
+        for (int row = from + (lane >> 3); row < to; row += 4)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + b * BOX_BYTES + row * 128 + (lane & 7) * 16), "r"(0)
+                         : "memory");
 }
 
 // A ring position and its phase.
@@ -340,29 +402,64 @@ struct Slot {
     }
 };
 
-// PAIR: a cluster of two CTAs works on 256 columns of Y with cta_group::2; each holds its own 128
-// columns of op(B) and half of the tile's rows of op(A).  CTA 0 issues for both; its `full`
-// barriers count what arrives in either.  Else `ranks` CTAs of a cluster divide the depth of one
-// tile, or a CTA walks whole tiles.
-template <bool PAIR, class T, class O>
-__global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
+// 16 sums of each lane from tensor memory.
+__device__ __forceinline__ void load_sums(uint32_t taddr, bool products, float (&v)[CHUNK])
 {
+    static_assert(CHUNK == 16, "columns");
+    if (!products) {
+#pragma unroll
+        for (int c = 0; c < CHUNK; ++c) v[c] = 0.0f;
+        return;
+    }
+    uint32_t r[CHUNK];
+    mx::tmem_load(taddr, r);
+#pragma unroll
+    for (int c = 0; c < CHUNK; ++c) v[c] = __uint_as_float(r[c]);
+}
+
+// The way back.
+__device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUNK])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+
+// PAIR: two CTAs work on 256 columns of Y with cta_group::2; each holds its own 128 columns of
+// op(B) and half of the tile's rows of op(A).  CTA 0 issues for both; its `full` barriers count what
+// arrives in either.  Else the `ranks` CTAs of a cluster divide the depth of one tile, or (ranks 1) a CTA
+// walks whole tiles.
+// LONG: the accumulators take LONG_STAGES stages (512 of depth) at a time, and the epilogue's warps
+// add these sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
+// 2048, sums come out 2.1e-6 off (2-norm, random operands), of 512 at a time 0.6e-6, which counts where
+// they are kept in FP32.
+template <bool PAIR, class T, class O, bool LONG>
+__global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
+{
+    constexpr int THREADS = threads_of(PAIR);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = p.stages, bar_offset = S * p.stage_bytes;
     const uint32_t sbase = tc::cvta_smem(smem), bars = sbase + bar_offset;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    // A pair's stages that a group ends in: what each CTA brings is counted by its own `tail`, and mended.
     auto fixed_bar = [&](int s) { return bars + 8u * (2 * S + s); };
-    auto acc_full_bar = [&](int a) { return bars + 8u * (3 * S + a); };
-    auto acc_free_bar = [&](int a) { return bars + 8u * (3 * S + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (3 * S + 4);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_offset + 8 * (3 * S + 5));
+    auto tail_bar = [&](int s) { return bars + 8u * (3 * S + s); };
+    auto acc_full_bar = [&](int a) { return bars + 8u * (4 * S + a); };
+    auto acc_free_bar = [&](int a) { return bars + 8u * (4 * S + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (4 * S + 4);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_offset + 8 * (4 * S + 5));
     int *const table = reinterpret_cast<int *>(smem + p.table);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int ctas = __shfl_sync(0xFFFFFFFFu, (int)cluster.num_blocks(), 0), cta = __shfl_sync(0xFFFFFFFFu, (int)cluster.block_rank(), 0);
+    // Which part of the depth, or which half of a pair (whose CTA 0 leads).
+    const int ranks = PAIR ? 1 : ctas, rank = PAIR ? 0 : cta, half = PAIR ? cta : 0;
     const unsigned long long lim = p.wait_limit_ns;
     const bool split = !PAIR && ranks > 1;
 
@@ -372,11 +469,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constan
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(full_bar(s), 1);
             tc::mbar_init(empty_bar(s), 1);
-            tc::mbar_init(fixed_bar(s), 1);
+            tc::mbar_init(fixed_bar(s), 2);
+            tc::mbar_init(tail_bar(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(acc_full_bar(a), 1);
-            tc::mbar_init(acc_free_bar(a), (PAIR ? 2 : 1) * EPI_WARPS);
+            tc::mbar_init(acc_free_bar(a), (PAIR ? 2 : 1) * 4 * SETS);
         }
         tc::mbar_init(drain_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -395,24 +493,32 @@ __global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constan
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
-    after_previous_kernel();
-    if (p.q.ragged != RAGGED_NONE && warp == 2) make_table(p, table, lane);
     tc::tc_fence_before();
-    if constexpr (PAIR)
+    if (ctas > 1)
         cluster.sync();
     else
         __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
 
+    // The first tiles are found, where the arguments say which they are, while the kernel before this one
+    // ends, and each role waits for that when it is ready to go.
     constexpr int COLUMNS = PAIR ? 2 * TILE_F : TILE_F;
-    Walk walk(p, table, COLUMNS);
-    const int tiles = walk.tiles();
-    const int first_tile = (int)blockIdx.x / ranks, tile_step = (int)gridDim.x / ranks;
+    const int first_tile = (int)blockIdx.x / ctas, tile_step = (int)gridDim.x / ctas;
+    if (p.q.ragged != RAGGED_NONE) {
+        after_previous_kernel();
+        if (warp == 2) make_table(p, table, lane);
+        __syncthreads();
+    }
+    Walk walk(p, table, COLUMNS, first_tile, tile_step);
+    Tile first{};
+    const bool any = walk.get(0, first);  // (else there is nothing for this CTA, or its cluster)
+    const bool waits = p.q.ragged == RAGGED_NONE;
+    const int stage_depth = uniform(p.blocks) * DEPTH;
     const bool fix_depth = p.q.ragged == RAGGED_DEPTH;
     // A tile's stages that are this CTA's.
     auto stages_of = [&](const Tile &o, int &from) {
-        const int all = (int)(((long long)o.depth + DEPTH - 1) / DEPTH);
+        const int all = (int)(((unsigned)o.depth + stage_depth - 1) >> (stage_depth == DEPTH ? 6 : 7));
         from = 0;
         if (!split) return all;
         from = (int)((long long)all * rank / ranks);
@@ -420,78 +526,108 @@ __global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constan
     };
     // MMA columns of a tile, and the rows of op(A) that this CTA brings for them.
     auto mma_cols = [&](const Tile &o) { return PAIR ? (o.valid + 31) & ~31 : (o.valid + 15) & ~15; };
+    // The k-th of a tile's n stages.  Where depths are ragged the last one comes first: it may have to be
+    // mended, while the tensor core is still at the tile before.
+    auto order = [&](int k, int n) { return !fix_depth ? k : k == 0 ? n - 1 : k - 1; };
     // Whether a stage with `left` of its depth to come ends inside the MMA's 16.
-    auto wants_fix = [&](int left) { return fix_depth && left < DEPTH && (left & 15) != 0; };
+    auto wants_fix = [&](int left) { return fix_depth && left < stage_depth && (left & 15) != 0; };
+    // That end of a stage becomes 0, in this CTA's part of both operands (x_boxes of op(A)).
+    auto fix = [&](uint32_t at, int left, int x_boxes) {
+        const uint32_t block = at + (left / DEPTH) * p.block_bytes;
+        const int first_row = left % DEPTH, to = (first_row + 15) & ~15;
+        zero_depth(block, 2, first_row, to, lane);
+        zero_depth(block + W_BYTES, x_boxes, first_row, to, lane);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads them
+        __syncwarp();
+    };
 
     if (warp == 0) {
         // ---- producer (one in each CTA): the whole warp walks along, one lane issues ----
+        // What the loop needs of the arguments is in registers, and the next barrier is looked at before
+        // this stage's copies are issued: the loop is a chain of short latencies.
+        const int withhold = uniform(p.withhold), w_across = uniform(p.w_across), x_across = uniform(p.x_across);
+        const uint32_t stage_bytes = uniform(p.stage_bytes), block_bytes = uniform(p.block_bytes);
+        const uint32_t full0 = full_bar(0), empty0 = empty_bar(0), lead0 = PAIR ? mx::map_to_rank(full0, 0) : full0;
+        const int x_step = x_across ? 64 : uniform(p.x_box);
+        const uint32_t box_bytes = (uint32_t)x_step * 128;
+        // From one box of op(A) to the next.
+        const int x_d0 = x_across ? x_step : 0, x_d1 = x_across ? 0 : x_step;
         Slot at;
+        uint32_t place = sbase;  // of the stage
         int g = 0;
-        bool ok = true;
-        uint32_t own_phase = 0, own_used = 0;  // rank 1 of a pair: stages that its own barriers count
-        for (int t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile o = walk.at(t);
-            int from;
-            const int n = stages_of(o, from), cols = mma_cols(o), own = PAIR ? cols / 2 : cols;
-            const int boxes = p.x_across ? (own + 63) / 64 : (own + p.x_box - 1) / p.x_box;
-            const uint32_t box_bytes = p.x_across ? BLOCK_BYTES : p.x_box * 128;
+        bool ok = true, ready = true;
+        uint32_t tail_phase = 0, tail_used = 0;  // of the tail barriers
+        Tile o = first;
+        int from, n = stages_of(o, from);
+        if (waits) after_previous_kernel();
+        bool more = any;
+        for (int tile = 1; ok && more; ++tile) {
+            const int cols = mma_cols(o), own = PAIR ? cols / 2 : cols;
+            const int boxes = (own + x_step - 1) / x_step, e = fix_depth ? 0 : o.e;
             const uint32_t bytes = W_BYTES + boxes * box_bytes;
-            const int f = o.f0 + (PAIR ? TILE_F * rank : 0), x0 = o.t0 + (PAIR ? own * rank : 0);
-            for (int k = from; k < from + n; ++k, ++g) {
-                ok = mx::warp_wait(empty_bar(at.s), at.phase ^ 1, err, tc::ERR_PRODUCER, lim) &&
-                     g != p.withhold;  // (testing: as if this copy never arrived)
+            const int f = o.f0 + TILE_F * half, x0 = o.t0 + own * half;
+            for (int k = 0; k < n; ++k, ++g) {
+                const int skip = (from + order(k, n)) * stage_depth, depth = o.k0 + skip, left = o.depth - skip;
+                ok = (ready || warp_wait(empty0 + 8 * at.s, at.phase ^ 1, err, tc::ERR_PRODUCER, lim)) &&
+                     g != withhold;  // (testing: as if this copy never arrived)
                 if (!ok) break;
-                const bool fix = PAIR && wants_fix(o.depth - k * DEPTH);
+                const bool tail = PAIR && wants_fix(left);
+                const uint32_t here = place, full = full0 + 8 * at.s, lead = lead0 + 8 * at.s;
+                const uint32_t bar = tail ? tail_bar(at.s) : full;
+                const bool two = stage_depth > DEPTH && left > DEPTH;
+                if (tail) {
+                    tail_used |= 1u << at.s;
+                    tail_phase ^= 1u << at.s;
+                }
+                at.next(S);
+                place = at.s == 0 ? sbase : place + stage_bytes;
+                const uint32_t next = test_wait(empty0 + 8 * at.s, at.phase ^ 1);
                 if (mx::elect_one()) {
-                    const uint32_t w_at = sbase + at.s * p.stage_bytes, x_at = w_at + W_BYTES;
-                    const int depth = o.k0 + k * DEPTH, e = fix_depth ? 0 : o.e;
-                    if (!PAIR || fix) {
-                        const uint32_t bar = full_bar(at.s);
-                        tc::mbar_arrive_expect_tx(bar, bytes);
-                        if (p.w_across) {
-                            tc::tma_load_3d(w_at, &p.w, bar, f, depth, e);
-                            tc::tma_load_3d(w_at + BLOCK_BYTES, &p.w, bar, f + 64, depth, e);
+                    if (!PAIR || tail)
+                        tc::mbar_arrive_expect_tx(bar, two ? 2 * bytes : bytes);
+                    else if (half == 0)
+                        tc::mbar_arrive_expect_tx(bar, two ? 4 * bytes : 2 * bytes);
+                    if (tail && half == 0) tc::mbar_arrive(full);  // (this use of it passes)
+#pragma unroll
+                    for (int block = 0; block < 2; ++block) {
+                        if (block == 1 && !two) break;
+                        const uint32_t w_at = here + block * block_bytes, x_at = w_at + W_BYTES;
+                        const int d = depth + block * DEPTH;
+                        const int w_c0 = w_across ? f : d, w_c1 = w_across ? d : f;
+                        const int x_c0 = x_across ? x0 : d, x_c1 = x_across ? d : x0;
+                        if (!PAIR || tail) {
+                            tc::tma_load_3d(w_at, &p.w, bar, w_c0, w_c1, e);
+                            if (w_across) tc::tma_load_3d(w_at + BOX_BYTES, &p.w, bar, w_c0 + 64, w_c1, e);
+#pragma unroll
+                            for (int b = 0; b < MAX_BOXES; ++b)
+                                if (b < boxes) mx::tma_load_2d(x_at + b * box_bytes, &p.x, bar, x_c0 + b * x_d0, x_c1 + b * x_d1);
                         } else {
-                            tc::tma_load_3d(w_at, &p.w, bar, depth, f, e);
-                        }
-                        for (int b = 0; b < boxes; ++b) {
-                            if (p.x_across)
-                                mx::tma_load_2d(x_at + b * BLOCK_BYTES, &p.x, bar, x0 + 64 * b, depth);
-                            else
-                                mx::tma_load_2d(x_at + b * box_bytes, &p.x, bar, depth, x0 + p.x_box * b);
-                        }
-                    } else {
-                        if (rank == 0) tc::mbar_arrive_expect_tx(full_bar(at.s), 2 * bytes);
-                        const uint32_t bar = mx::map_to_rank(full_bar(at.s), 0);
-                        if (p.w_across) {
-                            mx::pair_load_3d(w_at, &p.w, bar, f, depth, e);
-                            mx::pair_load_3d(w_at + BLOCK_BYTES, &p.w, bar, f + 64, depth, e);
-                        } else {
-                            mx::pair_load_3d(w_at, &p.w, bar, depth, f, e);
-                        }
-                        for (int b = 0; b < boxes; ++b) {
-                            if (p.x_across)
-                                mx::pair_load_2d(x_at + b * BLOCK_BYTES, &p.x, bar, x0 + 64 * b, depth);
-                            else
-                                mx::pair_load_2d(x_at + b * box_bytes, &p.x, bar, depth, x0 + p.x_box * b);
+                            mx::pair_load_3d(w_at, &p.w, lead, w_c0, w_c1, e);
+                            if (w_across) mx::pair_load_3d(w_at + BOX_BYTES, &p.w, lead, w_c0 + 64, w_c1, e);
+#pragma unroll
+                            for (int b = 0; b < MAX_BOXES; ++b)
+                                if (b < boxes) mx::pair_load_2d(x_at + b * box_bytes, &p.x, lead, x_c0 + b * x_d0, x_c1 + b * x_d1);
                         }
                     }
                 }
                 __syncwarp();
-                if (fix && rank == 1) {
-                    own_used |= 1u << at.s;
-                    own_phase ^= 1u << at.s;
-                }
-                at.next(S);
+                ready = __all_sync(0xFFFFFFFFu, next);
             }
+            more = walk.get(tile, o);
+            n = stages_of(o, from);
         }
         // Never leave with copies in flight into either CTA's shared memory.
-        if (!PAIR || rank == 0) {
+        if (half == 0)
             for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
                 tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
-        } else {
-            for (int s = 0; s < S; ++s)
-                if (own_used >> s & 1) tc::mbar_wait(full_bar(s), (own_phase >> s & 1) ^ 1, err, tc::ERR_DRAIN, lim, false);
+        for (int s = 0; s < S; ++s)
+            if (tail_used >> s & 1) tc::mbar_wait(tail_bar(s), (tail_phase >> s & 1) ^ 1, err, tc::ERR_DRAIN, lim, false);
+        if (half == 1 && !ok) {
+            // Having given up, CTA 1 may have asked for stages that CTA 0 no longer counts: a millisecond
+            // for its copies to land (they take some microseconds).
+            const uint64_t t0 = tc::global_timer();
+            while (tc::global_timer() - t0 < 1000000ull) {
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -499,60 +635,79 @@ __global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constan
         Slot at;
         bool ok = true;
         uint32_t fix_phase = 0;
-        if (!PAIR || rank == 0) {
+        if (waits) after_previous_kernel();
+        if (half == 0) {
+            const uint32_t fmt = p.q.type == FGEMM_BF16 ? (1u << 7) | (1u << 10) : 0u;
+            const uint32_t idesc0 = uniform((int)((1u << 4) | fmt | ((uint32_t)p.w_across << 15) | ((uint32_t)p.x_across << 16) |
+                                                  ((uint32_t)(COLUMNS >> 4) << 24)));
+            // 16 of depth: 32 bytes along it, 16 rows of 128 bytes across it.
+            const uint32_t wi = uniform(p.w_across ? 128 : 2), xi = uniform(p.x_across ? 128 : 2);
+            const uint32_t stage_bytes = uniform(p.stage_bytes), acc_step = uniform(p.acc_step);
+            const uint32_t block_step = uniform(p.block_bytes >> 4);
+            const int long_stages = LONG_DEPTH / stage_depth;
+            const uint32_t full0 = full_bar(0), empty0 = empty_bar(0);
+            // (Addresses count modulo 256 KB: above are the bits that tell the CTAs of a cluster apart.)
+            const uint64_t w_desc = p.w_across ? across_desc(0) : tc::kmajor_sw128_desc(0);
+            const uint64_t x_desc = p.x_across ? across_desc(0) : tc::kmajor_sw128_desc(0);
+            uint32_t place = sbase;
             int j = 0;
-            const uint32_t fmt = sizeof(T) == 2 && p.q.type == FGEMM_BF16 ? (1u << 7) | (1u << 10) : 0u;
-            const uint32_t idesc0 = (1u << 4) | fmt | ((uint32_t)p.w_across << 15) | ((uint32_t)p.x_across << 16) |
-                                    ((uint32_t)(COLUMNS >> 4) << 24);
-            for (int t = first_tile; ok && t < tiles; t += tile_step) {
-                const Tile o = walk.at(t);
+            bool ready = false;
+            Tile o = first;
+            bool more = any;
+            for (int tile = 1; ok && more; more = walk.get(tile++, o)) {
                 int from;
                 const int n = stages_of(o, from), cols = mma_cols(o);
-                if (n == 0) continue;
-                const int acc = j & 1;
-                // Tile j - 2's sums have been read.
-                if (j >= 2 && !mx::warp_wait(acc_free_bar(acc), ((j >> 1) - 1) & 1, err, tc::ERR_MMA_WAIT, lim)) {
-                    ok = false;
-                    break;
-                }
-                tc::tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * p.acc_step), idesc = idesc0 | ((uint32_t)(cols >> 3) << 17);
-                for (int k = from; k < from + n; ++k) {
-                    ok = mx::warp_wait(full_bar(at.s), at.phase, err, tc::ERR_MMA_WAIT, lim);
+                const uint32_t idesc = idesc0 | ((uint32_t)(cols >> 3) << 17);
+                uint32_t d = 0;
+                int since = 0;  // stages that this accumulator holds
+                for (int k = 0; k < n; ++k) {
+                    const int left = o.depth - (from + order(k, n)) * stage_depth;
+                    const int acc = j & 1;
+                    if (since == 0) {  // the sums before the last ones have been read
+                        ok = j < 2 || warp_wait(acc_free_bar(acc), ((j >> 1) - 1) & 1, err, tc::ERR_MMA_WAIT, lim);
+                        if (!ok) break;
+                        d = tmem + (uint32_t)acc * acc_step;
+                    }
+                    ok = ready || warp_wait(full0 + 8 * at.s, at.phase, err, tc::ERR_MMA_WAIT, lim);
                     if (!ok) break;
-                    const int left = o.depth - k * DEPTH, steps = min(DEPTH / 16, (left + 15) / 16);
-                    const uint32_t w_at = sbase + at.s * p.stage_bytes, x_at = w_at + W_BYTES;
+                    const bool last = k + 1 == n || (LONG && since + 1 == long_stages);
+                    const int steps = (min(stage_depth, left) + 15) >> 4;
                     if (wants_fix(left)) {
-                        zero_depth(w_at, 2, left, 16 * steps, lane);
-                        zero_depth(x_at, ((PAIR ? cols / 2 : cols) + 63) / 64, left, 16 * steps, lane);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads them
-                        __syncwarp();
-                        if (PAIR) {
-                            ok = cluster_wait(fixed_bar(at.s), fix_phase >> at.s & 1, err, tc::ERR_MMA_WAIT, lim);
+                        if constexpr (PAIR) {  // the menders of both CTAs have been there
+                            ok = warp_wait<true>(fixed_bar(at.s), fix_phase >> at.s & 1, err, tc::ERR_MMA_WAIT, lim);
                             fix_phase ^= 1u << at.s;
                             if (!ok) break;
+                        } else {
+                            fix(place, left, (cols + 63) / 64);
                         }
                     }
+                    const uint64_t wd = w_desc + ((place >> 4) & 0x3FFFu), xd = x_desc + (((place + W_BYTES) >> 4) & 0x3FFFu);
+                    const uint32_t empty = empty0 + 8 * at.s;
+                    at.next(S);
+                    place = at.s == 0 ? sbase : place + stage_bytes;
+                    const uint32_t next = test_wait(full0 + 8 * at.s, at.phase);
                     tc::tc_fence_after();
                     if (mx::elect_one()) {
-                        const uint64_t wd = p.w_across ? across_desc(w_at) : tc::kmajor_sw128_desc(w_at);
-                        const uint64_t xd = p.x_across ? across_desc(x_at) : tc::kmajor_sw128_desc(x_at);
-                        // 16 of depth: 32 bytes along it, 16 rows of 128 bytes across it.
-                        const uint32_t wi = p.w_across ? 128u : 2u, xi = p.x_across ? 128u : 2u;
-                        for (int i = 0; i < steps; ++i)
-                            mma<PAIR>(d, wd + wi * i, xd + xi * i, idesc, k > from || i > 0);
+#pragma unroll
+                        for (int i = 0; i < 2 * DEPTH / 16; ++i) {
+                            const uint32_t block = i < DEPTH / 16 ? 0 : block_step;
+                            if (i < steps)
+                                mma<PAIR>(d, wd + (block + wi * (i % (DEPTH / 16))), xd + (block + xi * (i % (DEPTH / 16))), idesc,
+                                          since > 0 || i > 0);
+                        }
                         if constexpr (PAIR) {
-                            mx::pair_commit(empty_bar(at.s));
-                            if (k + 1 == from + n) mx::pair_commit(acc_full_bar(acc));
+                            mx::pair_commit(empty);
+                            if (last) mx::pair_commit(acc_full_bar(acc));
                         } else {
-                            tc::umma_commit(empty_bar(at.s));
-                            if (k + 1 == from + n) tc::umma_commit(acc_full_bar(acc));
+                            tc::umma_commit(empty);
+                            if (last) tc::umma_commit(acc_full_bar(acc));
                         }
                     }
                     __syncwarp();
-                    at.next(S);
+                    ready = __all_sync(0xFFFFFFFFu, next);
+                    since = last ? 0 : since + 1;
+                    j += last;
                 }
-                ++j;
             }
             if (!ok) {  // give up: nothing issued may still be running at teardown
                 if (mx::elect_one()) {
@@ -564,115 +719,176 @@ __global__ void __launch_bounds__(THREADS, 1) gemm16_kernel(const __grid_constan
                 __syncwarp();
                 tc::mbar_wait(drain_bar, 0, err, tc::ERR_DRAIN, lim, false);
             }
-        } else if (fix_depth) {
-            // CTA 1 of a pair overwrites its own part of the stages that a group ends in.
-            for (int t = first_tile; ok && t < tiles; t += tile_step) {
-                const Tile o = walk.at(t);
+        }
+        __syncwarp();
+    } else if (PAIR && warp == 2 + 4 * SETS) {
+        // ---- mender (one in each CTA of a pair): overwrites its CTA's part of the stages that a group ends in,
+        // as soon as they are there ----
+        if (fix_depth) {
+            Slot at;
+            uint32_t phases = 0;
+            Tile o = first;
+            bool more = any, ok = true;
+            for (int tile = 1; ok && more; more = walk.get(tile++, o)) {
                 int from;
-                const int n = stages_of(o, from), left = o.depth - (n - 1) * DEPTH;
-                for (int k = 0; k + 1 < n; ++k) at.next(S);
-                if (n == 0) continue;
-                if (wants_fix(left)) {
-                    ok = mx::warp_wait(full_bar(at.s), fix_phase >> at.s & 1, err, tc::ERR_MMA_WAIT, lim);
-                    fix_phase ^= 1u << at.s;
+                const int n = stages_of(o, from), left = o.depth - (from + order(0, n)) * stage_depth;
+                if (n > 0 && wants_fix(left)) {
+                    ok = warp_wait(tail_bar(at.s), phases >> at.s & 1, err, tc::ERR_MMA_WAIT, lim);
                     if (!ok) break;
-                    const uint32_t w_at = sbase + at.s * p.stage_bytes;
-                    const int to = (left + 15) & ~15;
-                    zero_depth(w_at, 2, left, to, lane);
-                    zero_depth(w_at + W_BYTES, (mma_cols(o) / 2 + 63) / 64, left, to, lane);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+                    phases ^= 1u << at.s;
+                    fix(sbase + at.s * p.stage_bytes, left, (mma_cols(o) / 2 + 63) / 64);
                     if (lane == 0) mx::arrive_at(mx::map_to_rank(fixed_bar(at.s), 0));
                 }
-                at.next(S);
+                for (int k = 0; k < n; ++k) at.next(S);
             }
         }
         __syncwarp();
     } else {
-        // ---- epilogue: warps of two sets of four, a set takes every other chunk of 32 rows ----
+        // ---- epilogue: sets of four warps; the sets take the chunks of rows in turn ----
         const int q = warp & 3, set = (warp - 2) >> 2;
+        auto give_back = [&](int acc) {  // this warp has read an accumulator
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    arrive_remote(mx::map_to_rank(acc_free_bar(acc), 0));
+                else
+                    tc::mbar_arrive(acc_free_bar(acc));
+            }
+        };
+        const Epilogue epi(p);
+        const float *const biases = p.q.bias;
+        const int N = uniform(p.q.N), acc_step = uniform(p.acc_step);
+        const long long stride_y = __shfl_sync(0xFFFFFFFFu, p.q.stride_y, 0);
         int j = 0;
-        for (int t = first_tile; t < tiles; t += tile_step) {
-            const Tile o = walk.at(t);
+        Tile o = first;
+        if (waits) after_previous_kernel();
+        bool more = any;
+        for (int tile = 1; more; more = walk.get(tile++, o)) {
             int from;
-            const bool products = stages_of(o, from) > 0;
-            const int acc = j & 1, n = o.f0 + (PAIR ? TILE_F * rank : 0) + 32 * q + lane;
-            const bool in = n < p.q.N;
+            const int stages = stages_of(o, from), n = o.f0 + TILE_F * half + 32 * q + lane;
+            const int turns = LONG ? (stages * stage_depth + LONG_DEPTH - 1) / LONG_DEPTH : stages > 0;
+            const bool in = n < N;
             // (on its way during the wait)
-            const float bias = p.q.bias && in && !split ? p.q.bias[(long long)o.e * p.q.N + n] : 0.0f;
-            if (products && !mx::warp_wait(acc_full_bar(acc), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim)) break;
-            tc::tc_fence_after();
-            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.acc_step);
+            const float bias = biases && in ? biases[(long long)o.e * N + n] : 0.0f;
+            O *const y = static_cast<O *>(p.q.y) + o.e * stride_y + o.t0 * epi.ldy + n;
+            T *const z = static_cast<T *>(p.q.z) + o.t0 * epi.ldz + n;
+            const O *const r_at = static_cast<const O *>(p.q.r) + o.e * stride_y + o.t0 * epi.ldr + n;
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             float sum = 0.0f;
-#pragma unroll 1
-            for (int c0 = 32 * set; c0 < o.valid; c0 += 64) {
-                uint32_t r[32];
-                if (products) {
-                    tc::tmem_ld_32cols(src + (uint32_t)c0, r);
-                } else {
+            const int share = (o.valid + ranks - 1) / ranks;  // rows that a rank of the cluster joins
+            auto finish = [&](float (&v)[CHUNK], int c0) {
+                if (split) {  // to the rank that joins the row: by rank, row, 128 columns
+                    int to = c0 / share, row = c0 - to * share;
+                    const uint32_t mine = sbase + p.join + (uint32_t)(rank * share * TILE_F + 32 * q + lane) * 4;
+                    uint32_t at = mx::map_to_rank(mine, to);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) r[c] = 0;
+                    for (int c = 0; c < CHUNK; ++c) {
+                        if (c0 + c < o.valid) store_remote(at + (uint32_t)row * TILE_F * 4, v[c]);
+                        if (++row == share) {
+                            row = 0;
+                            to = min(to + 1, ranks - 1);
+                            at = mx::map_to_rank(mine, to);
+                        }
+                    }
+                } else {
+                    sum += finish_rows<T, O>(epi, v, y + c0 * epi.ldy, z + c0 * epi.ldz, r_at + c0 * epi.ldr, bias, o.valid - c0, in);
                 }
-                float v[32];
+            };
+            bool ok = true;
+            if constexpr (LONG) {
+                // All turns but the last are added up in registers, and then with the last one where its
+                // sums are, in tensor memory.
+                if (turns > 1) {
+                    constexpr int MOST = (PAIR ? 256 : 64) / CHUNK / SETS;
+                    float sums[MOST][CHUNK];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
-                if (split) {  // row c of the tile: 128 sums, one for each column
-                    float *const part = reinterpret_cast<float *>(smem) + c0 * TILE_F + 32 * q + lane;
+                    for (int i = 0; i < MOST; ++i)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c0 + c < o.valid) part[c * TILE_F] = v[c];
-                } else {
-                    sum += finish_rows<T, O>(p, v, (long long)o.t0 + c0, n, o.e, bias, o.valid - c0, in);
+                        for (int c = 0; c < CHUNK; ++c) sums[i][c] = 0.0f;
+#pragma unroll 1
+                    for (int turn = 0; ok && turn < turns; ++turn) {
+                        ok = warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const bool last = turn + 1 == turns;
+#pragma unroll
+                        for (int i = 0; i < MOST; ++i) {
+                            const int c0 = CHUNK * (SETS * i + set);
+                            if (c0 < o.valid) {
+                                const uint32_t at = lanes + (uint32_t)((j & 1) * acc_step + c0);
+                                float v[CHUNK];
+                                load_sums(at, true, v);
+#pragma unroll
+                                for (int c = 0; c < CHUNK; ++c) sums[i][c] += v[c];
+                                if (last) store_sums(at, sums[i]);
+                            }
+                        }
+                        if (!last) {
+                            give_back(j & 1);
+                            ++j;
+                        }
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
             }
-            if (products) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR)
-                        mx::arrive_at(mx::map_to_rank(acc_free_bar(acc), 0));
-                    else
-                        tc::mbar_arrive(acc_free_bar(acc));
-                }
+            if (!LONG || turns == 1) ok = turns == 0 || warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim);
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int c0 = CHUNK * set; c0 < o.valid; c0 += SETS * CHUNK) {
+                float v[CHUNK];
+                load_sums(lanes + (uint32_t)((j & 1) * acc_step + c0), turns > 0, v);
+                finish(v, c0);
+            }
+            if (turns > 0) {
+                give_back(j & 1);
                 ++j;
             }
-            const long long part = 2ll * o.row_tile + set;
-            if (p.q.partial && in && part < p.q.partials) p.q.partial[part * p.q.N + n] = sum;
+            const long long row = (long long)SETS * o.row_tile + set;
+            if (p.q.partial && in && row < p.q.partials) p.q.partial[row * p.q.N + n] = sum;
         }
         __syncwarp();
     }
 
     if (split) {
-        // Every CTA of the cluster adds up its share of the tile's rows over the ranks, in rank order.
-        // (A rank that gave up leaves its memory as it was; the error word says that Y is undefined.)
+        // Every CTA of the cluster has been sent its share of the tile's rows by all ranks (its own room
+        // for them is apart from the stages, which it may still use meanwhile) and adds them up, in rank
+        // order.  (A rank that gave up sends nothing; the error word says that Y is undefined.)
+        const Epilogue epi(p);
+        float bias = 0.0f;
+        const int q = warp & 3, set = (warp - 2) >> 2, n = first.f0 + TILE_F * half + 32 * q + lane;
+        if (warp >= 2 && any && p.q.bias && n < p.q.N) bias = p.q.bias[(long long)first.e * p.q.N + n];
         cluster.sync();
-        if (first_tile < tiles) {
-            Walk again(p, table, COLUMNS);
-            const Tile o = again.at(first_tile);
-            const int from = o.valid * rank / ranks, to = o.valid * (rank + 1) / ranks;
-            for (int i = threadIdx.x; i < (to - from) * TILE_F; i += THREADS) {
-                const int c = from + i / TILE_F, f = i % TILE_F, n = o.f0 + f;
-                if (n >= p.q.N) continue;
-                float part[8];
+        if (warp >= 2 && any) {
+            const int share = (first.valid + ranks - 1) / ranks, rows = min(share, first.valid - rank * share);
+            const float *const part = reinterpret_cast<const float *>(smem + p.join) + 32 * q + lane;
+            constexpr int FEW = 8;
+#pragma unroll 1
+            for (int c0 = FEW * set; c0 < rows; c0 += SETS * FEW) {
+                float v[FEW];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < ranks) part[r] = *cluster.map_shared_rank(reinterpret_cast<float *>(smem) + c * TILE_F + f, r);
-                float sum = part[0];
+                for (int c = 0; c < FEW; ++c) v[c] = 0.0f;
+#pragma unroll 2
+                for (int r = 0; r < ranks; ++r) {
 #pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    if (r < ranks) sum += part[r];
-                finish_one<T, O>(p, sum, (long long)o.t0 + c, n, o.e);
+                    for (int c = 0; c < FEW; ++c)
+                        if (c0 + c < rows) v[c] += part[(r * share + c0 + c) * TILE_F];
+                }
+                const long long row = first.t0 + rank * share + c0, base = first.e * p.q.stride_y + n;
+                finish_rows<T, O>(epi, v, static_cast<O *>(p.q.y) + base + row * epi.ldy, static_cast<T *>(p.q.z) + n + row * epi.ldz,
+                                  static_cast<const O *>(p.q.r) + base + row * epi.ldr, bias, rows - c0, n < p.q.N);
             }
         }
-        cluster.sync();
     }
 
     if (p.q.partial_start && blockIdx.x == 0) {
         for (int e = threadIdx.x; e <= p.q.groups; e += THREADS)
-            p.q.partial_start[e] = p.q.ragged == RAGGED_ROWS ? 2 * (walk.first[e] / p.tiles_f) : 2 * p.tiles_t * e;
+            p.q.partial_start[e] = SETS * (p.q.ragged == RAGGED_ROWS ? walk.first[e] / p.tiles_f : p.tiles_t * e);
     }
 
-    // No CTA of a pair leaves while the other may still reach its memory.
+    // No CTA of a pair leaves while the other may still reach its memory.  (What ranks send each other has
+    // arrived.)
     tc::tc_fence_before();
     if constexpr (PAIR)
         cluster.sync();

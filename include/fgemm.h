@@ -648,12 +648,13 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
                               size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * How a product runs on a GPU with `num_sms` SMs, as 16 * rows + ranks: tiles of 128 columns of Y by at
- * most `rows` rows, each tile's depth divided among `ranks` CTAs; ranks 0: tiles of 256 columns by pairs of
- * CTAs.  grouped 0: fgemm_gemm16 and its gradient (sums: with col_sums), 1: by groups, 2:
+ * How a product runs on a GPU with `num_sms` SMs: 16 * rows + ranks (tiles of 128 columns of Y by at most
+ * `rows` rows, each tile's depth divided among `ranks` CTAs), + 8192 where pairs of CTAs take 256 columns,
+ * + 16384 where the sums of a long depth are added up in turns of 512 (col_sums, or FP32 out).
+ * grouped 0: fgemm_gemm16 and its gradient (sums: with col_sums), 1: by groups, 2:
  * fgemm_gemm16_weight_grad (sizes as that call has them).  -1 for arguments out of range.  Host-only: no CUDA call.
  */
-int fgemm_gemm16_plan(int grouped, int groups, int M, int N, int K, int sums, int num_sms);
+int fgemm_gemm16_plan(fgemm_dtype out_type, int grouped, int groups, int M, int N, int K, int sums, int num_sms);
 
 #ifdef __cplusplus
 }
