@@ -1,5 +1,4 @@
-// gemm16_device.cuh -- activations of the 16-bit layers and their derivatives, in FP32, without
-// branches and with two instructions of the special-function unit each.
+// gemm16_device.cuh -- activations of the 16-bit layers and their derivatives, in FP32.
 //
 // The factor that may be infinite is clamped where the other one is 0 (or the product below
 // FP32's range), so that a pre-activation of -inf gives 0 and not 0 * inf.  A NaN stays one.
@@ -44,42 +43,42 @@ __device__ __forceinline__ float reciprocal_fast(float x)
     return r;
 }
 
-// For a = |z|: e = exp(-a^2/2) and the normal tail q = Phi(-a) = e g(a).  g falls from 1/2 as 1/a: a
-// polynomial in t = 1 / (1 + 0.31 a), the variable of Hastings' approximations (1955), its coefficients a
-// minimax fit of the relative error for a up to 20 (1.7e-7; 5e-7 as evaluated in FP32).  Beyond 20 both
-// are 0.  By normcdff the layer's epilogue took 1.3 times the whole product (8192 x 11008 x 4096, Z
-// kept: 562 us against 431 without an activation).
-__device__ __forceinline__ void normal_tail(float a, float &e, float &q)
+template <int N>
+__device__ __forceinline__ float polynomial(const float (&c)[N], float x)
 {
-    const float t = reciprocal_fast(fmaf(0.31f, a, 1.0f));
-    e = exp2_fast(-0.721347520444482f * a * a);  // log2(e) / 2
-    float g = fmaf(0.0359170846f, t, -0.141935625f);
-    g = fmaf(g, t, 0.155671924f);
-    g = fmaf(g, t, -0.0154948533f);
-    g = fmaf(g, t, 0.110444422f);
-    g = fmaf(g, t, 0.107662495f);
-    g = fmaf(g, t, 0.124079033f);
-    g = fmaf(g, t, 0.123655601f);
-    q = e * (g * t);
+    float h = c[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) h = fmaf(h, x, c[i]);
+    return h;
 }
 
-// z Phi(z) = max(0, z) - |z| Phi(-|z|).
+// z Phi(z) = max(0, z) - a q for a = |z| and the normal tail q = Phi(-a) = exp(-a^2/2) g(a).  g falls from 1/2
+// as 1/a: a polynomial in t = 1 / (1 + 0.31 a), the variable of Hastings' approximations (1955), its
+// coefficients a minimax fit of the relative error for a up to 20 (1.7e-7; 5e-7 as evaluated in FP32).  From
+// 20 on q is 0.  (By normcdff the layer's epilogue took 1.3 times the whole product: 8192 x 11008 x
+// 4096, Z kept, 562 us against 431 without an activation.)
 __device__ __forceinline__ float gelu(float z)
 {
-    const float a = at_most(fabsf(z), 20.0f);
-    float e, q;
-    normal_tail(a, e, q);
+    constexpr float g[] = {0.0359170846f, -0.141935625f, 0.155671924f, -0.0154948533f,
+                           0.110444422f,  0.107662495f,  0.124079033f, 0.123655601f};
+    const float a = at_most(fabsf(z), 20.0f), t = reciprocal_fast(fmaf(0.31f, a, 1.0f));
+    const float q = exp2_fast(-0.721347520444482f * a * a) * (polynomial(g, t) * t);  // log2(e) / 2
     return fmaf(-a, q, relu(z));
 }
 
-// Phi(z) + z phi(z): s for z < 0, 1 - s for z > 0, with s = Phi(-|z|) - |z| phi(z).
+// Phi(z) + z phi(z), with Phi(z) = 1/2 + z P(2 z^2 / 5.5^2 - 1) for |z| up to 5.5, beyond which Phi is 0 or 1 to
+// within FP32's rounding: P is a Chebyshev fit of this even function, off by less than 1e-8, its coefficients add up to
+// 0.4, and Phi as evaluated is 1.5e-8 off on average, 6e-8 at most, which is what 1 + erff comes to.  (A gradient
+// is rounded to 16 bits, to the other side the more often the less exact it is.  By the tail above it is
+// 2.3e-7 off, and the weights' gradient of 2048 rows was twice as far off.)
 __device__ __forceinline__ float gelu_slope(float z)
 {
-    const float a = at_most(fabsf(z), 20.0f);
-    float e, q;
-    normal_tail(a, e, q);
-    const float s = fmaf(a * -0.398942280401433f, e, q);
-    return z > 0.0f ? 1.0f - s : s;
+    constexpr float p[] = {0.000118079995f, -0.000285676331f, 0.000183916665f, -0.000356754608f, 0.00140742643f, -0.00265870243f,
+                           0.00407412974f, -0.00665067835f, 0.0104686366f, -0.015062524f, 0.0203073174f, -0.0260361508f,
+                           0.0320769101f, -0.0387937948f, 0.0477373339f, -0.0641723126f, 0.12855193f};
+    const float c = at_least(at_most(z, 5.5f), -5.5f);
+    const float cdf = fmaf(c, polynomial(p, fmaf(c * c, 2.0f / (5.5f * 5.5f), -1.0f)), 0.5f);
+    return fmaf(c, 0.398942280401433f * exp2_fast(-0.721347520444482f * z * z), cdf);
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return reciprocal_fast(1.0f + exp2_fast(-1.44269504088896f * z)); }
@@ -117,6 +116,31 @@ template <> __device__ __forceinline__ uint32_t pack<__half>(float a, float b)
 {
     const __half2 v = __floats2half2_rn(a, b);
     return reinterpret_cast<const uint32_t &>(v);
+}
+
+// act'(z) (GELU, SiLU) as its definition reads, each step rounded to nearest; a few units in the last place off.
+static __device__ __noinline__ float slope_by_definition(float z, int act)
+{
+    if (act == FGEMM_ACT_GELU) {
+        const float cdf = __fmul_rn(0.5f, erfcf(__fmul_rn(-z, 0.707106781186548f)));
+        const float w = at_least(at_most(z, 20.0f), -20.0f);  // (0 * inf)
+        return __fadd_rn(cdf, __fmul_rn(__fmul_rn(w, expf(__fmul_rn(__fmul_rn(-0.5f, z), z))), 0.398942280401433f));
+    }
+    const float c = at_least(at_most(z, 80.0f), -80.0f), s = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-c)));
+    return __fmul_rn(s, __fadd_rn(1.0f, __fmul_rn(c, __fadd_rn(1.0f, -s))));
+}
+
+// v act'(z) as it is rounded to T when act' is evaluated by its definition: by the fast evaluation where
+// all values within both evaluations' errors round alike, else by the definition (one BF16 element in
+// 4000).  Both evaluations of GELU's slope are off by less than 2.5e-7, SiLU's by (1 + |z|) times that.
+template <class T>
+__device__ __forceinline__ float through_exactly(float v, float z, int act)
+{
+    const float fast = through(v, z, act);
+    if (act != FGEMM_ACT_GELU && act != FGEMM_ACT_SILU) return fast;
+    const float off = fabsf(v) * (act == FGEMM_ACT_GELU ? 5e-7f : fmaf(5e-7f, at_most(fabsf(z), 80.0f), 5e-7f));
+    const uint32_t both = pack<T>(fast - off, fast + off);
+    return ((both ^ (both >> 16)) & 0xFFFFu) == 0 ? fast : __fmul_rn(v, slope_by_definition(z, act));
 }
 
 }  // namespace h16

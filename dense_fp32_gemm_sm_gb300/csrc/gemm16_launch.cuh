@@ -75,6 +75,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     // Tiles of one product are of like sizes: 4100 rows by 256 are 17 of 256 (the last of 4), or of 242.
     const long long even = ((long long)q.M + row_tiles - 1) / row_tiles;
     p.step = (int)((even + 31) / 32 * 32 < p.nt ? (even + 31) / 32 * 32 : p.nt);
+    if (q.ragged != RAGGED_ROWS) p.nt = p.step;
     long long tiles = row_tiles * tiles_f;
     if (q.ragged == RAGGED_DEPTH) tiles *= q.groups;
     if (q.ragged == RAGGED_ROWS) tiles = (row_tiles + (q.groups < q.M ? q.groups : q.M)) * tiles_f;  // at most
@@ -83,8 +84,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.tiles_f = (int)tiles_f;
     const int own = PAIR ? p.nt / 2 : p.nt;  // rows of op(A) that a CTA brings
     // Boxes: a whole tile's where all tiles are alike, else small enough that a short tile brings little more.
-    const int own_step = PAIR ? p.step / 2 : p.step;
-    p.x_box = q.ragged == RAGGED_ROWS ? (own < 64 ? own : 64) : own_step;
+    p.x_box = q.ragged == RAGGED_ROWS && own > 64 ? 64 : own;
     const int x_bytes = q.ta ? (own + 63) / 64 * BOX_BYTES : (own + p.x_box - 1) / p.x_box * p.x_box * 128;
     p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
@@ -98,7 +98,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.table = p.stages * p.stage_bytes + (bar_bytes(p.stages) + 15) / 16 * 16;
     p.join = p.table + (table_bytes + 15) / 16 * 16;
     const int smem = 1024 + p.join + join_bytes;
-    p.acc_step = p.nt;
+    p.acc_step = PAIR ? 256 : p.nt;
     p.tmem_cols = 32;
     while (p.tmem_cols < 2 * p.acc_step) p.tmem_cols *= 2;
     if (p.tmem_cols > 512) return FGEMM_ERR_NOT_SUPPORTED;

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(32 * ACT_WARPS) act_grad_kernel(ActGrad p, int
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float v = to_float(g[j]);
-                if (gated) v = through(v, to_float(z[j]), p.act);
+                if (gated) v = through_exactly<T>(v, to_float(z[j]), p.act);
                 sum[j] += v;
                 d[j] = from_float<T>(v);
             }

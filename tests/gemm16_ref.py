@@ -5,12 +5,14 @@ exact in FP32.  A sum of K of them (and the accumulator) rounds or cuts each add
 at most by u of the largest partial sum, which is at most mag = sum |a||b|: K + 2 of these with the
 scaling by alpha.  Then
     Z is off by dz = |alpha| (K + 2) u mag + u (|alpha P| + |bias|),
-    act(Z) by 1.13 dz (no activation here is steeper) and its own evaluation: normcdff 5 units, a
-        product 1 (GELU: 8 u |y|); the exponential 2 + 1.16 |z| units, sum and division 4 (SiLU:
-        (8 + 1.2 |z|) u |y|); with FP32's underflow (1e-30) for both,
+    act(Z) by 1.13 dz (no activation here is steeper) and its own evaluation.  GELU, max(0, z) - a q: q is off by
+        (6 + 1.2 z^2) u of itself (5e-7 the polynomial and t, 2 units the exponential, z^2 of its
+        argument): (6 + 1.2 z^2) u a q + u |y|.  SiLU: the exponential 2 + 1.16 |z| units, sum and division
+        4: (8 + 1.2 |z|) u |y|.  FP32's underflow (1e-30) for both.
     beta R by u (|beta R| + |y|) more.
-    act'(Z) of a given Z:  GELU  Phi + z phi: 8 u Phi, and the exponential of -z^2/2, off by
-        (4 + 1.2 z^2) units with its argument: (6 + 1.2 z^2) u |z| phi;
+    act'(Z) of a given Z:  GELU, Phi + z phi: Phi is 1/2 + z P, a sum that rounds by u/2, P with coefficients that
+        add up to 0.4 off by u/2 of them a step and |z| times that, less than u in all (|z| P < 1/2): 1.5 u, and
+        of z phi (at most 0.25) (4 + 1.2 z^2) units of it: 1.5 u + (4 + 1.2 z^2) u |z| phi;
         SiLU  s (1 + z (1 - s)): s off by (8 + 1.2 |z|) u, 1 - s by as much of s and a unit of 1:
         (12 + 3 |z|) u s (1 + |z|);  ReLU none.
 Rounding to nearest is monotone, so an output lies between value - tol and value + tol, both
@@ -40,7 +42,9 @@ def act(z, name):
         return torch.where(z > 0, z, torch.where(z.isnan(), z, 0 * z.nan_to_num(0, 0, 0))), torch.zeros_like(z)
     if name == "gelu":
         y = z.clamp(min=-50) * cdf(z)
-        return y, 8 * U * y.abs() + 1e-30
+        q = cdf(-z.abs())
+        w = z.clamp(-30, 30)
+        return y, (6 + 1.2 * w * w) * U * w.abs() * q + U * y.abs() + 1e-30
     if name == "silu":
         y = z.clamp(min=-800) * torch.sigmoid(z)
         return y, (8 + 1.2 * z.abs()).clamp(max=200) * U * y.abs() + 1e-30
@@ -55,7 +59,7 @@ def slope(z, name):
     if name == "gelu":
         c, p = cdf(z), phi(z)
         w = z.clamp(-50, 50)
-        return c + w * p, 8 * U * c + (6 + 1.2 * w * w) * U * w.abs() * p + 1e-30
+        return c + w * p, 1.5 * U + (4 + 1.2 * w * w) * U * w.abs() * p
     if name == "silu":
         s = torch.sigmoid(z)
         return s * (1 + z.clamp(-800, 800) * torch.sigmoid(-z)), (12 + 3 * a) * U * s * (1 + a) + 1e-30
