@@ -44,12 +44,15 @@ struct Product {
 };
 
 // How a product runs: tiles of 128 (pair: 256) columns of the output by at most nt rows; a tile's
-// depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs or pairs); CTAs an
-// SM; and whether sums over a long depth are added up in turns (where they are kept in FP32: `fine`).
+// depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs or pairs);
+// and whether sums over a long depth are added up in turns (where they are kept in FP32: `fine`).
 struct Plan {
-    int pair, nt, ranks, per_sm, in_turns;
+    int pair, nt, ranks, in_turns;
 };
 Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, bool fine, int sms);
+
+// Depth whose products the tensor core adds up at a time, where sums are kept in FP32.
+constexpr int LONG_DEPTH = 768;
 
 // Least rows of a tile where column sums are wanted, which bounds their partial sums.
 constexpr int SUMS_ROWS = 32;
@@ -57,12 +60,17 @@ constexpr int SUMS_ROWS = 32;
 inline long long partial_rows(long long groups, long long M) { return 2 * ((M + SUMS_ROWS - 1) / SUMS_ROWS + groups); }
 
 fgemm_status launch_product(const Product &q, cudaStream_t stream);
-template <class T> fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream);
+template <class T, class O> fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream);
 
-// Y (rows x cols, ldy a multiple of 8) = X (ldx), 16-bit elements, for `batch` matrices stride_x
-// elements apart (Y's follow each other).
-fgemm_status launch_realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch,
-                            void *y, long long ldy, cudaStream_t stream);
+// Copies of `batch` matrices of 16-bit elements, rows x cols, whose rows start on 16 bytes at y.  pieces 0: none.
+struct Realign {
+    const uint16_t *x;
+    long long ldx, stride_x, rows, pieces;
+    int cols, per_row;  // 16-byte pieces of a row
+    uint4 *y;
+};
+Realign realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch, void *y);
+fgemm_status launch_realign(const Realign &a, const Realign &b, cudaStream_t stream);
 
 struct ActGrad {
     fgemm_dtype type;

@@ -84,15 +84,17 @@ fgemm_status run(Product &q, float *col_sums, void *workspace, size_t workspace_
     void *const b = copy_b ? space.take(copy_bytes(b_rows, b_cols, batch)) : nullptr;
     if (!space.ok || ((col_sums || copy_a || copy_b) && !aligned(workspace, 16))) return FGEMM_ERR_INVALID_VALUE;
     if (!dims_supported(q.M, q.N, q.K)) return FGEMM_ERR_NOT_SUPPORTED;
-    if (copy_a) {
-        const fgemm_status st = launch_realign(q.a, q.lda, 0, a_rows, (int)a_cols, 1, a, even_ld(a_cols), stream);
+    if (copy_a || copy_b) {
+        const Realign none{}, ca = copy_a ? realign(q.a, q.lda, 0, a_rows, (int)a_cols, 1, a) : none;
+        const Realign cb = copy_b ? realign(q.b, q.ldb, q.stride_b, b_rows, (int)b_cols, batch, b) : none;
+        const fgemm_status st = launch_realign(ca, cb, stream);
         if (st != FGEMM_OK) return st;
+    }
+    if (copy_a) {
         q.a = a;
         q.lda = even_ld(a_cols);
     }
     if (copy_b) {
-        const fgemm_status st = launch_realign(q.b, q.ldb, q.stride_b, b_rows, (int)b_cols, batch, b, even_ld(b_cols), stream);
-        if (st != FGEMM_OK) return st;
         q.b = b;
         q.ldb = even_ld(b_cols);
         q.stride_b = b_rows * q.ldb;

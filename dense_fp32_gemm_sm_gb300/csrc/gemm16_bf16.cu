@@ -4,7 +4,7 @@
 namespace fgemm {
 namespace h16 {
 
-template fgemm_status launch_product_type<__nv_bfloat16>(const Product &q, const Plan &plan, cudaStream_t stream);
+template fgemm_status launch_product_type<__nv_bfloat16, __nv_bfloat16>(const Product &q, const Plan &plan, cudaStream_t stream);
 
 }  // namespace h16
 }  // namespace fgemm

@@ -1,0 +1,10 @@
+// gemm16_f16_f32.cu -- kernel instances of the products of F16 matrices into FP32.
+#include "gemm16_launch.cuh"
+
+namespace fgemm {
+namespace h16 {
+
+template fgemm_status launch_product_type<__half, float>(const Product &q, const Plan &plan, cudaStream_t stream);
+
+}  // namespace h16
+}  // namespace fgemm

@@ -52,10 +52,10 @@ static bool prepare(unsigned **err, int *sms)
 
 static bool paired(const void *p, long long ld, fgemm_dtype t) { return t != FGEMM_F32 && reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
-template <bool PAIR, class T, class O, bool LONG>
+template <bool PAIR, class T, class O, bool LONG, bool FULL>
 static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    constexpr auto kernel = &gemm16_kernel<PAIR, T, O, LONG>;
+    constexpr auto kernel = &gemm16_kernel<PAIR, T, O, LONG, FULL>;
     unsigned *err = nullptr;
     int sms = 0;
     if (!prepare<decltype(kernel), kernel>(&err, &sms)) {
@@ -89,8 +89,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
     const int join_bytes = !PAIR && plan.ranks > 1 ? (p.nt + plan.ranks) * TILE_F * 4 : 0;  // (shares are rounded up)
-    const int room = (plan.per_sm > 1 ? MOST_SMEM / plan.per_sm - 1024 : MOST_SMEM) - 1024 - table_bytes - join_bytes -
-                     bar_bytes(MAX_STAGES) - 32;
+    const int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 32;
     p.blocks = room >= 6 * p.block_bytes ? 2 : 1;
     p.stage_bytes = p.blocks * p.block_bytes;
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
@@ -104,6 +103,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     if (p.tmem_cols > 512) return FGEMM_ERR_NOT_SUPPORTED;
     p.y_pairs = paired(q.y, q.ldy, q.out_type) && q.stride_y % 2 == 0 && q.N % 2 == 0;
     p.z_pairs = paired(q.z, q.ldz, q.type) && q.N % 2 == 0;
+    p.r_pairs = paired(q.r, q.ldr, q.out_type) && q.stride_y % 2 == 0 && q.N % 2 == 0;
     p.wait_limit_ns = tc_wait_limit_ns();
     p.withhold = tc_withheld_k_block();
     if (q.K > 0 && q.alpha != 0.0f) {
@@ -114,24 +114,25 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
             !make_map(&p.x, q.a, bf16, 2, q.ta ? q.K : q.M, q.ta ? q.M : q.K, q.lda, 1, 0, q.ta ? DEPTH : p.x_box))
             return FGEMM_ERR_NOT_SUPPORTED;
     }
-    const long long most = PAIR ? sms / 2 : (long long)sms * plan.per_sm;
+    const long long most = PAIR ? sms / 2 : sms;
     const dim3 grid((unsigned)(ctas * ((!PAIR && plan.ranks > 1) || tiles < most ? tiles : most)));
     return mx::launch(kernel, grid, threads_of(PAIR), (size_t)smem, stream, (unsigned)ctas, p, err) == cudaSuccess ? FGEMM_OK
                                                                                                         : FGEMM_ERR_LAUNCH;
 }
 
-template <class T, class O, bool LONG>
+template <bool PAIR, class T, class O>
 static fgemm_status launch_kind(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    return plan.pair ? launch_instance<true, T, O, LONG>(q, plan, stream) : launch_instance<false, T, O, LONG>(q, plan, stream);
+    const bool full = q.slope || q.z || q.beta != 0.0f || q.partial;
+    if (plan.in_turns)
+        return full ? launch_instance<PAIR, T, O, true, true>(q, plan, stream) : launch_instance<PAIR, T, O, true, false>(q, plan, stream);
+    return full ? launch_instance<PAIR, T, O, false, true>(q, plan, stream) : launch_instance<PAIR, T, O, false, false>(q, plan, stream);
 }
 
-template <class T>
+template <class T, class O>
 fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    if (q.out_type == FGEMM_F32)
-        return plan.in_turns ? launch_kind<T, float, true>(q, plan, stream) : launch_kind<T, float, false>(q, plan, stream);
-    return plan.in_turns ? launch_kind<T, T, true>(q, plan, stream) : launch_kind<T, T, false>(q, plan, stream);
+    return plan.pair ? launch_kind<true, T, O>(q, plan, stream) : launch_kind<false, T, O>(q, plan, stream);
 }
 
 }  // namespace h16

@@ -14,9 +14,10 @@ double most(double a, double b) { return a > b ? a : b; }
 double least(double a, double b) { return a < b ? a : b; }
 
 // The estimate in us.  Fitted to 660 measurements of 60 products (1 to 8192 rows, 80 to 11008 columns, depths of 72
-// to 11008, both ends cold in L2): the plan of the least estimate took 1.6 % longer than the best one on average.
-//   64 of depth through a pair's barriers 0.139 us and more with the rows of its tile, through one CTA's
-//   0.103; a tile's epilogue; what all CTAs bring through L2 at 14 TB/s; the launch, and the joining of ranks.
+// to 11008, operands not in L2): the plan of the least estimate took 1.6 % longer than the best one on average.
+//   64 of depth through a pair's barriers 0.165 us and more with the rows of its tile, through one CTA's
+//   0.168; a tile's epilogue; what all CTAs bring through L2 at 15.7 TB/s, and from memory at 6.4; the launch, and the
+//   joining of ranks.
 struct Work {
     double row_tiles, rows;  // tiles of rows (all groups'), rows of one
     double N, blocks;        // columns, 64-deep blocks of a product
@@ -28,12 +29,12 @@ double estimate(const Work &w, bool pair, int ranks, int sms)
 {
     const double tiles = w.row_tiles * w.products * up(w.N, pair ? 256 : 128);
     const double stage = (pair ? 32768 : 16384) + 128 * w.rows, share = up(w.blocks, ranks);
-    const double memory = most(tiles * ranks * share * stage / 14.2e6, w.bytes / 10.1e6);
+    const double memory = most(tiles * ranks * share * stage / 15.7e6, w.bytes / 6.4e6);
     const double waves = pair ? up(tiles, sms / 2) : up(tiles * ranks, sms);
-    const double depth = share * (pair ? most(0.133, 0.1385 + 0.00074 * w.rows) : 0.1034);
-    const double epilogue = (pair ? 0.01135 : 0.00573) * w.rows;
-    const double t = (pair ? 3.03 : 3.18) + most(waves * most(depth, epilogue) + least(depth, epilogue), memory);
-    return ranks > 1 ? t + 0.62 + 0.0316 * w.rows : t;
+    const double depth = share * (pair ? most(0.165, 0.088 + 0.00083 * w.rows) : 0.168);
+    const double epilogue = (pair ? 0.0104 : 0.01285) * w.rows;
+    const double t = (pair ? 2.47 : 2.12) + most(waves * most(depth, epilogue) + least(depth, epilogue), memory);
+    return ranks > 1 ? t + 1.5 + 0.0154 * w.rows : t;
 }
 
 }  // namespace
@@ -45,7 +46,7 @@ Plan plan_product(long long M, long long N, long long K, int ragged, long long g
     const double depth = ragged == RAGGED_DEPTH ? (double)K / (double)groups : (double)K;
     // Column sums: the room for partial ones is two rows for every SUMS_ROWS rows and two a group.
     const int least_rows = sums ? SUMS_ROWS : 1;
-    Plan best{0, 0, 1, 1, 0};
+    Plan best{0, 0, 1, 0};
     double least_time = 0;
     const auto consider = [&](bool pair, int nt, int ranks) {
         Work w;
@@ -56,13 +57,13 @@ Plan plan_product(long long M, long long N, long long K, int ragged, long long g
         w.blocks = up(depth, 64) + (ragged == RAGGED_DEPTH && groups > 1 ? 0.5 : 0.0);
         w.products = ragged == RAGGED_DEPTH ? (double)groups : 1.0;
         w.bytes = 2.0 * (M * (double)K + used * K * (double)N) + 2.0 * w.products * M * (double)N;
-        // A cluster's ranks all run at once or not at all: no more of them than SMs.
-        const double ctas = w.row_tiles * w.products * up(w.N, 128);
-        if (ranks > 1 && (ctas * ranks > sms || w.blocks < 2 * ranks)) return;
+        // A cluster's ranks all run at once or not at all, on SMs of one part of the GPU: no more of them than SMs, of large
+        // clusters than four fifths (24 clusters of six did not fit at once: 14.7 us in place of 8.5).
+        const double ctas = w.row_tiles * w.products * up(w.N, 128) * ranks;
+        if (ranks > 1 && (ctas > sms || (ranks > 4 && ctas > 0.8 * sms) || w.blocks < 2 * ranks)) return;
         const double t = estimate(w, pair, ranks, sms);
         if (best.nt == 0 || t < least_time) {
-            // Two CTAs an SM where there are more tiles than SMs: the epilogue of one beside the products of the other.
-            best = Plan{pair, nt, ranks, !pair && ctas > sms ? 2 : 1, 0};
+            best = Plan{pair, nt, ranks, 0};
             least_time = t;
         }
     };
@@ -75,18 +76,46 @@ Plan plan_product(long long M, long long N, long long K, int ragged, long long g
             consider(false, nt, ranks);
         }
     }
-    best.in_turns = fine && K > 512;
+    best.in_turns = fine && K > LONG_DEPTH;
     return best;
 }
+
+namespace {
+
+// The last plans of this thread: weighing the candidates takes 1 us of a call's 4.
+struct Planned {
+    long long M, N, K;
+    int ragged, groups, sums, fine, sms;
+    Plan plan;
+};
+
+Plan planned(const Product &q, int sms)
+{
+    static thread_local Planned last[8];
+    static thread_local unsigned next = 0;
+    const int sums = q.partial != nullptr, fine = sums || q.out_type == FGEMM_F32;
+    for (const Planned &p : last)
+        if (p.M == q.M && p.N == q.N && p.K == q.K && p.ragged == q.ragged && p.groups == q.groups && p.sums == sums &&
+            p.fine == fine && p.sms == sms)
+            return p.plan;
+    Planned &p = last[next++ % 8];
+    p = Planned{q.M, q.N, q.K, q.ragged, q.groups, sums, fine, sms,
+                plan_product(q.M, q.N, q.K, q.ragged, q.groups, sums != 0, fine != 0, sms)};
+    return p.plan;
+}
+
+}  // namespace
 
 fgemm_status launch_product(const Product &q, cudaStream_t stream)
 {
     int sms = 0;
     if (device_sm_count(&sms) != 0) return FGEMM_ERR_LAUNCH;
-    const Plan plan = plan_product(q.M, q.N, q.K, q.ragged, q.groups, q.partial != nullptr,
-                                   q.partial != nullptr || q.out_type == FGEMM_F32, sms);
-    return q.type == FGEMM_BF16 ? launch_product_type<__nv_bfloat16>(q, plan, stream)
-                                : launch_product_type<__half>(q, plan, stream);
+    const Plan plan = planned(q, sms);
+    if (q.type == FGEMM_BF16)
+        return q.out_type == FGEMM_F32 ? launch_product_type<__nv_bfloat16, float>(q, plan, stream)
+                                       : launch_product_type<__nv_bfloat16, __nv_bfloat16>(q, plan, stream);
+    return q.out_type == FGEMM_F32 ? launch_product_type<__half, float>(q, plan, stream)
+                                   : launch_product_type<__half, __half>(q, plan, stream);
 }
 
 }  // namespace h16

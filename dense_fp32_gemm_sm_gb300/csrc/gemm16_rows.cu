@@ -13,21 +13,21 @@ namespace {
 
 // ---- rows on 16-byte boundaries ----------------------------------------------------------
 
-// A thread makes 16 bytes of a row.  Bounded by its reads, 2 bytes a lane and instruction, of which eight
-// share their sectors in L1.
-__global__ void __launch_bounds__(256) realign_kernel(const uint16_t *x, long long ldx, long long stride_x, long long rows, int cols,
-                                                      long long total, uint4 *y, int pieces)
+// One or two matrices (or batches of them), the second's pieces behind the first's: a thread makes 16 bytes of a
+// row.  Bounded by its reads, 2 bytes a lane and instruction, of which eight share their sectors in L1.
+__global__ void __launch_bounds__(256) realign_kernel(Realign a, Realign b)
 {
     after_previous_kernel();
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = i / pieces;
-        const int c0 = (int)(i - row * pieces) * 8;
-        const long long m = row / rows;
-        const uint16_t *const src = x + m * stride_x + (row - m * rows) * ldx + c0;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < a.pieces + b.pieces; i += gridDim.x * 256ll) {
+        const bool second = i >= a.pieces;
+        const Realign &m = second ? b : a;
+        const long long piece = second ? i - a.pieces : i, row = piece / m.per_row, matrix = row / m.rows;
+        const int c0 = (int)(piece - row * m.per_row) * 8;
+        const uint16_t *const src = m.x + matrix * m.stride_x + (row - matrix * m.rows) * m.ldx + c0;
         uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c0 + j < cols ? src[j] : 0;
-        y[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        for (int j = 0; j < 8; ++j) v[j] = c0 + j < m.cols ? src[j] : 0;
+        m.y[piece] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
 
@@ -40,7 +40,7 @@ constexpr int SLICE_ROWS = 64;
 // D = G act'(Z) for a slice of a group's rows by 256 columns, and its column sums.  VEC: a lane's eight
 // columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(32 * ACT_WARPS) act_grad_kernel(ActGrad p, int strips, int slices)
+__global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, int strips, int slices)
 {
     __shared__ float sums[ACT_WARPS][ACT_COLUMNS];
     after_previous_kernel();
@@ -61,35 +61,47 @@ __global__ void __launch_bounds__(32 * ACT_WARPS) act_grad_kernel(ActGrad p, int
     T *const D = static_cast<T *>(p.d);
     const bool gated = p.act != FGEMM_ACT_NONE;
     if (column(0) < p.N) {
-#pragma unroll 2
-        for (long long r = from + warp; r < to; r += ACT_WARPS) {
-            __align__(16) T g[8], z[8];
-            if (VEC) {
-                *reinterpret_cast<uint4 *>(g) = *reinterpret_cast<const uint4 *>(G + r * p.ldg + column(0));
-                if (gated) *reinterpret_cast<uint4 *>(z) = *reinterpret_cast<const uint4 *>(Z + r * p.ldz + column(0));
-            } else {
+        // Two rows of a warp are on their way at a time.  (Four leave two blocks an SM in place of four.)
+        constexpr int BATCH = 2;
+        for (long long r0 = from + warp; r0 < to; r0 += BATCH * ACT_WARPS) {
+            __align__(16) T g[BATCH][8], z[BATCH][8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = column(j) < p.N;
-                    g[j] = in ? G[r * p.ldg + column(j)] : from_float<T>(0.0f);
-                    if (gated) z[j] = in ? Z[r * p.ldz + column(j)] : from_float<T>(0.0f);
-                }
-            }
-            __align__(16) T d[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = to_float(g[j]);
-                if (gated) v = through_exactly<T>(v, to_float(z[j]), p.act);
-                sum[j] += v;
-                d[j] = from_float<T>(v);
-            }
-            if (D) {
+            for (int i = 0; i < BATCH; ++i) {
+                const long long r = r0 + i * ACT_WARPS;
+                if (r >= to) break;
                 if (VEC) {
-                    *reinterpret_cast<uint4 *>(D + r * p.ldd + column(0)) = *reinterpret_cast<const uint4 *>(d);
+                    *reinterpret_cast<uint4 *>(g[i]) = *reinterpret_cast<const uint4 *>(G + r * p.ldg + column(0));
+                    if (gated) *reinterpret_cast<uint4 *>(z[i]) = *reinterpret_cast<const uint4 *>(Z + r * p.ldz + column(0));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (column(j) < p.N) D[r * p.ldd + column(j)] = d[j];
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = column(j) < p.N;
+                        g[i][j] = in ? G[r * p.ldg + column(j)] : from_float<T>(0.0f);
+                        if (gated) z[i][j] = in ? Z[r * p.ldz + column(j)] : from_float<T>(0.0f);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const long long r = r0 + i * ACT_WARPS;
+                if (r >= to) break;
+                __align__(16) uint32_t d[4];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    float v0 = to_float(g[i][j]), v1 = to_float(g[i][j + 1]);
+                    if (gated) through_exactly<T>(v0, v1, to_float(z[i][j]), to_float(z[i][j + 1]), p.act);
+                    sum[j] += v0;
+                    sum[j + 1] += v1;
+                    d[j / 2] = pack<T>(v0, v1);
+                }
+                if (D) {
+                    if (VEC) {
+                        *reinterpret_cast<uint4 *>(D + r * p.ldd + column(0)) = *reinterpret_cast<const uint4 *>(d);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (column(j) < p.N) D[r * p.ldd + column(j)] = reinterpret_cast<const T *>(d)[j];
+                    }
                 }
             }
         }
@@ -138,14 +150,17 @@ fgemm_status status(cudaError_t e) { return e == cudaSuccess ? FGEMM_OK : FGEMM_
 
 }  // namespace
 
-fgemm_status launch_realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch, void *y,
-                            long long ldy, cudaStream_t stream)
+Realign realign(const void *x, long long ldx, long long stride_x, long long rows, int cols, long long batch, void *y)
 {
-    const int pieces = (int)(ldy / 8);
-    const long long total = rows * batch * pieces, blocks = (total + 255) / 256;
+    const int per_row = (cols + 7) / 8;
+    return Realign{static_cast<const uint16_t *>(x), ldx, stride_x, rows, rows * batch * per_row, cols, per_row, static_cast<uint4 *>(y)};
+}
+
+fgemm_status launch_realign(const Realign &a, const Realign &b, cudaStream_t stream)
+{
+    const long long blocks = (a.pieces + b.pieces + 255) / 256;
     const dim3 grid((unsigned)(blocks < 152 * 64 ? blocks : 152 * 64));
-    return status(mx::launch(realign_kernel, grid, 256, 0, stream, 1, static_cast<const uint16_t *>(x), ldx, stride_x, rows, cols,
-                             total, static_cast<uint4 *>(y), pieces));
+    return status(mx::launch(realign_kernel, grid, 256, 0, stream, 1, a, b));
 }
 
 long long act_slices(long long groups, long long M)

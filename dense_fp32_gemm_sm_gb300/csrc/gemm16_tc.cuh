@@ -37,7 +37,7 @@ constexpr int DEPTH = 64;        // 16-bit elements of a block: 128 bytes
 constexpr int SETS = 2;  // of four epilogue warps: one for 32 lanes of tensor memory each
 __host__ __device__ constexpr int threads_of(bool pair) { return 64 + 128 * SETS + (pair ? 32 : 0); }  // producer, MMA, epilogue; mender
 constexpr int CHUNK = 16;      // accumulator columns that a warp finishes at a time
-constexpr int LONG_DEPTH = 512;  // depth whose products the tensor core adds up, where sums are kept in FP32
+
 constexpr int MAX_STAGES = 12;
 constexpr int W_BYTES = TILE_F * 128;
 constexpr int BOX_BYTES = 64 * 128;  // a box of an operand stored across the depth
@@ -54,7 +54,7 @@ struct Args {
     int stages, stage_bytes, acc_step, tmem_cols;
     int blocks, block_bytes;  // 64-deep blocks of a stage (1 or 2), each of op(B), then of op(A)
     int table, join;         // offsets in shared memory: the groups' table, the sums that ranks send each other
-    int y_pairs, z_pairs;    // pairs of columns are aligned
+    int y_pairs, z_pairs, r_pairs;  // pairs of columns are aligned
     unsigned long long wait_limit_ns;
     int withhold;
 };
@@ -272,13 +272,61 @@ __device__ __forceinline__ void make_table(const Args &p, int *table, int lane)
 
 // ---- epilogue ---------------------------------------------------------------------------
 
-// Elements [row c][this lane's column], c < rows, into v.
-template <class T, int N>
-__device__ __forceinline__ void load_rows(float (&v)[N], const T *src, long long ld, int rows, bool in)
-{
+// Elements [row c][this lane's column], c < rows, on their way to registers: loaded here, taken as
+// floats later.  16-bit types, where pairs of columns are aligned: lanes 2i and 2i + 1 load both columns of
+// a row each, and exchange them then.
+template <int N>
+struct Ahead {
+    uint32_t raw[N];
+
+    template <class T>
+    __device__ __forceinline__ void load(const T *src, long long ld, int rows, bool in, bool pairs)
+    {
+        if constexpr (sizeof(T) == 2) {
+            if (pairs) {
+                const int odd = threadIdx.x & 1, last = in ? rows - odd : 0;
+                src += odd ? ld - 1 : 0;
 #pragma unroll
-    for (int c = 0; c < N; ++c, src += ld) v[c] = in && c < rows ? to_float(*src) : 0.0f;
-}
+                for (int c = 0; c < N; c += 2, src += 2 * ld)
+                    raw[c] = c < last ? *reinterpret_cast<const uint32_t *>(src) : 0u;
+                return;
+            }
+        }
+        const int last = in ? rows : 0;
+#pragma unroll
+        for (int c = 0; c < N; ++c, src += ld) {
+            if constexpr (sizeof(T) == 2)
+                raw[c] = c < last ? *reinterpret_cast<const uint16_t *>(src) : 0u;
+            else
+                raw[c] = c < last ? __float_as_uint(to_float(*src)) : 0u;
+        }
+    }
+
+    template <class T>
+    __device__ __forceinline__ void take(float (&v)[N], bool pairs) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            if (pairs) {
+                const bool odd = threadIdx.x & 1;
+#pragma unroll
+                for (int c = 0; c < N; c += 2) {
+                    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, raw[c], 1);
+                    const uint32_t first = odd ? other >> 16 : raw[c], second = odd ? raw[c] >> 16 : other;
+                    v[c] = from_bits<T>(first);
+                    v[c + 1] = from_bits<T>(second);
+                }
+                return;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            if constexpr (sizeof(T) == 2)
+                v[c] = from_bits<T>(raw[c]);
+            else
+                v[c] = __uint_as_float(raw[c]);
+        }
+    }
+};
 
 // Store v to rows c < rows of this lane's column.  16-bit types, where pairs of columns are aligned:
 // lanes 2i and 2i + 1 exchange their values of two rows, and each stores both columns of one.
@@ -306,7 +354,10 @@ __device__ __forceinline__ void store_rows(T *out, long long ld, const float (&v
 
 // What the epilogue needs of the arguments, in registers: from the constant bank each of them would
 // cost a chunk of rows 40 cycles and more (a chunk of 16 rows took 1400 cycles).
-enum { WITH_Z = 16, WITH_R = 32, WITH_SUMS = 64, SLOPE = 128, Y_PAIRS = 256, Z_PAIRS = 512 };
+enum { WITH_Z = 16, WITH_R = 32, WITH_SUMS = 64, SLOPE = 128, Y_PAIRS = 256, Z_PAIRS = 512, R_PAIRS = 1024 };
+// FULL: with Z, R, a slope or column sums.  Without, in instances of their own, the code of a chunk is short enough
+// that jumps over what a call does not want cost nothing (1353 x 6488 x 72: 12.5 us in place of 10.3).
+template <bool FULL>
 struct Epilogue {
     float alpha, beta;
     int mode;  // act, and the above
@@ -322,17 +373,31 @@ struct Epilogue {
         ldr = __shfl_sync(0xFFFFFFFFu, q.ldr, 0);
         const int z = q.slope ? q.act != FGEMM_ACT_NONE : q.z != nullptr;
         mode = uniform(q.act | (z ? WITH_Z : 0) | (!q.slope && q.beta != 0.0f ? WITH_R : 0) | (q.partial ? WITH_SUMS : 0) |
-                       (q.slope ? SLOPE : 0) | (p.y_pairs ? Y_PAIRS : 0) | (p.z_pairs ? Z_PAIRS : 0));
+                       (q.slope ? SLOPE : 0) | (p.y_pairs ? Y_PAIRS : 0) | (p.z_pairs ? Z_PAIRS : 0) | (p.r_pairs ? R_PAIRS : 0));
     }
     __device__ __forceinline__ int act() const { return mode & 15; }
-    __device__ __forceinline__ bool has(int what) const { return (mode & what) != 0; }
+    __device__ __forceinline__ bool has(int what) const
+    {
+        return (FULL || (what & (WITH_Z | WITH_R | WITH_SUMS | SLOPE)) == 0) && (mode & what) != 0;
+    }
+
+    // What finish_rows reads, Z for a slope or R.
+    template <class T, class O, int N>
+    __device__ __forceinline__ void load(Ahead<N> &ahead, const T *z, const O *r, int rows, bool in) const
+    {
+        if (has(SLOPE)) {
+            if (has(WITH_Z)) ahead.load(z, ldz, rows, in, has(Z_PAIRS));
+        } else if (has(WITH_R)) {
+            ahead.load(r, ldr, rows, in, has(R_PAIRS));
+        }
+    }
 };
 
-// N sums of this lane's column to `rows` rows of it, the first at y (and z, r); returns the sum of what
-// Y holds of them, before its rounding.
-template <class T, class O, int N>
-__device__ __forceinline__ float finish_rows(const Epilogue &q, float (&v)[N], O *y, T *z, const O *r, float bias, int rows,
-                                             bool in)
+// N sums of this lane's column to `rows` rows of it, the first at y (and z); ahead: what of Z or R goes in.
+// Returns the sum of what Y holds of them, before its rounding.
+template <class T, class O, bool FULL, int N>
+__device__ __forceinline__ float finish_rows(const Epilogue<FULL> &q, float (&v)[N], const Ahead<N> &ahead, O *y, T *z, float bias,
+                                             int rows, bool in)
 {
 #pragma unroll
     for (int c = 0; c < N; ++c) v[c] = fmaf(q.alpha, v[c], bias);
@@ -340,7 +405,7 @@ __device__ __forceinline__ float finish_rows(const Epilogue &q, float (&v)[N], O
     if (q.has(SLOPE)) {
         if (q.has(WITH_Z)) {
             float x[N];
-            load_rows(x, z, q.ldz, rows, in);
+            ahead.template take<T>(x, q.has(Z_PAIRS));
             if (act == FGEMM_ACT_RELU) {
 #pragma unroll
                 for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_RELU);
@@ -366,7 +431,7 @@ __device__ __forceinline__ float finish_rows(const Epilogue &q, float (&v)[N], O
         }
         if (q.has(WITH_R)) {
             float x[N];
-            load_rows(x, r, q.ldr, rows, in);
+            ahead.template take<O>(x, q.has(R_PAIRS));
 #pragma unroll
             for (int c = 0; c < N; ++c) v[c] = fmaf(q.beta, x[c], v[c]);
         }
@@ -436,8 +501,8 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
 // add these sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
 // 2048, sums come out 2.1e-6 off (2-norm, random operands), of 512 at a time 0.6e-6, which counts where
 // they are kept in FP32.
-template <bool PAIR, class T, class O, bool LONG>
-__global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
+template <bool PAIR, class T, class O, bool LONG, bool FULL>
+__global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
 {
     constexpr int THREADS = threads_of(PAIR);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -756,7 +821,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
                     tc::mbar_arrive(acc_free_bar(acc));
             }
         };
-        const Epilogue epi(p);
+        const Epilogue<FULL> epi(p);
         const float *const biases = p.q.bias;
         const int N = uniform(p.q.N), acc_step = uniform(p.acc_step);
         const long long stride_y = __shfl_sync(0xFFFFFFFFu, p.q.stride_y, 0);
@@ -777,7 +842,10 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             float sum = 0.0f;
             const int share = (o.valid + ranks - 1) / ranks;  // rows that a rank of the cluster joins
-            auto finish = [&](float (&v)[CHUNK], int c0) {
+            auto load_ahead = [&](Ahead<CHUNK> &ahead, int c0) {
+                if (c0 < o.valid && !split) epi.load(ahead, z + c0 * epi.ldz, r_at + c0 * epi.ldr, o.valid - c0, in);
+            };
+            auto finish = [&](float (&v)[CHUNK], const Ahead<CHUNK> &ahead, int c0) {
                 if (split) {  // to the rank that joins the row: by rank, row, 128 columns
                     int to = c0 / share, row = c0 - to * share;
                     const uint32_t mine = sbase + p.join + (uint32_t)(rank * share * TILE_F + 32 * q + lane) * 4;
@@ -792,9 +860,13 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
                         }
                     }
                 } else {
-                    sum += finish_rows<T, O>(epi, v, y + c0 * epi.ldy, z + c0 * epi.ldz, r_at + c0 * epi.ldr, bias, o.valid - c0, in);
+                    sum += finish_rows<T, O, FULL>(epi, v, ahead, y + c0 * epi.ldy, z + c0 * epi.ldz, bias, o.valid - c0, in);
                 }
             };
+            // What of Z or R the first chunk takes comes during the wait, each next chunk's during the one before
+            // (the gradient of 8192 x 4096, depth 2048, through GELU: 174 us without, 119 with).
+            Ahead<CHUNK> ahead;
+            if (!LONG) load_ahead(ahead, CHUNK * set);
             bool ok = true;
             if constexpr (LONG) {
                 // All turns but the last are added up in registers, and then with the last one where its
@@ -832,6 +904,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
             }
+            if (LONG) load_ahead(ahead, CHUNK * set);
             if (!LONG || turns == 1) ok = turns == 0 || warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim);
             if (!ok) break;
             tc::tc_fence_after();
@@ -839,14 +912,16 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
             for (int c0 = CHUNK * set; c0 < o.valid; c0 += SETS * CHUNK) {
                 float v[CHUNK];
                 load_sums(lanes + (uint32_t)((j & 1) * acc_step + c0), turns > 0, v);
-                finish(v, c0);
+                const Ahead<CHUNK> now = ahead;
+                load_ahead(ahead, c0 + SETS * CHUNK);
+                finish(v, now, c0);
             }
             if (turns > 0) {
                 give_back(j & 1);
                 ++j;
             }
             const long long row = (long long)SETS * o.row_tile + set;
-            if (p.q.partial && in && row < p.q.partials) p.q.partial[row * p.q.N + n] = sum;
+            if (FULL && p.q.partial && in && row < p.q.partials) p.q.partial[row * p.q.N + n] = sum;
         }
         __syncwarp();
     }
@@ -855,7 +930,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
         // Every CTA of the cluster has been sent its share of the tile's rows by all ranks (its own room
         // for them is apart from the stages, which it may still use meanwhile) and adds them up, in rank
         // order.  (A rank that gave up sends nothing; the error word says that Y is undefined.)
-        const Epilogue epi(p);
+        const Epilogue<FULL> epi(p);
         float bias = 0.0f;
         const int q = warp & 3, set = (warp - 2) >> 2, n = first.f0 + TILE_F * half + 32 * q + lane;
         if (warp >= 2 && any && p.q.bias && n < p.q.N) bias = p.q.bias[(long long)first.e * p.q.N + n];
@@ -866,6 +941,10 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
             constexpr int FEW = 8;
 #pragma unroll 1
             for (int c0 = FEW * set; c0 < rows; c0 += SETS * FEW) {
+                const long long row = first.t0 + rank * share + c0, base = first.e * p.q.stride_y + n;
+                T *const z = static_cast<T *>(p.q.z) + n + row * epi.ldz;
+                Ahead<FEW> ahead;
+                epi.load(ahead, z, static_cast<const O *>(p.q.r) + base + row * epi.ldr, rows - c0, n < p.q.N);
                 float v[FEW];
 #pragma unroll
                 for (int c = 0; c < FEW; ++c) v[c] = 0.0f;
@@ -875,14 +954,12 @@ __global__ void __launch_bounds__(threads_of(PAIR), PAIR ? 1 : 2) gemm16_kernel(
                     for (int c = 0; c < FEW; ++c)
                         if (c0 + c < rows) v[c] += part[(r * share + c0 + c) * TILE_F];
                 }
-                const long long row = first.t0 + rank * share + c0, base = first.e * p.q.stride_y + n;
-                finish_rows<T, O>(epi, v, static_cast<O *>(p.q.y) + base + row * epi.ldy, static_cast<T *>(p.q.z) + n + row * epi.ldz,
-                                  static_cast<const O *>(p.q.r) + base + row * epi.ldr, bias, rows - c0, n < p.q.N);
+                finish_rows<T, O, FULL>(epi, v, ahead, static_cast<O *>(p.q.y) + base + row * epi.ldy, z, bias, rows - c0, n < p.q.N);
             }
         }
     }
 
-    if (p.q.partial_start && blockIdx.x == 0) {
+    if (FULL && p.q.partial_start && blockIdx.x == 0) {
         for (int e = threadIdx.x; e <= p.q.groups; e += THREADS)
             p.q.partial_start[e] = SETS * (p.q.ragged == RAGGED_ROWS ? walk.first[e] / p.tiles_f : p.tiles_t * e);
     }
