@@ -56,7 +56,7 @@ constexpr int LONG_DEPTH = 768;
 
 // Least rows of a tile where column sums are wanted, which bounds their partial sums.
 constexpr int SUMS_ROWS = 32;
-// Partial sums of columns: two of every tile of rows, or one of every 64 rows (act16_grad).
+// Partial sums of columns: two of every tile of rows, or (act16_grad) one of every slice, of 16 rows at least.
 inline long long partial_rows(long long groups, long long M) { return 2 * ((M + SUMS_ROWS - 1) / SUMS_ROWS + groups); }
 
 fgemm_status launch_product(const Product &q, cudaStream_t stream);
@@ -82,7 +82,7 @@ struct ActGrad {
     float *partial;  // or null: no sums
 };
 // Slices of a group's rows, each with a partial sum.
-long long act_slices(long long groups, long long M);
+long long act_slices(long long groups, long long M, long long N);
 fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream);
 
 // sums[e][j] = the partial rows start[e] .. start[e+1] of column j, in order (start == null: `each` a group).

@@ -329,7 +329,7 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
     p.partial = col_sums ? static_cast<float *>(workspace) : nullptr;
     const fgemm_status st = launch_act_grad(p, stream);
     if (st != FGEMM_OK || !col_sums) return st;
-    return launch_sums(p.partial, nullptr, act_slices(groups, M), groups, N, col_sums, stream);
+    return launch_sums(p.partial, nullptr, act_slices(groups, M, N), groups, N, col_sums, stream);
 }
 
 int fgemm_gemm16_plan(fgemm_dtype out_type, int grouped, int groups, int M, int N, int K, int sums, int num_sms)

@@ -1,4 +1,6 @@
-// gemm16_device.cuh -- activations of the 16-bit layers and their derivatives, in FP32.
+// gemm16_device.cuh -- activations of the 16-bit layers and their derivatives, in FP32, two values at a time
+// where the arithmetic counts: sm_103a has FP32 instructions of two lanes, and a chunk of 16 rows
+// through GELU's slope was bound by its 40 instructions an element.
 //
 // The factor that may be infinite is clamped where the other one is 0 (or the product below
 // FP32's range), so that a pre-activation of -inf gives 0 and not 0 * inf.  A NaN stays one.
@@ -13,6 +15,32 @@ using mx::after_previous_kernel;
 using mx::from_float;
 using mx::relu;
 using mx::to_float;
+
+// ---- 16-bit values -------------------------------------------------------------------------
+
+// The value of 16 bits (the low half of a word).
+template <class T> __device__ __forceinline__ float from_bits(uint32_t bits);
+template <> __device__ __forceinline__ float from_bits<__nv_bfloat16>(uint32_t bits) { return __uint_as_float(bits << 16); }
+template <> __device__ __forceinline__ float from_bits<__half>(uint32_t bits)
+{
+    const uint16_t low = (uint16_t)bits;
+    return __half2float(reinterpret_cast<const __half &>(low));
+}
+
+// Two values to 16 bits, a in the low half.
+template <class T> __device__ __forceinline__ uint32_t pack(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+template <> __device__ __forceinline__ uint32_t pack<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return reinterpret_cast<const uint32_t &>(v);
+}
+
+// ---- FP32, one and two at a time ------------------------------------------------------------
 
 // min and max that keep a NaN.
 __device__ __forceinline__ float at_most(float x, float most)
@@ -43,106 +71,6 @@ __device__ __forceinline__ float reciprocal_fast(float x)
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ float polynomial(const float (&c)[N], float x)
-{
-    float h = c[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) h = fmaf(h, x, c[i]);
-    return h;
-}
-
-__device__ constexpr float TAIL[] = {0.0359170846f, -0.141935625f, 0.155671924f, -0.0154948533f,
-                                     0.110444422f,  0.107662495f,  0.124079033f, 0.123655601f};
-
-// z Phi(z) = max(0, z) - a q for a = |z| and the normal tail q = Phi(-a) = exp(-a^2/2) g(a).  g falls from 1/2
-// as 1/a: a polynomial in t = 1 / (1 + 0.31 a), the variable of Hastings' approximations (1955), its
-// coefficients a minimax fit of the relative error for a up to 20 (1.7e-7; 5e-7 as evaluated in FP32).  From
-// 20 on q is 0.  TAIL are its coefficients.  (By normcdff the layer's epilogue took 1.3 times the whole product: 8192 x 11008 x
-// 4096, Z kept, 562 us against 431 without an activation.)
-__device__ __forceinline__ float gelu(float z)
-{
-    const float a = at_most(fabsf(z), 20.0f), t = reciprocal_fast(fmaf(0.31f, a, 1.0f));
-    const float q = exp2_fast(-0.721347520444482f * a * a) * (polynomial(TAIL, t) * t);  // log2(e) / 2
-    return fmaf(-a, q, relu(z));
-}
-
-__device__ constexpr float CDF[] = {0.000118079995f, -0.000285676331f, 0.000183916665f, -0.000356754608f, 0.00140742643f, -0.00265870243f,
-                                    0.00407412974f, -0.00665067835f, 0.0104686366f, -0.015062524f, 0.0203073174f, -0.0260361508f,
-                                    0.0320769101f, -0.0387937948f, 0.0477373339f, -0.0641723126f, 0.12855193f};
-
-// Phi(z) + z phi(z), with Phi(z) = 1/2 + z P(2 z^2 / 5.5^2 - 1) for |z| up to 5.5, beyond which Phi is 0 or 1 to
-// within FP32's rounding: P is a Chebyshev fit of this even function, off by less than 1e-8, its coefficients add up to
-// 0.4, and Phi as evaluated is 1.5e-8 off on average, 6e-8 at most, which is what 1 + erff comes to.  (A gradient
-// is rounded to 16 bits, to the other side the more often the less exact it is.  By the tail above it is
-// 2.3e-7 off, and the weights' gradient of 2048 rows was twice as far off.)  P's coefficients are CDF.
-__device__ __forceinline__ float gelu_slope(float z)
-{
-    const float c = at_least(at_most(z, 5.5f), -5.5f);
-    const float cdf = fmaf(c, polynomial(CDF, fmaf(c * c, 2.0f / (5.5f * 5.5f), -1.0f)), 0.5f);
-    return fmaf(c, 0.398942280401433f * exp2_fast(-0.721347520444482f * z * z), cdf);
-}
-
-__device__ __forceinline__ float sigmoid(float z) { return reciprocal_fast(1.0f + exp2_fast(-1.44269504088896f * z)); }
-
-__device__ __forceinline__ float silu(float z)
-{
-    z = at_least(z, -100.0f);
-    return z * sigmoid(z);
-}
-
-__device__ __forceinline__ float silu_slope(float z)
-{
-    z = at_most(at_least(z, -100.0f), 100.0f);
-    const float s = sigmoid(z);
-    return s * fmaf(z, 1.0f - s, 1.0f);
-}
-
-// v act'(z).  ReLU's is a gate: what is behind a closed one, NaN included, does not matter.
-__device__ __forceinline__ float through(float v, float z, int act)
-{
-    return act == FGEMM_ACT_RELU ? (z > 0.0f ? v : 0.0f)
-           : act == FGEMM_ACT_GELU ? v * gelu_slope(z)
-           : act == FGEMM_ACT_SILU ? v * silu_slope(z)
-                                   : v;
-}
-
-// The value of 16 bits (the low half of a word).
-template <class T> __device__ __forceinline__ float from_bits(uint32_t bits);
-template <> __device__ __forceinline__ float from_bits<__nv_bfloat16>(uint32_t bits) { return __uint_as_float(bits << 16); }
-template <> __device__ __forceinline__ float from_bits<__half>(uint32_t bits)
-{
-    const uint16_t low = (uint16_t)bits;
-    return __half2float(reinterpret_cast<const __half &>(low));
-}
-
-// Two values to 16 bits, a in the low half.
-template <class T> __device__ __forceinline__ uint32_t pack(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return reinterpret_cast<const uint32_t &>(v);
-}
-template <> __device__ __forceinline__ uint32_t pack<__half>(float a, float b)
-{
-    const __half2 v = __floats2half2_rn(a, b);
-    return reinterpret_cast<const uint32_t &>(v);
-}
-
-// act'(z) (GELU, SiLU) as its definition reads, each step rounded to nearest; a few units in the last place off.
-static __device__ __noinline__ float slope_by_definition(float z, int act)
-{
-    if (act == FGEMM_ACT_GELU) {
-        const float cdf = __fmul_rn(0.5f, erfcf(__fmul_rn(-z, 0.707106781186548f)));
-        const float w = at_least(at_most(z, 20.0f), -20.0f);  // (0 * inf)
-        return __fadd_rn(cdf, __fmul_rn(__fmul_rn(w, expf(__fmul_rn(__fmul_rn(-0.5f, z), z))), 0.398942280401433f));
-    }
-    const float c = at_least(at_most(z, 80.0f), -80.0f), s = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-c)));
-    return __fmul_rn(s, __fadd_rn(1.0f, __fmul_rn(c, __fadd_rn(1.0f, -s))));
-}
-
-// ---- two values at a time: sm_103a has FP32 instructions of two lanes --------------------------
-
 struct Two {
     uint64_t bits;
 };
@@ -153,6 +81,8 @@ __device__ __forceinline__ Two two(float a, float b)
     asm("mov.b64 %0, {%1, %2};" : "=l"(r.bits) : "f"(a), "f"(b));
     return r;
 }
+
+__device__ __forceinline__ Two both(float x) { return two(x, x); }
 
 __device__ __forceinline__ void split(Two x, float &a, float &b)
 {
@@ -173,23 +103,108 @@ __device__ __forceinline__ Two mul(Two a, Two b)
     return r;
 }
 
-// GELU's slope of both, by the tail as in gelu(): 1/2 - (1/2 - s) for z < 0, 1/2 + (1/2 - s) for z > 0, with
-// s = Phi(-|z|) - |z| phi(z), off by less than 6e-7.  (Fewer operations than gelu_slope, which these would bound.)
+template <int N>
+__device__ __forceinline__ Two polynomial(const float (&c)[N], Two x)
+{
+    Two h = both(c[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) h = fma(h, x, both(c[i]));
+    return h;
+}
+
+__device__ __forceinline__ Two exp2_fast(Two x)
+{
+    float a, b;
+    split(x, a, b);
+    return two(exp2_fast(a), exp2_fast(b));
+}
+
+__device__ __forceinline__ Two reciprocal_fast(Two x)
+{
+    float a, b;
+    split(x, a, b);
+    return two(reciprocal_fast(a), reciprocal_fast(b));
+}
+
+// exp(-x^2 / 2).
+__device__ __forceinline__ Two bell(Two x) { return exp2_fast(mul(mul(both(-0.721347520444482f), x), x)); }
+
+// ---- GELU -----------------------------------------------------------------------------------
+
+// z Phi(z) = max(0, z) - a q for a = |z| and the normal tail q = Phi(-a) = exp(-a^2/2) g(a).  g falls from 1/2
+// as 1/a: a polynomial (TAIL times t) in t = 1 / (1 + 0.31 a), the variable of Hastings' approximations
+// (1955), its coefficients a minimax fit of the relative error for a up to 20 (1.7e-7; 5e-7 as evaluated in
+// FP32).  From 20 on q is 0.  (By normcdff the layer's epilogue took 1.3 times the whole product: 8192 x 11008
+// x 4096, Z kept, 562 us against 431 without an activation.)
+__device__ constexpr float TAIL[] = {0.0359170846f, -0.141935625f, 0.155671924f, -0.0154948533f,
+                                     0.110444422f,  0.107662495f,  0.124079033f, 0.123655601f};
+
+__device__ __forceinline__ void gelu(float &z0, float &z1)
+{
+    const Two a = two(at_most(fabsf(z0), 20.0f), at_most(fabsf(z1), 20.0f));
+    const Two t = reciprocal_fast(fma(a, both(0.31f), both(1.0f))), q = mul(bell(a), mul(polynomial(TAIL, t), t));
+    split(fma(mul(a, both(-1.0f)), q, two(relu(z0), relu(z1))), z0, z1);
+}
+
+// The slope Phi(z) + z phi(z), with Phi(z) = 1/2 + z P(2 z^2 / 5.5^2 - 1) for |z| up to 5.5, beyond which Phi is 0 or
+// 1 to within FP32's rounding: P (CDF) is a Chebyshev fit of this even function, off by less than 1e-8, its
+// coefficients add up to 0.4, and Phi as evaluated is 1.5e-8 off on average, 6e-8 at most, which is what
+// 1 + erff comes to.  (A gradient is rounded to 16 bits, to the other side the more often the less exact it is.  By
+// the tail above it is 2.3e-7 off, and the weights' gradient of 2048 rows was twice as far off.)
+__device__ constexpr float CDF[] = {0.000118079995f, -0.000285676331f, 0.000183916665f, -0.000356754608f, 0.00140742643f, -0.00265870243f,
+                                    0.00407412974f,  -0.00665067835f,  0.0104686366f,   -0.015062524f,    0.0203073174f,  -0.0260361508f,
+                                    0.0320769101f,   -0.0387937948f,   0.0477373339f,   -0.0641723126f,   0.12855193f};
+
+__device__ __forceinline__ Two gelu_slope(float z0, float z1)
+{
+    const Two c = two(at_least(at_most(z0, 5.5f), -5.5f), at_least(at_most(z1, 5.5f), -5.5f));
+    const Two cdf = fma(c, polynomial(CDF, fma(mul(c, c), both(2.0f / (5.5f * 5.5f)), both(-1.0f))), both(0.5f));
+    return fma(c, mul(both(0.398942280401433f), bell(two(z0, z1))), cdf);
+}
+
+// The same by the tail: 1/2 - (1/2 - s) for z < 0, 1/2 + (1/2 - s) for z > 0, with s = Phi(-|z|) - |z| phi(z),
+// off by less than 6e-7; fewer operations.
 __device__ __forceinline__ Two gelu_slope_near(float z0, float z1)
 {
-    const float a0 = at_most(fabsf(z0), 20.0f), a1 = at_most(fabsf(z1), 20.0f);
-    float t0, t1, e0, e1;
-    const Two a = two(a0, a1);
-    split(fma(a, two(0.31f, 0.31f), two(1.0f, 1.0f)), t0, t1);
-    split(mul(mul(two(-0.721347520444482f, -0.721347520444482f), a), a), e0, e1);
-    const Two t = two(reciprocal_fast(t0), reciprocal_fast(t1)), e = two(exp2_fast(e0), exp2_fast(e1));
-    Two g = two(TAIL[0], TAIL[0]);
-#pragma unroll
-    for (int i = 1; i < (int)(sizeof(TAIL) / sizeof(float)); ++i) g = fma(g, t, two(TAIL[i], TAIL[i]));
-    // e (g t - a / sqrt(2 pi))
-    const Two s = mul(e, fma(g, t, mul(a, two(-0.398942280401433f, -0.398942280401433f))));
-    const Two half = two(0.5f, 0.5f), sign = two(copysignf(1.0f, z0), copysignf(1.0f, z1));
-    return fma(sign, fma(s, two(-1.0f, -1.0f), half), half);
+    const Two a = two(at_most(fabsf(z0), 20.0f), at_most(fabsf(z1), 20.0f));
+    const Two t = reciprocal_fast(fma(a, both(0.31f), both(1.0f)));
+    // exp(-a^2/2) (g t - a / sqrt(2 pi))
+    const Two s = mul(bell(a), fma(polynomial(TAIL, t), t, mul(a, both(-0.398942280401433f))));
+    return fma(two(copysignf(1.0f, z0), copysignf(1.0f, z1)), fma(s, both(-1.0f), both(0.5f)), both(0.5f));
+}
+
+// ---- SiLU -----------------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float z) { return reciprocal_fast(1.0f + exp2_fast(-1.44269504088896f * z)); }
+
+__device__ __forceinline__ float silu(float z)
+{
+    z = at_least(z, -100.0f);
+    return z * sigmoid(z);
+}
+
+__device__ __forceinline__ float silu_slope(float z)
+{
+    z = at_most(at_least(z, -100.0f), 100.0f);
+    const float s = sigmoid(z);
+    return s * fmaf(z, 1.0f - s, 1.0f);
+}
+
+// ---- gradients ------------------------------------------------------------------------------
+
+// ReLU's gradient is a gate: what is behind a closed one, NaN included, does not matter.
+__device__ __forceinline__ float gate(float v, float z) { return z > 0.0f ? v : 0.0f; }
+
+// act'(z) (GELU, SiLU) as its definition reads, each step rounded to nearest; a few units in the last place off.
+static __device__ __noinline__ float slope_by_definition(float z, int act)
+{
+    if (act == FGEMM_ACT_GELU) {
+        const float cdf = __fmul_rn(0.5f, erfcf(__fmul_rn(-z, 0.707106781186548f)));
+        const float w = at_least(at_most(z, 20.0f), -20.0f);  // (0 * inf)
+        return __fadd_rn(cdf, __fmul_rn(__fmul_rn(w, expf(__fmul_rn(__fmul_rn(-0.5f, z), z))), 0.398942280401433f));
+    }
+    const float c = at_least(at_most(z, 80.0f), -80.0f), s = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-c)));
+    return __fmul_rn(s, __fadd_rn(1.0f, __fmul_rn(c, __fadd_rn(1.0f, -s))));
 }
 
 // v act'(z) of two values, as they are rounded to T when act' is evaluated by its definition: by the fast
@@ -199,25 +214,24 @@ __device__ __forceinline__ Two gelu_slope_near(float z0, float z1)
 template <class T>
 __device__ __forceinline__ void through_exactly(float &v0, float &v1, float z0, float z1, int act)
 {
-    if (act != FGEMM_ACT_GELU && act != FGEMM_ACT_SILU) {
-        v0 = through(v0, z0, act);
-        v1 = through(v1, z1, act);
+    if (act == FGEMM_ACT_RELU) {
+        v0 = gate(v0, z0);
+        v1 = gate(v1, z1);
         return;
     }
     const Two size = two(fabsf(v0), fabsf(v1));
     Two fast, off;
     if (act == FGEMM_ACT_GELU) {
         fast = mul(two(v0, v1), gelu_slope_near(z0, z1));
-        off = mul(size, two(8.5e-7f, 8.5e-7f));
+        off = mul(size, both(8.5e-7f));
     } else {
         const Two far = two(at_most(fabsf(z0), 80.0f), at_most(fabsf(z1), 80.0f));
         fast = mul(two(v0, v1), two(silu_slope(z0), silu_slope(z1)));
-        off = mul(size, fma(far, two(5e-7f, 5e-7f), two(5e-7f, 5e-7f)));
+        off = mul(size, fma(far, both(5e-7f), both(5e-7f)));
     }
-    const Two one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
     float a0, a1, b0, b1, f0, f1;
-    split(fma(off, minus, fast), a0, a1);
-    split(fma(off, one, fast), b0, b1);
+    split(fma(off, both(-1.0f), fast), a0, a1);
+    split(fma(off, both(1.0f), fast), b0, b1);
     split(fast, f0, f1);
     const uint32_t differ = pack<T>(a0, a1) ^ pack<T>(b0, b1);
     if (differ != 0) {

@@ -14,10 +14,10 @@ double most(double a, double b) { return a > b ? a : b; }
 double least(double a, double b) { return a < b ? a : b; }
 
 // The estimate in us.  Fitted to 660 measurements of 60 products (1 to 8192 rows, 80 to 11008 columns, depths of 72
-// to 11008, operands not in L2): the plan of the least estimate took 1.6 % longer than the best one on average.
-//   64 of depth through a pair's barriers 0.165 us and more with the rows of its tile, through one CTA's
-//   0.168; a tile's epilogue; what all CTAs bring through L2 at 15.7 TB/s, and from memory at 6.4; the launch, and the
-//   joining of ranks.
+// to 11008, operands not in L2): the plan of the least estimate took 1.4 % longer than the best one on average.
+//   64 of depth through a pair's barriers 0.151 us and more with the rows of its tile, through one CTA's
+//   0.151; a tile's epilogue and its way through the roles; what all CTAs bring through L2 at 15.8 TB/s, and from memory
+//   at 6.6; the launch, and the joining of ranks.
 struct Work {
     double row_tiles, rows;  // tiles of rows (all groups'), rows of one
     double N, blocks;        // columns, 64-deep blocks of a product
@@ -29,12 +29,12 @@ double estimate(const Work &w, bool pair, int ranks, int sms)
 {
     const double tiles = w.row_tiles * w.products * up(w.N, pair ? 256 : 128);
     const double stage = (pair ? 32768 : 16384) + 128 * w.rows, share = up(w.blocks, ranks);
-    const double memory = most(tiles * ranks * share * stage / 15.7e6, w.bytes / 6.4e6);
+    const double memory = most(tiles * ranks * share * stage / 15.8e6, w.bytes / 6.6e6);
     const double waves = pair ? up(tiles, sms / 2) : up(tiles * ranks, sms);
-    const double depth = share * (pair ? most(0.165, 0.088 + 0.00083 * w.rows) : 0.168);
-    const double epilogue = (pair ? 0.0104 : 0.01285) * w.rows;
-    const double t = (pair ? 2.47 : 2.12) + most(waves * most(depth, epilogue) + least(depth, epilogue), memory);
-    return ranks > 1 ? t + 1.5 + 0.0154 * w.rows : t;
+    const double depth = share * (pair ? most(0.151, 0.117 + 0.00065 * w.rows) : 0.151);
+    const double epilogue = (pair ? 0.22 + 0.0104 * w.rows : 0.56 + 0.0097 * w.rows);
+    const double t = (pair ? 2.52 : 1.81) + most(waves * most(depth, epilogue) + least(depth, epilogue), memory);
+    return ranks > 1 ? t + 1.22 + 0.0187 * w.rows : t;
 }
 
 }  // namespace

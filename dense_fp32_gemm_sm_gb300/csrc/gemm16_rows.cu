@@ -35,7 +35,6 @@ __global__ void __launch_bounds__(256) realign_kernel(Realign a, Realign b)
 
 constexpr int ACT_COLUMNS = 256;  // of a block: eight a lane
 constexpr int ACT_WARPS = 8;      // rows of a block at a time
-constexpr int SLICE_ROWS = 64;
 
 // D = G act'(Z) for a slice of a group's rows by 256 columns, and its column sums.  VEC: a lane's eight
 // columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
@@ -163,16 +162,19 @@ fgemm_status launch_realign(const Realign &a, const Realign &b, cudaStream_t str
     return status(mx::launch(realign_kernel, grid, 256, 0, stream, 1, a, b));
 }
 
-long long act_slices(long long groups, long long M)
+// 64 rows a slice, fewer (16 at least, two a warp) where there are not blocks for all SMs: of 77 x 1237 a
+// warp's eight rows, some of whose values take the definition, were 12 us.
+long long act_slices(long long groups, long long M, long long N)
 {
-    const long long rows = (M + groups - 1) / groups;
-    return rows > SLICE_ROWS ? (rows + SLICE_ROWS - 1) / SLICE_ROWS : 1;
+    const long long rows = (M + groups - 1) / groups, strips = (N + ACT_COLUMNS - 1) / ACT_COLUMNS;
+    const long long fewest = (rows + 63) / 64, most = (rows + 15) / 16, wanted = 4 * 152 / (strips * groups);
+    return wanted < fewest ? fewest : wanted < most ? wanted : most;
 }
 
 fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream)
 {
     const int strips = (p.N - 1) / ACT_COLUMNS + 1;
-    const long long slices = act_slices(p.groups, p.M), blocks = strips * slices * p.groups;
+    const long long slices = act_slices(p.groups, p.M, p.N), blocks = strips * slices * p.groups;
     if (blocks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
     const bool vec = p.N % 8 == 0 && vectors(p.g, p.ldg) && vectors(p.z, p.ldz) && vectors(p.d, p.ldd);
     const auto kernel = p.type == FGEMM_BF16 ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)

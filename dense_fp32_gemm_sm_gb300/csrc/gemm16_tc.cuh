@@ -400,7 +400,7 @@ __device__ __forceinline__ float finish_rows(const Epilogue<FULL> &q, float (&v)
                                              int rows, bool in)
 {
 #pragma unroll
-    for (int c = 0; c < N; ++c) v[c] = fmaf(q.alpha, v[c], bias);
+    for (int c = 0; c < N; c += 2) split(fma(two(v[c], v[c + 1]), both(q.alpha), both(bias)), v[c], v[c + 1]);
     const int act = q.act();
     if (q.has(SLOPE)) {
         if (q.has(WITH_Z)) {
@@ -408,13 +408,13 @@ __device__ __forceinline__ float finish_rows(const Epilogue<FULL> &q, float (&v)
             ahead.template take<T>(x, q.has(Z_PAIRS));
             if (act == FGEMM_ACT_RELU) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_RELU);
+                for (int c = 0; c < N; ++c) v[c] = gate(v[c], x[c]);
             } else if (act == FGEMM_ACT_GELU) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_GELU);
+                for (int c = 0; c < N; c += 2) split(mul(two(v[c], v[c + 1]), gelu_slope(x[c], x[c + 1])), v[c], v[c + 1]);
             } else {
 #pragma unroll
-                for (int c = 0; c < N; ++c) v[c] = through(v[c], x[c], FGEMM_ACT_SILU);
+                for (int c = 0; c < N; ++c) v[c] *= silu_slope(x[c]);
             }
         }
     } else {
@@ -424,7 +424,7 @@ __device__ __forceinline__ float finish_rows(const Epilogue<FULL> &q, float (&v)
             for (int c = 0; c < N; ++c) v[c] = relu(v[c]);
         } else if (act == FGEMM_ACT_GELU) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] = gelu(v[c]);
+            for (int c = 0; c < N; c += 2) gelu(v[c], v[c + 1]);
         } else if (act == FGEMM_ACT_SILU) {
 #pragma unroll
             for (int c = 0; c < N; ++c) v[c] = silu(v[c]);
@@ -497,10 +497,10 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
 // op(B) and half of the tile's rows of op(A).  CTA 0 issues for both; its `full` barriers count what
 // arrives in either.  Else the `ranks` CTAs of a cluster divide the depth of one tile, or (ranks 1) a CTA
 // walks whole tiles.
-// LONG: the accumulators take LONG_STAGES stages (512 of depth) at a time, and the epilogue's warps
-// add these sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
-// 2048, sums come out 2.1e-6 off (2-norm, random operands), of 512 at a time 0.6e-6, which counts where
-// they are kept in FP32.
+// LONG: the accumulators take a depth of LONG_DEPTH (768) at a time, and the epilogue's warps add these
+// sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
+// 2048, sums come out 2.1e-6 off (2-norm, random operands), of 768 at a time 0.6e-6, which counts where
+// they are kept in FP32.  (4096 x 11008 of a depth of 2048: 122 us in turns, 119 in one go.)
 template <bool PAIR, class T, class O, bool LONG, bool FULL>
 __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
 {

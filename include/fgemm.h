@@ -650,7 +650,7 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
 /*
  * How a product runs on a GPU with `num_sms` SMs: 16 * rows + ranks (tiles of 128 columns of Y by at most
  * `rows` rows, each tile's depth divided among `ranks` CTAs), + 8192 where pairs of CTAs take 256 columns,
- * + 16384 where the sums of a long depth are added up in turns of 512 (col_sums, or FP32 out).
+ * + 16384 where the sums of a long depth are added up in turns of 768 (col_sums, or FP32 out).
  * grouped 0: fgemm_gemm16 and its gradient (sums: with col_sums), 1: by groups, 2:
  * fgemm_gemm16_weight_grad (sizes as that call has them).  -1 for arguments out of range.  Host-only: no CUDA call.
  */
