@@ -81,12 +81,12 @@ struct ActGrad {
     long long ldg, ldz, ldd;
     float *partial;  // or null: no sums
 };
-// Slices of a group's rows, each with a partial sum.
-long long act_slices(long long groups, long long M, long long N);
-fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream);
+// The gradient, and (partial not null) its column sums, N floats a group.
+fgemm_status launch_act_grad(const ActGrad &p, float *sums, cudaStream_t stream);
 
-// sums[e][j] = the partial rows start[e] .. start[e+1] of column j, in order (start == null: `each` a group).
-fgemm_status launch_sums(const float *partial, const int *start, long long each, int groups, int N, float *sums,
+// sums[e][j] = the partial rows of group e, of `most` there may be, of column j, in order: rows
+// start[e] .. start[e+1], or (start null) those of the slices that `of` leaves.
+fgemm_status launch_sums(const float *partial, long long most, const int *start, const ActGrad *of, int groups, int N, float *sums,
                          cudaStream_t stream);
 
 }  // namespace h16

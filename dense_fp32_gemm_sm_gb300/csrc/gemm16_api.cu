@@ -101,7 +101,7 @@ fgemm_status run(Product &q, float *col_sums, void *workspace, size_t workspace_
     }
     const fgemm_status st = launch_product(q, stream);
     if (st != FGEMM_OK || !col_sums) return st;
-    return launch_sums(q.partial, q.partial_start, 0, q.groups, q.N, col_sums, stream);
+    return launch_sums(q.partial, q.partials, q.partial_start, nullptr, q.groups, q.N, col_sums, stream);
 }
 
 fgemm_status zero(float *x, size_t n, cudaStream_t stream)
@@ -327,9 +327,7 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
     p.ldz = ldz;
     p.ldd = ldd;
     p.partial = col_sums ? static_cast<float *>(workspace) : nullptr;
-    const fgemm_status st = launch_act_grad(p, stream);
-    if (st != FGEMM_OK || !col_sums) return st;
-    return launch_sums(p.partial, nullptr, act_slices(groups, M, N), groups, N, col_sums, stream);
+    return launch_act_grad(p, col_sums, stream);
 }
 
 int fgemm_gemm16_plan(fgemm_dtype out_type, int grouped, int groups, int M, int N, int K, int sums, int num_sms)

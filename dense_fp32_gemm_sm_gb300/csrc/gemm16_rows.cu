@@ -36,22 +36,50 @@ __global__ void __launch_bounds__(256) realign_kernel(Realign a, Realign b)
 constexpr int ACT_COLUMNS = 256;  // of a block: eight a lane
 constexpr int ACT_WARPS = 8;      // rows of a block at a time
 
-// D = G act'(Z) for a slice of a group's rows by 256 columns, and its column sums.  VEC: a lane's eight
-// columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
+// Rows of group e, the first at `first`.
+__device__ __forceinline__ int rows_of(const int *offsets, int e, int M, int &first)
+{
+    first = max(0, min(offsets[e], M));
+    return max(max(0, min(offsets[e + 1], M)) - first, 0);
+}
+
+// D = G act'(Z) for a slice of a group's rows (`height` at most) by 256 columns, and its column sums.  The
+// slices of all groups are counted through, so that a group of many rows has many blocks.
+// VEC: a lane's eight columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, int strips, int slices)
+__global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, int strips, int height)
 {
     __shared__ float sums[ACT_WARPS][ACT_COLUMNS];
     after_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int strip = blockIdx.x % strips, part = blockIdx.x / strips, e = part / slices, slice = part % slices;
-    long long first = 0, rows = p.M;
+    const int strip = blockIdx.x % strips, part = blockIdx.x / strips;
+    long long from = (long long)part * height, to = min(from + height, (long long)p.M);
     if (p.offsets) {
-        const int a = max(0, min(p.offsets[e], p.M)), b = max(0, min(p.offsets[e + 1], p.M));
-        first = a;
-        rows = max(b - a, 0);
+        // 32 groups at a time: the one whose slices, added up, pass this block's.
+        int before = 0, e0 = 0;
+        unsigned found = 0;
+        for (; e0 < p.groups; e0 += 32) {
+            const int e = e0 + lane;
+            int first = 0;
+            const int rows = e < p.groups ? rows_of(p.offsets, e, p.M, first) : 0, own = (rows + height - 1) / height;
+            int sum = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int other = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d) sum += other;
+            }
+            found = __ballot_sync(0xFFFFFFFFu, before + sum > part);
+            if (found) {
+                const int at = __ffs(found) - 1;
+                const long long start = first + (long long)(part - before - (sum - own)) * height;
+                from = __shfl_sync(0xFFFFFFFFu, start, at);
+                to = __shfl_sync(0xFFFFFFFFu, min(start + height, (long long)first + rows), at);
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (!found) return;  // (there is room for a short slice of every group)
     }
-    const long long from = first + rows * slice / slices, to = first + rows * (slice + 1) / slices;
     const int c0 = strip * ACT_COLUMNS;
     auto column = [&](int j) { return c0 + (VEC ? 8 * lane + j : lane + 32 * j); };
     float sum[8] = {};
@@ -122,13 +150,27 @@ __global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, 
 // ---- partial column sums -----------------------------------------------------------------
 
 // 32 columns of a group by 8 warps, each adding up every eighth row; then the warps' sums, in order.
-__global__ void __launch_bounds__(256) sums_kernel(const float *partial, const int *start, long long each, int strips, int N, float *sums)
+// start: the groups' first partial rows; null: those of act_grad_kernel's slices.
+__global__ void __launch_bounds__(256) sums_kernel(const float *partial, long long most, const int *start, const int *offsets, int M,
+                                                   int height, int strips, int N, float *sums)
 {
     __shared__ float part[8][32];
     after_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int strip = blockIdx.x % strips, e = blockIdx.x / strips, n = strip * 32 + lane;
-    const long long from = start ? start[e] : each * e, to = start ? start[e + 1] : each * (e + 1);
+    long long from = 0, to = most;
+    if (start) {
+        from = start[e];
+        to = start[e + 1];
+    } else if (offsets) {
+        int first, before = 0;
+        for (int i = lane; i < e; i += 32) before += (rows_of(offsets, i, M, first) + height - 1) / height;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
+        from = before;
+        to = from + (rows_of(offsets, e, M, first) + height - 1) / height;
+    }
+    to = min(to, most);
     float sum = 0.0f;
     if (n < N) {
 #pragma unroll 4
@@ -162,31 +204,41 @@ fgemm_status launch_realign(const Realign &a, const Realign &b, cudaStream_t str
     return status(mx::launch(realign_kernel, grid, 256, 0, stream, 1, a, b));
 }
 
-// 64 rows a slice, fewer (16 at least, two a warp) where there are not blocks for all SMs: of 77 x 1237 a
+// Rows of a slice: 64, fewer (16 at least, two a warp) where there are not blocks for all SMs: of 77 x 1237 a
 // warp's eight rows, some of whose values take the definition, were 12 us.
-long long act_slices(long long groups, long long M, long long N)
+static int slice_rows(long long M, long long N)
 {
-    const long long rows = (M + groups - 1) / groups, strips = (N + ACT_COLUMNS - 1) / ACT_COLUMNS;
-    const long long fewest = (rows + 63) / 64, most = (rows + 15) / 16, wanted = 4 * 152 / (strips * groups);
-    return wanted < fewest ? fewest : wanted < most ? wanted : most;
+    const long long strips = (N + ACT_COLUMNS - 1) / ACT_COLUMNS, fair = (M * strips / (4 * 152) + 7) / 8 * 8;
+    return (int)(fair < 16 ? 16 : fair < 64 ? fair : 64);
 }
 
-fgemm_status launch_act_grad(const ActGrad &p, cudaStream_t stream)
+// Slices there may be: each group's last one may be short.  (partial_rows has room for them.)
+static long long most_slices(const ActGrad &p)
+{
+    const int height = slice_rows(p.M, p.N);
+    return p.offsets ? p.M / height + (p.groups < p.M ? p.groups : p.M) : (p.M + height - 1ll) / height;
+}
+
+fgemm_status launch_act_grad(const ActGrad &p, float *sums, cudaStream_t stream)
 {
     const int strips = (p.N - 1) / ACT_COLUMNS + 1;
-    const long long slices = act_slices(p.groups, p.M, p.N), blocks = strips * slices * p.groups;
+    const long long blocks = strips * most_slices(p);
     if (blocks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
     const bool vec = p.N % 8 == 0 && vectors(p.g, p.ldg) && vectors(p.z, p.ldz) && vectors(p.d, p.ldd);
     const auto kernel = p.type == FGEMM_BF16 ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
                                              : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);
-    return status(mx::launch(kernel, dim3((unsigned)blocks), 32 * ACT_WARPS, 0, stream, 1, p, strips, (int)slices));
+    const fgemm_status st = status(mx::launch(kernel, dim3((unsigned)blocks), 32 * ACT_WARPS, 0, stream, 1, p, strips, slice_rows(p.M, p.N)));
+    if (st != FGEMM_OK || !p.partial) return st;
+    return launch_sums(p.partial, most_slices(p), nullptr, &p, p.groups, p.N, sums, stream);
 }
 
-fgemm_status launch_sums(const float *partial, const int *start, long long each, int groups, int N, float *sums, cudaStream_t stream)
+fgemm_status launch_sums(const float *partial, long long most, const int *start, const ActGrad *of, int groups, int N, float *sums,
+                         cudaStream_t stream)
 {
     const int strips = (N - 1) / 32 + 1;
     if ((long long)strips * groups > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
-    return status(mx::launch(sums_kernel, dim3((unsigned)(strips * groups)), 256, 0, stream, 1, partial, start, each, strips, N, sums));
+    return status(mx::launch(sums_kernel, dim3((unsigned)(strips * groups)), 256, 0, stream, 1, partial, most, start,
+                             of ? of->offsets : nullptr, of ? of->M : 0, of ? slice_rows(of->M, of->N) : 1, strips, N, sums));
 }
 
 }  // namespace h16

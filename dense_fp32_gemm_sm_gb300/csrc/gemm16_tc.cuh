@@ -214,7 +214,7 @@ struct Walk {
             t -= first[group];
             row0 = begin[group];
             rows = begin[group + 1] - row0;
-            height_t = min(((rows + tiles_t - 1) / tiles_t + 31) & ~31, p.nt);
+            height_t = min((int)(((unsigned)rows + tiles_t - 1) / tiles_t + 31) & ~31, p.nt);
             row_tile0 = first[group] / p.tiles_f;
         } else if (p.q.ragged == RAGGED_DEPTH) {
             const int per = p.tiles_t * p.tiles_f;
@@ -255,7 +255,7 @@ __device__ __forceinline__ void make_table(const Args &p, int *table, int lane)
             if (lane >= d) end = max(end, other);
         }
         const int before = __shfl_up_sync(0xFFFFFFFFu, end, 1), rows = end - (lane == 0 ? most : before);
-        int sum = p.q.ragged == RAGGED_ROWS ? (rows + p.nt - 1) / p.nt * p.tiles_f : 0;
+        int sum = p.q.ragged == RAGGED_ROWS ? (int)(((unsigned)rows + p.nt - 1) / p.nt) * p.tiles_f : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int other = __shfl_up_sync(0xFFFFFFFFu, sum, d);
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
         for (int tile = 1; more; more = walk.get(tile++, o)) {
             int from;
             const int stages = stages_of(o, from), n = o.f0 + TILE_F * half + 32 * q + lane;
-            const int turns = LONG ? (stages * stage_depth + LONG_DEPTH - 1) / LONG_DEPTH : stages > 0;
+            const int turns = LONG ? (int)(((unsigned)(stages * stage_depth) + LONG_DEPTH - 1) / LONG_DEPTH) : stages > 0;
             const bool in = n < N;
             // (on its way during the wait)
             const float bias = biases && in ? biases[(long long)o.e * N + n] : 0.0f;
@@ -905,7 +905,9 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
                 }
             }
             if (LONG) load_ahead(ahead, CHUNK * set);
-            if (!LONG || turns == 1) ok = turns == 0 || warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim);
+            // (A wait for a whole tile's depth, of which a stage takes 0.3 us: 2^31 rows take 5 s.)
+            if (!LONG || turns == 1)
+                ok = turns == 0 || warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim + 1024ull * stages);
             if (!ok) break;
             tc::tc_fence_after();
 #pragma unroll 1

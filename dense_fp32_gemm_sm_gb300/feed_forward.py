@@ -50,7 +50,7 @@ class FeedForward:
         self.type, self.dtype = _TYPES[w1.dtype], w1.dtype
 
     def _rows(self, x, cols):
-        if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != cols or (x.shape[0] and x.stride(1) != 1):
+        if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != cols or (x.shape[0] and cols > 1 and x.stride(1) != 1):
             raise ValueError("a matrix of %s with %d contiguous columns" % (self.dtype, cols))
         if x.shape[0] > 1 and x.stride(0) < cols:
             raise ValueError("rows that overlap (row stride %d for %d columns): pass .contiguous()" % (x.stride(0), cols))
@@ -147,9 +147,12 @@ class FeedForward:
     def backward(self, g, saved: Saved):
         """(dX, dW1, dW2, db1, db2) for the gradient g of Y; None for a bias that is not there."""
         ldg = self._rows(g, self.K)
-        if g.shape[0] != saved.x.shape[0]:
-            raise ValueError("%d gradients for %d tokens" % (g.shape[0], saved.x.shape[0]))
-        M, offsets, E = g.shape[0], saved.offsets, self.experts or 1
+        M, offsets, E = g.shape[0], self._offsets(saved.offsets), self.experts or 1
+        if M != saved.x.shape[0]:
+            raise ValueError("%d gradients for %d tokens" % (M, saved.x.shape[0]))
+        self._rows(saved.x, self.K)
+        if tuple(saved.z.shape) != (M, self.N) or saved.z.dtype != self.dtype:
+            raise ValueError("saved by a block of %d columns of %s" % (saved.z.shape[1], saved.z.dtype))
         lead = () if self.experts is None else (self.experts,)
         dev = self.w1.device
         db1 = torch.empty(*lead, self.N, device=dev) if self.b1 is not None else None

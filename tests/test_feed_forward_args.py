@@ -41,3 +41,14 @@ def test_tokens_and_offsets():
             experts.forward(half(5, 4), bad)
     with pytest.raises(ValueError):
         one.backward(half(5, 4), Saved(half(6, 4), half(6, 6), half(6, 6), None))
+    for saved in (Saved(half(5, 4), half(5, 8), half(5, 8), None), Saved(half(5, 3), half(5, 6), half(5, 6), None),
+                  Saved(half(5, 4), half(4, 6), half(4, 6), None), Saved(half(5, 4), half(5, 6), half(5, 6), off),
+                  Saved(half(5, 4), half(5, 6).half(), half(5, 6), None)):
+        with pytest.raises(ValueError):
+            one.backward(half(5, 4), saved)
+    with pytest.raises(ValueError):
+        experts.backward(half(5, 4), Saved(half(5, 4), half(5, 6), half(5, 6), None))
+
+
+def test_rows_of_one_column():
+    assert FeedForward(half(1, 6), half(6, 1))._rows(half(1, 5).t(), 1) == 1

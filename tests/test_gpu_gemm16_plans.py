@@ -265,3 +265,53 @@ def test_many_rows_and_columns():
         assert torch.equal(y[r].double(), (a[r].double() @ b.double().t()).clamp(min=0))
     for c in (0, 17777, 33999):
         assert torch.equal(y[:, c].double(), (a.double() @ b[c].double()).clamp(min=0))
+
+
+def test_one_weight_for_all_groups():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    M, N, K, E = 200, 136, 72, 3
+    x, w = ints(g, M, K), ints(g, K, N)
+    off = torch.tensor([0, 70, 71, M], dtype=torch.int32, device="cuda")
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    fg.gemm16_grouped(fg.BF16, fg.BF16, 0, E, M, N, K, off, 1.0, x, K, w, N, 0, None, 0, None, 0, 0.0, None, 0, y, N)
+    assert torch.equal(y, (x.double() @ w.double()).bfloat16())
+
+
+@pytest.mark.parametrize("E,full", [(64, 17), (1024, 1023), (33, 32)])
+def test_all_rows_in_one_of_many_groups(E, full):
+    """Sums of integers, exact: the slices of a gradient are counted through all groups."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    M, N = 5000, 264
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[full + 1:] = M
+    x, z = ints(g, M, N), ints(g, M, N)
+    d, s = torch.full_like(x, 9), torch.full((E, N), float("nan"), device="cuda")
+    ws = torch.full((fg.gemm16_sums_workspace_size(E, M, N),), 255, dtype=torch.uint8, device="cuda")
+    fg.act16_grad(fg.BF16, E, M, N, off, fg.ACT_RELU, x, N, z, N, d, N, s, ws, ws.numel())
+    want = torch.where(z > 0, x, 0)
+    assert torch.equal(d, want) and torch.equal(s[full].double(), want.double().sum(0))
+    assert not s[:full].any() and not s[full + 1:].any()
+
+
+def test_depths_near_the_limit():
+    """2^31 - 256: one tile's sums take seconds, in one go and in turns."""
+    K = (1 << 31) - 256
+    a, b = (torch.zeros(K, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i, k in enumerate((0, 767, 768, 1 << 30, K - 129, K - 1)):
+        a[k], b[k] = i + 1, 1
+    y, s = torch.zeros(1, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, device="cuda")
+    ws = torch.empty(fg.gemm16_sums_workspace_size(1, 1, 1), dtype=torch.uint8, device="cuda")
+    fg.gemm16_grad(fg.BF16, fg.BF16, 0, 1, 1, 1, K, 1.0, a, K, b, K, fg.ACT_NONE, None, 0, y, 1, s, ws, ws.numel())
+    assert y.item() == 21 and s.item() == 21
+    del a, b
+    x, g = (torch.zeros(K, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i, k in enumerate((0, 1, 127, 128, 1 << 30, K - 129, K - 1)):
+        x[k, i], g[k, 7 - i] = i + 1, 1
+    off = torch.tensor([0, K], dtype=torch.int32, device="cuda")
+    c = torch.full((8, 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    fg.gemm16_weight_grad(fg.BF16, fg.BF16, 1, K, 8, 8, off, 1.0, x, 8, g, 8, 0.0, c, 8, 64)
+    want = torch.zeros(8, 8)
+    for i in range(7):
+        want[i, 7 - i] = i + 1
+    assert torch.equal(c.cpu().float(), want)
+    assert fg.device_status() == fg.OK
