@@ -52,10 +52,10 @@ static bool prepare(unsigned **err, int *sms)
 
 static bool paired(const void *p, long long ld, fgemm_dtype t) { return t != FGEMM_F32 && reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
-template <bool PAIR, class T, class O, bool LONG, bool FULL>
+template <bool PAIR, class T, class O, bool LONG, Kind KIND>
 static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    constexpr auto kernel = &gemm16_kernel<PAIR, T, O, LONG, FULL>;
+    constexpr auto kernel = &gemm16_kernel<PAIR, T, O, LONG, KIND>;
     unsigned *err = nullptr;
     int sms = 0;
     if (!prepare<decltype(kernel), kernel>(&err, &sms)) {
@@ -89,14 +89,20 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
     const int join_bytes = !PAIR && plan.ranks > 1 ? (p.nt + plan.ranks) * TILE_F * 4 : 0;  // (shares are rounded up)
-    const int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 32;
+    int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 48;
+    // Rings of Z where three stages of two blocks stay.
+    const int z_bytes = 4 * SETS * Z_SLOTS * Z_SLOT_BYTES;
+    const bool z_ring = PAIR && KIND == GRADIENT && q.act != FGEMM_ACT_NONE && q.N % 8 == 0 && q.ldz % 8 == 0 &&
+                        reinterpret_cast<uintptr_t>(q.z) % 16 == 0 && room - z_bytes >= 6 * p.block_bytes;
+    if (z_ring) room -= z_bytes;
     p.blocks = room >= 6 * p.block_bytes ? 2 : 1;
     p.stage_bytes = p.blocks * p.block_bytes;
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     if (p.stages < 2) return FGEMM_ERR_NOT_SUPPORTED;
     p.table = p.stages * p.stage_bytes + (bar_bytes(p.stages) + 15) / 16 * 16;
     p.join = p.table + (table_bytes + 15) / 16 * 16;
-    const int smem = 1024 + p.join + join_bytes;
+    p.z_ring = z_ring ? (p.join + join_bytes + 15) / 16 * 16 : 0;
+    const int smem = 1024 + (z_ring ? p.z_ring + z_bytes : p.join + join_bytes);
     p.acc_step = PAIR ? 256 : p.nt;
     p.tmem_cols = 32;
     while (p.tmem_cols < 2 * p.acc_step) p.tmem_cols *= 2;
@@ -120,19 +126,20 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
                                                                                                         : FGEMM_ERR_LAUNCH;
 }
 
-template <bool PAIR, class T, class O>
+template <bool PAIR, class T, class O, bool LONG>
 static fgemm_status launch_kind(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    const bool full = q.slope || q.z || q.beta != 0.0f || q.partial;
-    if (plan.in_turns)
-        return full ? launch_instance<PAIR, T, O, true, true>(q, plan, stream) : launch_instance<PAIR, T, O, true, false>(q, plan, stream);
-    return full ? launch_instance<PAIR, T, O, false, true>(q, plan, stream) : launch_instance<PAIR, T, O, false, false>(q, plan, stream);
+    if (q.slope && (q.act != FGEMM_ACT_NONE || q.partial)) return launch_instance<PAIR, T, O, LONG, GRADIENT>(q, plan, stream);
+    if (!q.slope && (q.z || q.beta != 0.0f)) return launch_instance<PAIR, T, O, LONG, FORWARD>(q, plan, stream);
+    return launch_instance<PAIR, T, O, LONG, PLAIN>(q, plan, stream);
 }
 
 template <class T, class O>
 fgemm_status launch_product_type(const Product &q, const Plan &plan, cudaStream_t stream)
 {
-    return plan.pair ? launch_kind<true, T, O>(q, plan, stream) : launch_kind<false, T, O>(q, plan, stream);
+    if (plan.in_turns)
+        return plan.pair ? launch_kind<true, T, O, true>(q, plan, stream) : launch_kind<false, T, O, true>(q, plan, stream);
+    return plan.pair ? launch_kind<true, T, O, false>(q, plan, stream) : launch_kind<false, T, O, false>(q, plan, stream);
 }
 
 }  // namespace h16

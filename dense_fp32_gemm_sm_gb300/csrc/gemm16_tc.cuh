@@ -37,6 +37,8 @@ constexpr int DEPTH = 64;        // 16-bit elements of a block: 128 bytes
 constexpr int SETS = 2;  // of four epilogue warps: one for 32 lanes of tensor memory each
 __host__ __device__ constexpr int threads_of(bool pair) { return 64 + 128 * SETS + (pair ? 32 : 0); }  // producer, MMA, epilogue; mender
 constexpr int CHUNK = 16;      // accumulator columns that a warp finishes at a time
+constexpr int Z_SLOTS = 4;     // of a warp's ring of Z: chunks of 16 rows by 32 columns
+constexpr int Z_SLOT_BYTES = CHUNK * 64;
 
 constexpr int MAX_STAGES = 12;
 constexpr int W_BYTES = TILE_F * 128;
@@ -55,6 +57,7 @@ struct Args {
     int blocks, block_bytes;  // 64-deep blocks of a stage (1 or 2), each of op(B), then of op(A)
     int table, join;         // offsets in shared memory: the groups' table, the sums that ranks send each other
     int y_pairs, z_pairs, r_pairs;  // pairs of columns are aligned
+    int z_ring;  // offset in shared memory of the rings of Z whose slope is taken; 0: Z comes to registers
     unsigned long long wait_limit_ns;
     int withhold;
 };
@@ -355,9 +358,11 @@ __device__ __forceinline__ void store_rows(T *out, long long ld, const float (&v
 // What the epilogue needs of the arguments, in registers: from the constant bank each of them would
 // cost a chunk of rows 40 cycles and more (a chunk of 16 rows took 1400 cycles).
 enum { WITH_Z = 16, WITH_R = 32, WITH_SUMS = 64, SLOPE = 128, Y_PAIRS = 256, Z_PAIRS = 512, R_PAIRS = 1024 };
-// FULL: with Z, R, a slope or column sums.  Without, in instances of their own, the code of a chunk is short enough
-// that jumps over what a call does not want cost nothing (1353 x 6488 x 72: 12.5 us in place of 10.3).
-template <bool FULL>
+// The kernel comes in three kinds, PLAIN (bias and activation), FORWARD (with Z or R) and GRADIENT (a slope or
+// column sums): the code of a chunk is short enough then that jumps over what a call does not want cost
+// little (1353 x 6488 x 72: 12.5 us in place of 10.3 where all were one).
+enum Kind { PLAIN, FORWARD, GRADIENT };
+template <Kind KIND>
 struct Epilogue {
     float alpha, beta;
     int mode;  // act, and the above
@@ -373,12 +378,16 @@ struct Epilogue {
         ldr = __shfl_sync(0xFFFFFFFFu, q.ldr, 0);
         const int z = q.slope ? q.act != FGEMM_ACT_NONE : q.z != nullptr;
         mode = uniform(q.act | (z ? WITH_Z : 0) | (!q.slope && q.beta != 0.0f ? WITH_R : 0) | (q.partial ? WITH_SUMS : 0) |
-                       (q.slope ? SLOPE : 0) | (p.y_pairs ? Y_PAIRS : 0) | (p.z_pairs ? Z_PAIRS : 0) | (p.r_pairs ? R_PAIRS : 0));
+                       (p.y_pairs ? Y_PAIRS : 0) | (p.z_pairs ? Z_PAIRS : 0) | (p.r_pairs ? R_PAIRS : 0));
     }
     __device__ __forceinline__ int act() const { return mode & 15; }
     __device__ __forceinline__ bool has(int what) const
     {
-        return (FULL || (what & (WITH_Z | WITH_R | WITH_SUMS | SLOPE)) == 0) && (mode & what) != 0;
+        if (what == SLOPE) return KIND == GRADIENT;
+        if (KIND == PLAIN && what == WITH_Z) return false;
+        if (KIND != FORWARD && what == WITH_R) return false;
+        if (KIND != GRADIENT && what == WITH_SUMS) return false;
+        return (mode & what) != 0;
     }
 
     // What finish_rows reads, Z for a slope or R.
@@ -395,8 +404,8 @@ struct Epilogue {
 
 // N sums of this lane's column to `rows` rows of it, the first at y (and z); ahead: what of Z or R goes in.
 // Returns the sum of what Y holds of them, before its rounding.
-template <class T, class O, bool FULL, int N>
-__device__ __forceinline__ float finish_rows(const Epilogue<FULL> &q, float (&v)[N], const Ahead<N> &ahead, O *y, T *z, float bias,
+template <class T, class O, Kind KIND, int N>
+__device__ __forceinline__ float finish_rows(const Epilogue<KIND> &q, float (&v)[N], const Ahead<N> &ahead, O *y, T *z, float bias,
                                              int rows, bool in)
 {
 #pragma unroll
@@ -467,6 +476,12 @@ struct Slot {
     }
 };
 
+// 16 bytes to shared memory, on their way when this returns.
+__device__ __forceinline__ void copy_16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 // 16 sums of each lane from tensor memory.
 __device__ __forceinline__ void load_sums(uint32_t taddr, bool products, float (&v)[CHUNK])
 {
@@ -501,7 +516,7 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
 // sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
 // 2048, sums come out 2.1e-6 off (2-norm, random operands), of 768 at a time 0.6e-6, which counts where
 // they are kept in FP32.  (4096 x 11008 of a depth of 2048: 122 us in turns, 119 in one go.)
-template <bool PAIR, class T, class O, bool LONG, bool FULL>
+template <bool PAIR, class T, class O, bool LONG, Kind KIND>
 __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
 {
     constexpr int THREADS = threads_of(PAIR);
@@ -821,8 +836,10 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
                     tc::mbar_arrive(acc_free_bar(acc));
             }
         };
-        const Epilogue<FULL> epi(p);
+        const Epilogue<KIND> epi(p);
         const float *const biases = p.q.bias;
+        const bool staged = KIND == GRADIENT && PAIR && uniform(p.z_ring) != 0;
+        const uint32_t ring = sbase + p.z_ring + (warp - 2) * (Z_SLOTS * Z_SLOT_BYTES);
         const int N = uniform(p.q.N), acc_step = uniform(p.acc_step);
         const long long stride_y = __shfl_sync(0xFFFFFFFFu, p.q.stride_y, 0);
         int j = 0;
@@ -860,13 +877,30 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
                         }
                     }
                 } else {
-                    sum += finish_rows<T, O, FULL>(epi, v, ahead, y + c0 * epi.ldy, z + c0 * epi.ldz, bias, o.valid - c0, in);
+                    sum += finish_rows<T, O, KIND>(epi, v, ahead, y + c0 * epi.ldy, z + c0 * epi.ldz, bias, o.valid - c0, in);
                 }
             };
             // What of Z or R the first chunk takes comes during the wait, each next chunk's during the one before
             // (the gradient of 8192 x 4096, depth 2048, through GELU: 174 us without, 119 with).
             Ahead<CHUNK> ahead;
-            if (!LONG) load_ahead(ahead, CHUNK * set);
+            if (!LONG && !staged) load_ahead(ahead, CHUNK * set);
+            // Or (pairs, rows of Z on 16 bytes) four chunks are on their way through shared memory: a chunk takes less
+            // time than memory does to answer, which the tensor core waits for where a tile's last sums keep it from the
+            // turn after the next one.  (Groups of 512 x 4096, depth 2048, with column sums: through ReLU 123 us, by
+            // registers 137 to 145; GELU 141 and 146; SiLU 136 and 141 to 146.  Without sums no turns, and 110 either way.)
+            auto send_for = [&](int c0) {
+                const int row = c0 + (lane >> 2), c = 8 * (lane & 3) - lane;
+                const T *const src = z + row * epi.ldz + c;
+                const uint32_t dst = ring + (c0 / (SETS * CHUNK) % Z_SLOTS) * Z_SLOT_BYTES + lane * 16;
+                if (n + c < N && row < o.valid) copy_16(dst, src);
+                if (n + c < N && row + 8 < o.valid) copy_16(dst + Z_SLOT_BYTES / 2, src + 8 * epi.ldz);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            if (staged) {
+                __syncwarp();  // (the tile before has been read)
+#pragma unroll
+                for (int i = 0; i < Z_SLOTS; ++i) send_for(CHUNK * (SETS * i + set));
+            }
             bool ok = true;
             if constexpr (LONG) {
                 // All turns but the last are added up in registers, and then with the last one where its
@@ -904,7 +938,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
             }
-            if (LONG) load_ahead(ahead, CHUNK * set);
+            if (LONG && !staged) load_ahead(ahead, CHUNK * set);
             // (A wait for a whole tile's depth, of which a stage takes 0.3 us: 2^31 rows take 5 s.)
             if (!LONG || turns == 1)
                 ok = turns == 0 || warp_wait(acc_full_bar(j & 1), (j >> 1) & 1, err, tc::ERR_EPILOGUE, lim + 1024ull * stages);
@@ -914,17 +948,29 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
             for (int c0 = CHUNK * set; c0 < o.valid; c0 += SETS * CHUNK) {
                 float v[CHUNK];
                 load_sums(lanes + (uint32_t)((j & 1) * acc_step + c0), turns > 0, v);
-                const Ahead<CHUNK> now = ahead;
-                load_ahead(ahead, c0 + SETS * CHUNK);
-                finish(v, now, c0);
+                if (staged) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(Z_SLOTS - 1) : "memory");
+                    __syncwarp();
+                    const uint8_t *const slot = smem + (ring - sbase) + (c0 / (SETS * CHUNK) % Z_SLOTS) * Z_SLOT_BYTES;
+                    Ahead<CHUNK> now;
+                    now.load(reinterpret_cast<const T *>(slot) + lane, 32, o.valid - c0, in, true);
+                    __syncwarp();
+                    send_for(c0 + Z_SLOTS * SETS * CHUNK);
+                    finish(v, now, c0);
+                } else {
+                    const Ahead<CHUNK> now = ahead;
+                    load_ahead(ahead, c0 + SETS * CHUNK);
+                    finish(v, now, c0);
+                }
             }
             if (turns > 0) {
                 give_back(j & 1);
                 ++j;
             }
             const long long row = (long long)SETS * o.row_tile + set;
-            if (FULL && p.q.partial && in && row < p.q.partials) p.q.partial[row * p.q.N + n] = sum;
+            if (KIND == GRADIENT && p.q.partial && in && row < p.q.partials) p.q.partial[row * p.q.N + n] = sum;
         }
+        if (staged) asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
 
@@ -932,7 +978,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
         // Every CTA of the cluster has been sent its share of the tile's rows by all ranks (its own room
         // for them is apart from the stages, which it may still use meanwhile) and adds them up, in rank
         // order.  (A rank that gave up sends nothing; the error word says that Y is undefined.)
-        const Epilogue<FULL> epi(p);
+        const Epilogue<KIND> epi(p);
         float bias = 0.0f;
         const int q = warp & 3, set = (warp - 2) >> 2, n = first.f0 + TILE_F * half + 32 * q + lane;
         if (warp >= 2 && any && p.q.bias && n < p.q.N) bias = p.q.bias[(long long)first.e * p.q.N + n];
@@ -956,12 +1002,12 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
                     for (int c = 0; c < FEW; ++c)
                         if (c0 + c < rows) v[c] += part[(r * share + c0 + c) * TILE_F];
                 }
-                finish_rows<T, O, FULL>(epi, v, ahead, static_cast<O *>(p.q.y) + base + row * epi.ldy, z, bias, rows - c0, n < p.q.N);
+                finish_rows<T, O, KIND>(epi, v, ahead, static_cast<O *>(p.q.y) + base + row * epi.ldy, z, bias, rows - c0, n < p.q.N);
             }
         }
     }
 
-    if (FULL && p.q.partial_start && blockIdx.x == 0) {
+    if (KIND == GRADIENT && p.q.partial_start && blockIdx.x == 0) {
         for (int e = threadIdx.x; e <= p.q.groups; e += THREADS)
             p.q.partial_start[e] = SETS * (p.q.ragged == RAGGED_ROWS ? walk.first[e] / p.tiles_f : p.tiles_t * e);
     }
