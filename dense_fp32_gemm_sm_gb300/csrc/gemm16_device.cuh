@@ -164,13 +164,15 @@ __device__ __forceinline__ Two gelu_slope(float z0, float z1)
 
 // The same by the tail: 1/2 - (1/2 - s) for z < 0, 1/2 + (1/2 - s) for z > 0, with s = Phi(-|z|) - |z| phi(z),
 // off by less than 6e-7; fewer operations.
-__device__ __forceinline__ Two gelu_slope_near(float z0, float z1)
+__device__ __forceinline__ float gelu_slope_near(float z)
 {
-    const Two a = two(at_most(fabsf(z0), 20.0f), at_most(fabsf(z1), 20.0f));
-    const Two t = reciprocal_fast(fma(a, both(0.31f), both(1.0f)));
+    const float a = at_most(fabsf(z), 20.0f), t = reciprocal_fast(fmaf(0.31f, a, 1.0f));
+    float g = TAIL[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) g = fmaf(g, t, TAIL[i]);
     // exp(-a^2/2) (g t - a / sqrt(2 pi))
-    const Two s = mul(bell(a), fma(polynomial(TAIL, t), t, mul(a, both(-0.398942280401433f))));
-    return fma(two(copysignf(1.0f, z0), copysignf(1.0f, z1)), fma(s, both(-1.0f), both(0.5f)), both(0.5f));
+    const float s = exp2_fast(-0.721347520444482f * a * a) * fmaf(g, t, -0.398942280401433f * a);
+    return 0.5f + copysignf(0.5f - s, z);
 }
 
 // ---- SiLU -----------------------------------------------------------------------------------
@@ -207,39 +209,34 @@ static __device__ __noinline__ float slope_by_definition(float z, int act)
     return __fmul_rn(s, __fadd_rn(1.0f, __fmul_rn(c, __fadd_rn(1.0f, -s))));
 }
 
-// v act'(z) of two values, as they are rounded to T when act' is evaluated by its definition: by the fast
+// v act'(z) of two values, and the pair rounded to T as when act' is evaluated by its definition: by the fast
 // evaluation where all values within both evaluations' errors round alike, else by the definition (one
-// BF16 element in 3000).  GELU's slope is off by less than 6e-7 and 2.5e-7, SiLU's by (1 + |z|) times 2.5e-7 in
+// BF16 element in 1500).  GELU's slope is off by less than 6e-7 and 2.5e-7, SiLU's by (1 + |z|) times 2.5e-7 in
 // both.
-template <class T>
-__device__ __forceinline__ void through_exactly(float &v0, float &v1, float z0, float z1, int act)
+template <class T, int ACT>
+__device__ __forceinline__ uint32_t through_exactly(float &v0, float &v1, float z0, float z1)
 {
-    if (act == FGEMM_ACT_RELU) {
+    if (ACT == FGEMM_ACT_NONE) return pack<T>(v0, v1);
+    if (ACT == FGEMM_ACT_RELU) {
         v0 = gate(v0, z0);
         v1 = gate(v1, z1);
-        return;
+        return pack<T>(v0, v1);
     }
-    const Two size = two(fabsf(v0), fabsf(v1));
-    Two fast, off;
-    if (act == FGEMM_ACT_GELU) {
-        fast = mul(two(v0, v1), gelu_slope_near(z0, z1));
-        off = mul(size, both(8.5e-7f));
-    } else {
-        const Two far = two(at_most(fabsf(z0), 80.0f), at_most(fabsf(z1), 80.0f));
-        fast = mul(two(v0, v1), two(silu_slope(z0), silu_slope(z1)));
-        off = mul(size, fma(far, both(5e-7f), both(5e-7f)));
-    }
-    float a0, a1, b0, b1, f0, f1;
-    split(fma(off, both(-1.0f), fast), a0, a1);
-    split(fma(off, both(1.0f), fast), b0, b1);
-    split(fast, f0, f1);
-    const uint32_t differ = pack<T>(a0, a1) ^ pack<T>(b0, b1);
+    const bool gelu = ACT == FGEMM_ACT_GELU;
+    const float w0 = gelu ? 8.5e-7f : fmaf(at_most(fabsf(z0), 80.0f), 5e-7f, 5e-7f), g0 = fabsf(v0);
+    const float w1 = gelu ? 8.5e-7f : fmaf(at_most(fabsf(z1), 80.0f), 5e-7f, 5e-7f), g1 = fabsf(v1);
+    // (Not to be contracted with a sum that they go into: column sums are the same with D and without.)
+    const float f0 = __fmul_rn(v0, gelu ? gelu_slope_near(z0) : silu_slope(z0));
+    const float f1 = __fmul_rn(v1, gelu ? gelu_slope_near(z1) : silu_slope(z1));
+    const uint32_t d = pack<T>(fmaf(-w0, g0, f0), fmaf(-w1, g1, f1)), differ = d ^ pack<T>(fmaf(w0, g0, f0), fmaf(w1, g1, f1));
     if (differ != 0) {
-        if (differ & 0xFFFFu) f0 = __fmul_rn(v0, slope_by_definition(z0, act));
-        if (differ >> 16) f1 = __fmul_rn(v1, slope_by_definition(z1, act));
+        v0 = differ & 0xFFFFu ? __fmul_rn(v0, slope_by_definition(z0, ACT)) : f0;
+        v1 = differ >> 16 ? __fmul_rn(v1, slope_by_definition(z1, ACT)) : f1;
+        return pack<T>(v0, v1);
     }
     v0 = f0;
     v1 = f1;
+    return d;
 }
 
 }  // namespace h16

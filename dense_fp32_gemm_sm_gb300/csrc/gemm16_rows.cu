@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(256) realign_kernel(Realign a, Realign b)
 constexpr int ACT_COLUMNS = 256;  // of a block: eight a lane
 constexpr int ACT_WARPS = 8;      // rows of a block at a time
 
+template <class T> __device__ __forceinline__ uint32_t bits_of(T x) { return reinterpret_cast<const uint16_t &>(x); }
+
 // Rows of group e, the first at `first`.
 __device__ __forceinline__ int rows_of(const int *offsets, int e, int M, int &first)
 {
@@ -46,8 +48,16 @@ __device__ __forceinline__ int rows_of(const int *offsets, int e, int M, int &fi
 // D = G act'(Z) for a slice of a group's rows (`height` at most) by 256 columns, and its column sums.  The
 // slices of all groups are counted through, so that a group of many rows has many blocks.
 // VEC: a lane's eight columns are consecutive, 16 bytes an access; else 32 apart, for any alignment.
-template <class T, bool VEC>
-__global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, int strips, int height)
+// Memory bounds it without an activation and through ReLU (8192 x 11008: 60 and 85 us, 6.0 and 6.4 TB/s), 50
+// instructions an element through GELU and SiLU (131 and 111 us), a fifth of them for the few that take the definition.
+// (Those in a queue of the warp's or the block's, evaluated 32 at a time: 131 and 119 us, 133 and 125.)
+// Rows that a warp has on their way at a time, and blocks an SM has registers for.  (8192 x 11008, none: 60 us with 4 and 2, 78 with
+// 2 and 4; through ReLU 84 and 85; GELU and SiLU, which arithmetic bounds, 164 and 132, 153 and 112.)
+__host__ __device__ constexpr int act_batch(int act) { return act == FGEMM_ACT_NONE ? 4 : 2; }
+__host__ __device__ constexpr int act_blocks(int act) { return act == FGEMM_ACT_NONE ? 2 : 4; }
+
+template <class T, bool VEC, int ACT>
+__global__ void __launch_bounds__(32 * ACT_WARPS, act_blocks(ACT)) act_grad_kernel(ActGrad p, int strips, int height)
 {
     __shared__ float sums[ACT_WARPS][ACT_COLUMNS];
     after_previous_kernel();
@@ -83,53 +93,56 @@ __global__ void __launch_bounds__(32 * ACT_WARPS, 4) act_grad_kernel(ActGrad p, 
     const int c0 = strip * ACT_COLUMNS;
     auto column = [&](int j) { return c0 + (VEC ? 8 * lane + j : lane + 32 * j); };
     float sum[8] = {};
-    const T *const G = static_cast<const T *>(p.g);
-    const T *const Z = static_cast<const T *>(p.z);
-    T *const D = static_cast<T *>(p.d);
-    const bool gated = p.act != FGEMM_ACT_NONE;
-    if (column(0) < p.N) {
-        // Two rows of a warp are on their way at a time.  (Four leave two blocks an SM in place of four.)
-        constexpr int BATCH = 2;
-        for (long long r0 = from + warp; r0 < to; r0 += BATCH * ACT_WARPS) {
-            __align__(16) T g[BATCH][8], z[BATCH][8];
+    constexpr bool gated = ACT != FGEMM_ACT_NONE;
+    constexpr int BATCH = act_batch(ACT);
+    const int rows = (int)(to - from);
+    const long long ldg = p.ldg, ldz = p.ldz, ldd = p.ldd;
+    // At this slice's first row and the lane's first column.
+    const T *const G = static_cast<const T *>(p.g) + from * ldg + column(0);
+    const T *const Z = gated ? static_cast<const T *>(p.z) + from * ldz + column(0) : nullptr;
+    T *const D = p.d ? static_cast<T *>(p.d) + from * ldd + column(0) : nullptr;
+    const bool in = column(0) < p.N;  // (VEC: all eight are, then)
+    // Eight elements, 32 apart unless VEC, as words of two.
+    auto load = [&](const T *x, uint32_t (&w)[4]) {
+        if (VEC) {
+            if (in) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(x);
+        } else {
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const long long r = r0 + i * ACT_WARPS;
-                if (r >= to) break;
-                if (VEC) {
-                    *reinterpret_cast<uint4 *>(g[i]) = *reinterpret_cast<const uint4 *>(G + r * p.ldg + column(0));
-                    if (gated) *reinterpret_cast<uint4 *>(z[i]) = *reinterpret_cast<const uint4 *>(Z + r * p.ldz + column(0));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool in = column(j) < p.N;
-                        g[i][j] = in ? G[r * p.ldg + column(j)] : from_float<T>(0.0f);
-                        if (gated) z[i][j] = in ? Z[r * p.ldz + column(j)] : from_float<T>(0.0f);
-                    }
-                }
+            for (int j = 0; j < 8; j += 2) {
+                const uint32_t low = column(j) < p.N ? bits_of(x[32 * j]) : 0, high = column(j + 1) < p.N ? bits_of(x[32 * j + 32]) : 0;
+                w[j / 2] = low | high << 16;
             }
+        }
+    };
+#pragma unroll 1
+    for (int r0 = warp; r0 < rows; r0 += BATCH * ACT_WARPS) {
+        __align__(16) uint32_t g[BATCH][4], z[BATCH][4];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const long long r = r0 + i * ACT_WARPS;
-                if (r >= to) break;
-                __align__(16) uint32_t d[4];
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * ACT_WARPS;
+            if (r >= rows) break;
+            load(G + r * ldg, g[i]);
+            if (gated) load(Z + r * ldz, z[i]);
+        }
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    float v0 = to_float(g[i][j]), v1 = to_float(g[i][j + 1]);
-                    if (gated) through_exactly<T>(v0, v1, to_float(z[i][j]), to_float(z[i][j + 1]), p.act);
-                    sum[j] += v0;
-                    sum[j + 1] += v1;
-                    d[j / 2] = pack<T>(v0, v1);
-                }
-                if (D) {
-                    if (VEC) {
-                        *reinterpret_cast<uint4 *>(D + r * p.ldd + column(0)) = *reinterpret_cast<const uint4 *>(d);
-                    } else {
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * ACT_WARPS;
+            if (r >= rows) break;
+            __align__(16) uint32_t d[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (column(j) < p.N) D[r * p.ldd + column(j)] = reinterpret_cast<const T *>(d)[j];
-                    }
-                }
+            for (int j = 0; j < 4; ++j) {
+                float v0 = from_bits<T>(g[i][j]), v1 = from_bits<T>(g[i][j] >> 16);
+                d[j] = through_exactly<T, ACT>(v0, v1, gated ? from_bits<T>(z[i][j]) : 0.0f, gated ? from_bits<T>(z[i][j] >> 16) : 0.0f);
+                sum[2 * j] += v0;
+                sum[2 * j + 1] += v1;
+            }
+            if (D == nullptr) continue;
+            if (VEC) {
+                if (in) *reinterpret_cast<uint4 *>(D + r * ldd) = *reinterpret_cast<const uint4 *>(d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (column(j) < p.N) D[r * ldd + 32 * j] = reinterpret_cast<const T *>(d)[j];
             }
         }
     }
@@ -219,14 +232,23 @@ static long long most_slices(const ActGrad &p)
     return p.offsets ? p.M / height + (p.groups < p.M ? p.groups : p.M) : (p.M + height - 1ll) / height;
 }
 
+template <class T, bool VEC>
+static auto act_grad_of(int act)
+{
+    return act == FGEMM_ACT_NONE   ? act_grad_kernel<T, VEC, FGEMM_ACT_NONE>
+           : act == FGEMM_ACT_RELU ? act_grad_kernel<T, VEC, FGEMM_ACT_RELU>
+           : act == FGEMM_ACT_GELU ? act_grad_kernel<T, VEC, FGEMM_ACT_GELU>
+                                   : act_grad_kernel<T, VEC, FGEMM_ACT_SILU>;
+}
+
 fgemm_status launch_act_grad(const ActGrad &p, float *sums, cudaStream_t stream)
 {
     const int strips = (p.N - 1) / ACT_COLUMNS + 1;
     const long long blocks = strips * most_slices(p);
     if (blocks > 0x7FFFFFFF) return FGEMM_ERR_NOT_SUPPORTED;
     const bool vec = p.N % 8 == 0 && vectors(p.g, p.ldg) && vectors(p.z, p.ldz) && vectors(p.d, p.ldd);
-    const auto kernel = p.type == FGEMM_BF16 ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
-                                             : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);
+    const auto kernel = p.type == FGEMM_BF16 ? (vec ? act_grad_of<__nv_bfloat16, true>(p.act) : act_grad_of<__nv_bfloat16, false>(p.act))
+                                             : (vec ? act_grad_of<__half, true>(p.act) : act_grad_of<__half, false>(p.act));
     const fgemm_status st = status(mx::launch(kernel, dim3((unsigned)blocks), 32 * ACT_WARPS, 0, stream, 1, p, strips, slice_rows(p.M, p.N)));
     if (st != FGEMM_OK || !p.partial) return st;
     return launch_sums(p.partial, most_slices(p), nullptr, &p, p.groups, p.N, sums, stream);
