@@ -83,21 +83,22 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.tiles_t = (int)row_tiles;
     p.tiles_f = (int)tiles_f;
     const int own = PAIR ? p.nt / 2 : p.nt;  // rows of op(A) that a CTA brings
-    // Boxes: a whole tile's where all tiles are alike, else small enough that a short tile brings little more.
-    p.x_box = q.ragged == RAGGED_ROWS && own > 64 ? 64 : own;
+    // Boxes: a whole tile's where all tiles are alike, else half of it, so that a short tile brings little more.  (As 64 rows
+    // they bring 128 for 96: groups of 500 x 4096, depth 4096, 59 us in place of 52.)
+    p.x_box = q.ragged == RAGGED_ROWS && own > 64 ? own / 2 : own;
     const int x_bytes = q.ta ? (own + 63) / 64 * BOX_BYTES : (own + p.x_box - 1) / p.x_box * p.x_box * 128;
     p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
     const int join_bytes = !PAIR && plan.ranks > 1 ? (p.nt + plan.ranks) * TILE_F * 4 : 0;  // (shares are rounded up)
-    int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 48;
-    // Rings of Z where three stages of two blocks stay.
-    const int z_bytes = 4 * SETS * Z_SLOTS * Z_SLOT_BYTES;
-    const bool z_ring = PAIR && KIND == GRADIENT && q.act != FGEMM_ACT_NONE && q.N % 8 == 0 && q.ldz % 8 == 0 &&
-                        reinterpret_cast<uintptr_t>(q.z) % 16 == 0 && room - z_bytes >= 6 * p.block_bytes;
-    if (z_ring) room -= z_bytes;
+    const int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 48;
     p.blocks = room >= 6 * p.block_bytes ? 2 : 1;
     p.stage_bytes = p.blocks * p.block_bytes;
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
+    // Rings of Z where they cost no stage.  (Groups of 500 x 4096, depth 4096, 192 rows a tile, through ReLU: 56.5 us with four stages,
+    // 62 with three and rings; of 128 x 2048, depth 1024: 72 without rings, 65 with them.)
+    const int z_bytes = 4 * SETS * Z_SLOTS * Z_SLOT_BYTES;
+    const bool z_ring = PAIR && KIND == GRADIENT && q.act != FGEMM_ACT_NONE && q.N % 8 == 0 && q.ldz % 8 == 0 &&
+                        reinterpret_cast<uintptr_t>(q.z) % 16 == 0 && room - z_bytes >= p.stages * p.stage_bytes;
     if (p.stages < 2) return FGEMM_ERR_NOT_SUPPORTED;
     p.table = p.stages * p.stage_bytes + (bar_bytes(p.stages) + 15) / 16 * 16;
     p.join = p.table + (table_bytes + 15) / 16 * 16;
