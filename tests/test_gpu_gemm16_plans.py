@@ -315,3 +315,56 @@ def test_depths_near_the_limit():
         want[i, 7 - i] = i + 1
     assert torch.equal(c.cpu().float(), want)
     assert fg.device_status() == fg.OK
+
+
+# Rounds of tiles whose last one has few (for 152 SMs: tiles of 160 to 256 rows, by 2 and 4; a last tile of 4 rows).
+DIVIDED = [(5000, 5000, 72), (1500, 8200, 520), (3100, 6000, 520), (5000, 7700, 72), (4100, 8200, 1032), (4130, 8200, 1032),
+           (3000, 8200, 1032), (5000, 7700, 1032)]
+
+
+def room(size):
+    return torch.empty(size, dtype=torch.uint8, device="cuda"), size
+
+
+@pytest.mark.parametrize("M,N,K", DIVIDED)
+def test_last_rounds_of_few_tiles(M, N, K):
+    """Every row once: added in place, stored across and along the depth, through a gate."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, w, y0 = ints(g, M, K), ints(g, N, K), ints(g, M, N, dtype=torch.float32)
+    want = x.float() @ w.float().t()  # integers below 2^24
+    y = y0.clone()
+    fg.gemm16(fg.BF16, fg.F32, 0, 1, M, N, K, 1.0, x, K, w, K, None, 0, None, 0, 1.0, y, N, y, N)
+    assert torch.equal(y, want + y0)
+    xt, wt = torch.zeros(K, (M + 7) // 8 * 8, dtype=torch.bfloat16, device="cuda"), w.t().contiguous()
+    xt[:, :M] = x.t()
+    h, z = torch.full((M + 1, N), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((M + 1, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    fg.gemm16(fg.BF16, fg.BF16, 1, 0, M, N, K, 1.0, xt, xt.shape[1], wt, N, None, fg.ACT_RELU, z, N, 0.0, None, 0, h, N,
+              *room(fg.gemm16_copy_workspace_size(1, 0, 1, M, N, K)))
+    assert torch.equal(h[:M], want.clamp(min=0).bfloat16()) and torch.equal(z[:M], want.bfloat16())
+    assert (h[M] == 9).all() and (z[M] == 9).all()
+    gate = ints(g, M, N)
+    fg.gemm16_grad(fg.BF16, fg.BF16, 0, 1, M, N, K, 1.0, x, K, w, K, fg.ACT_RELU, gate, N, h, N)
+    assert torch.equal(h[:M], torch.where(gate > 0, want, 0).bfloat16()) and (h[M] == 9).all()
+
+
+@pytest.mark.parametrize("rows,N,K", [((700, 3, 900, 0, 1400, 260, 31), 4000, 520), ((1, 5000), 5000, 72), ((600, 600, 600), 7700, 1032),
+                                      ((257, 255, 1025, 2), 8200, 264)])
+def test_last_rounds_of_few_tiles_of_groups(rows, N, K):
+    g = torch.Generator(device="cuda").manual_seed(7)
+    E, M = len(rows), sum(rows)
+    at = [0]
+    for n in rows:
+        at.append(at[-1] + n)
+    off = torch.tensor(at, dtype=torch.int32, device="cuda")
+    x, w, y = ints(g, M + 2, K), ints(g, E, K, N), torch.full((M + 2, N), 9.0, device="cuda")
+    y0 = ints(g, M + 2, N, dtype=torch.float32)
+    y.copy_(y0)
+    fg.gemm16_grouped(fg.BF16, fg.F32, 0, E, M + 2, N, K, off, 1.0, x, K, w, N, K * N, None, 0, None, 0, 1.0, y, N, y, N,
+                      *room(fg.gemm16_copy_workspace_size(0, 0, E, M + 2, N, K)))
+    want = torch.cat([x[i:j].float() @ w[e].float() for e, (i, j) in enumerate(zip(at, at[1:]))])
+    assert torch.equal(y[:M], want + y0[:M]) and torch.equal(y[M:], y0[M:])
+    gr, c = ints(g, M + 2, N), ints(g, E, K, N, dtype=torch.float32)
+    sums = c + torch.stack([x[i:j].float().t() @ gr[i:j].float() for i, j in zip(at, at[1:])])
+    fg.gemm16_weight_grad(fg.BF16, fg.F32, E, M + 2, N, K, off, 1.0, x, K, gr, N, 1.0, c, N, K * N,
+                          *room(fg.gemm16_copy_workspace_size(1, 0, 1, K, N, M + 2)))
+    assert torch.equal(c, sums)
