@@ -14,7 +14,7 @@ double most(double a, double b) { return a > b ? a : b; }
 double least(double a, double b) { return a < b ? a : b; }
 
 // The estimate in us.  Fitted to 660 measurements of 60 products (1 to 8192 rows, 80 to 11008 columns, depths of 72
-// to 11008, operands not in L2): the plan of the least estimate took 1.4 % longer than the best one on average.
+// to 11008, operands not in L2): the plan of the least estimate took 1.6 % longer than the best one on average.
 //   64 of depth through a pair's barriers 0.151 us and more with the rows of its tile, through one CTA's
 //   0.151; a tile's epilogue and its way through the roles; what all CTAs bring through L2 at 15.8 TB/s, and from memory
 //   at 6.6; the launch, and the joining of ranks.
@@ -57,10 +57,11 @@ Plan plan_product(long long M, long long N, long long K, int ragged, long long g
         w.blocks = up(depth, 64) + (ragged == RAGGED_DEPTH && groups > 1 ? 0.5 : 0.0);
         w.products = ragged == RAGGED_DEPTH ? (double)groups : 1.0;
         w.bytes = 2.0 * (M * (double)K + used * K * (double)N) + 2.0 * w.products * M * (double)N;
-        // A cluster's ranks all run at once or not at all, on SMs of one part of the GPU: no more of them than SMs, of large
-        // clusters than four fifths (24 clusters of six did not fit at once: 14.7 us in place of 8.5).
+        // A cluster's ranks all run at once or not at all, on SMs of one part of the GPU: no more of them than SMs, of more
+        // than two than four fifths (24 clusters of six did not fit at once, 14.7 us in place of 8.5, nor on another GPU 48 of
+        // three, 11.8 in place of 6.6).
         const double ctas = w.row_tiles * w.products * up(w.N, 128) * ranks;
-        if (ranks > 1 && (ctas > sms || (ranks > 4 && ctas > 0.8 * sms) || w.blocks < 2 * ranks)) return;
+        if (ranks > 1 && (ctas > sms || (ranks > 2 && ctas > 0.8 * sms) || w.blocks < 2 * ranks)) return;
         const double t = estimate(w, pair, ranks, sms);
         if (best.nt == 0 || t < least_time) {
             best = Plan{pair, nt, ranks, 0};
