@@ -368,3 +368,35 @@ def test_last_rounds_of_few_tiles_of_groups(rows, N, K):
     fg.gemm16_weight_grad(fg.BF16, fg.F32, E, M + 2, N, K, off, 1.0, x, K, gr, N, 1.0, c, N, K * N,
                           *room(fg.gemm16_copy_workspace_size(1, 0, 1, K, N, M + 2)))
     assert torch.equal(c, sums)
+
+
+def test_calls_from_two_threads():
+    """Each with its own stream and workspace, sizes in turn: what a thread keeps of its plans is its own."""
+    import threading
+
+    sizes = [(1, 264, 520), (300, 1001, 72), (700, 1304, 1032), (64, 200, 264)]
+    failures = []
+
+    def work(seed):
+        try:
+            g = torch.Generator(device="cuda").manual_seed(seed)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for i in range(24):
+                    M, N, K = sizes[(i + seed) % len(sizes)]
+                    x, w, y = ints(g, M, K), ints(g, K, N), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+                    fg.gemm16(fg.BF16, fg.BF16, 0, 0, M, N, K, 1.0, x, K, w, N, None, 0, None, 0, 0.0, None, 0, y, N,
+                              *room(fg.gemm16_copy_workspace_size(0, 0, 1, M, N, K)))
+                    want = (x.double() @ w.double()).bfloat16()
+                    stream.synchronize()
+                    if not torch.equal(y, want):
+                        failures.append((seed, M, N, K))
+        except Exception as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures
