@@ -5,6 +5,7 @@
 #include "fgemm_internal.h"
 #include "gemm16.h"
 #include "gemm16_device.cuh"
+#include "gemm16_slices.h"
 #include "mxfp4_launch.h"
 
 namespace fgemm {
@@ -37,13 +38,6 @@ constexpr int ACT_COLUMNS = 256;  // of a block: eight a lane
 constexpr int ACT_WARPS = 8;      // rows of a block at a time
 
 template <class T> __device__ __forceinline__ uint32_t bits_of(T x) { return reinterpret_cast<const uint16_t &>(x); }
-
-// Rows of group e, the first at `first`.
-__device__ __forceinline__ int rows_of(const int *offsets, int e, int M, int &first)
-{
-    first = max(0, min(offsets[e], M));
-    return max(max(0, min(offsets[e + 1], M)) - first, 0);
-}
 
 // D = G act'(Z) for a slice of a group's rows (`height` at most) by 256 columns, and its column sums.  The
 // slices of all groups are counted through, so that a group of many rows has many blocks.
@@ -171,23 +165,19 @@ __global__ void __launch_bounds__(256) sums_kernel(const float *partial, long lo
     after_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int strip = blockIdx.x % strips, e = blockIdx.x / strips, n = strip * 32 + lane;
-    long long from = 0, to = most;
+    PartialRows rows{0, most};
     if (start) {
-        from = start[e];
-        to = start[e + 1];
+        rows = inside(start[e], start[e + 1], most);
     } else if (offsets) {
-        int first, before = 0;
-        for (int i = lane; i < e; i += 32) before += (rows_of(offsets, i, M, first) + height - 1) / height;
+        long long before = slices_before(offsets, lane, 32, e, M, height);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
-        from = before;
-        to = from + (rows_of(offsets, e, M, first) + height - 1) / height;
+        rows = inside(before, before + slices_of(offsets, e, M, height), most);
     }
-    to = min(to, most);
     float sum = 0.0f;
     if (n < N) {
 #pragma unroll 4
-        for (long long r = from + warp; r < to; r += 8) sum += partial[r * N + n];
+        for (long long r = rows.from + warp; r < rows.to; r += 8) sum += partial[r * N + n];
     }
     part[warp][lane] = sum;
     __syncthreads();
