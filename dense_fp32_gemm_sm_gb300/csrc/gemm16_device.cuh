@@ -57,6 +57,14 @@ __device__ __forceinline__ float at_least(float x, float least)
     return r;
 }
 
+// 1/2 + a b, held in 0 .. 1.
+__device__ __forceinline__ float half_and(float a, float b)
+{
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, 0f3F000000;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float r;
@@ -148,18 +156,22 @@ __device__ __forceinline__ void gelu(float &z0, float &z1)
 
 // The slope Phi(z) + z phi(z), with Phi(z) = 1/2 + z P(2 z^2 / 5.5^2 - 1) for |z| up to 5.5, beyond which Phi is 0 or
 // 1 to within FP32's rounding: P (CDF) is a Chebyshev fit of this even function, off by less than 1e-8, its
-// coefficients add up to 0.4, and Phi as evaluated is 1.5e-8 off on average, 6e-8 at most, which is what
-// 1 + erff comes to.  (A gradient is rounded to 16 bits, to the other side the more often the less exact it is.  By
-// the tail above it is 2.3e-7 off, and the weights' gradient of 2048 rows was twice as far off.)
+// coefficients add up to 0.4, and Phi as evaluated is 1.6e-8 off on average, 9e-8 at most.  (A gradient is
+// rounded to 16 bits, to the other side the more often the less exact it is.  By the tail above it is 2.3e-7 off,
+// and the weights' gradient of 2048 rows was twice as far off.)
 __device__ constexpr float CDF[] = {0.000118079995f, -0.000285676331f, 0.000183916665f, -0.000356754608f, 0.00140742643f, -0.00265870243f,
-                                    0.00407412974f,  -0.00665067835f,  0.0104686366f,   -0.015062524f,    0.0203073174f,  -0.0260361508f,
+                                    0.00407412974f,  -0.00665067835f,  0.0104686385f,   -0.015062524f,    0.0203073174f,  -0.0260361508f,
                                     0.0320769101f,   -0.0387937948f,   0.0477373339f,   -0.0641723126f,   0.12855193f};
 
 __device__ __forceinline__ Two gelu_slope(float z0, float z1)
 {
-    const Two c = two(at_least(at_most(z0, 5.5f), -5.5f), at_least(at_most(z1, 5.5f), -5.5f));
-    const Two cdf = fma(c, polynomial(CDF, fma(mul(c, c), both(2.0f / (5.5f * 5.5f)), both(-1.0f))), both(0.5f));
-    return fma(c, mul(both(0.398942280401433f), bell(two(z0, z1))), cdf);
+    const float c0 = at_least(at_most(z0, 5.5f), -5.5f), c1 = at_least(at_most(z1, 5.5f), -5.5f);
+    const Two c = two(c0, c1);
+    float p0, p1;
+    split(polynomial(CDF, fma(mul(c, c), both(2.0f / (5.5f * 5.5f)), both(-1.0f))), p0, p1);
+    // At -5.5 the halves' sum is -1.5e-8 (at 5.5 it rounds to 1): held in 0 .. 1, it is 0 from there on, and the slope ends with the
+    // bell.  (A NaN becomes 0 here, and is back by c.)
+    return fma(c, mul(both(0.398942280401433f), bell(two(z0, z1))), two(half_and(c0, p0), half_and(c1, p1)));
 }
 
 // The same by the tail: 1/2 - (1/2 - s) for z < 0, 1/2 + (1/2 - s) for z > 0, with s = Phi(-|z|) - |z| phi(z),
