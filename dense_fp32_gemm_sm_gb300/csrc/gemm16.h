@@ -45,14 +45,25 @@ struct Product {
 
 // How a product runs: tiles of 128 (pair: 256) columns of the output by at most nt rows; a tile's
 // depth divided among the `ranks` CTAs of a cluster (1: whole tiles by persistent CTAs or pairs);
-// and whether sums over a long depth are added up in turns (where they are kept in FP32: `fine`).
+// and whether sums over a long depth, of more than `one_go`, are added up in turns.
 struct Plan {
     int pair, nt, ranks, in_turns;
 };
-Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, bool fine, int sms);
+Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, long long one_go,
+                  int sms);
 
-// Depth whose products the tensor core adds up at a time, where sums are kept in FP32.
+// Depth whose products the tensor core adds up at a time, where a longer one is added up in turns.
 constexpr int LONG_DEPTH = 768;
+
+// The depth that is added up in one go.  The tensor core cuts where FP32 addition rounds, so a sum falls short by 0.8e-9 of itself
+// for each entry of depth where its addends are of one sign (F16, depth 2^16: 5.0e-5; 2^18: 2.1e-4; 2^20: 8.6e-4; in turns 4e-6
+// at any of these).  Kept in FP32, or summed on, that counts from one turn on; rounded to 16 bits, from where it is
+// more than a thirtieth of half a step: 1.3e-5 of F16's 4.9e-4 at 2^14, 1e-4 of BF16's 3.9e-3 at 2^17.
+inline long long one_go(fgemm_dtype out_type, bool sums)
+{
+    if (sums || out_type == FGEMM_F32) return LONG_DEPTH;
+    return out_type == FGEMM_F16 ? 1 << 14 : 1 << 17;
+}
 
 // Least rows of a tile where column sums are wanted, which bounds their partial sums.
 constexpr int SUMS_ROWS = 32;

@@ -335,9 +335,9 @@ int fgemm_gemm16_plan(fgemm_dtype out_type, int grouped, int groups, int M, int 
     if (grouped < 0 || grouped > 2 || groups < 1 || groups > FGEMM_MAX_GROUPS || M < 1 || N < 1 || K < 1 || num_sms < 2 ||
         !dims_supported(M, N, K))
         return -1;
-    const bool fine = out_type == FGEMM_F32 || sums != 0;
-    const Plan plan = grouped == 2 ? plan_product(K, N, M, RAGGED_DEPTH, groups, false, fine, num_sms)
-                                   : plan_product(M, N, K, grouped ? RAGGED_ROWS : RAGGED_NONE, groups, sums != 0, fine, num_sms);
+    const long long go = one_go(out_type, sums != 0);
+    const Plan plan = grouped == 2 ? plan_product(K, N, M, RAGGED_DEPTH, groups, false, go, num_sms)
+                                   : plan_product(M, N, K, grouped ? RAGGED_ROWS : RAGGED_NONE, groups, sums != 0, go, num_sms);
     return 16384 * plan.in_turns + 8192 * plan.pair + 16 * plan.nt + plan.ranks;
 }
 

@@ -131,12 +131,8 @@ template <bool PAIR, class T, class O, bool LONG>
 static fgemm_status launch_kind(const Product &q, const Plan &plan, cudaStream_t stream)
 {
     if (q.slope && (q.act != FGEMM_ACT_NONE || q.partial)) return launch_instance<PAIR, T, O, LONG, GRADIENT>(q, plan, stream);
-    if constexpr (LONG && sizeof(O) == 2) {
-        return FGEMM_ERR_NOT_SUPPORTED;  // (not planned: 16-bit outputs without column sums take no turns)
-    } else {
-        if (!q.slope && (q.z || q.beta != 0.0f)) return launch_instance<PAIR, T, O, LONG, FORWARD>(q, plan, stream);
-        return launch_instance<PAIR, T, O, LONG, PLAIN>(q, plan, stream);
-    }
+    if (!q.slope && (q.z || q.beta != 0.0f)) return launch_instance<PAIR, T, O, LONG, FORWARD>(q, plan, stream);
+    return launch_instance<PAIR, T, O, LONG, PLAIN>(q, plan, stream);
 }
 
 template <class T, class O>

@@ -39,7 +39,7 @@ double estimate(const Work &w, bool pair, int ranks, int sms)
 
 }  // namespace
 
-Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, bool fine, int sms)
+Plan plan_product(long long M, long long N, long long K, int ragged, long long groups, bool sums, long long one_go, int sms)
 {
     static const int pair_rows[] = {256, 224, 192, 160, 128, 96, 64}, rows[] = {64, 32, 16}, all_ranks[] = {1, 2, 3, 4, 5, 6, 8};
     const double used = (double)(ragged == RAGGED_ROWS ? (groups < M ? groups : M) : 1);
@@ -77,7 +77,7 @@ Plan plan_product(long long M, long long N, long long K, int ragged, long long g
             consider(false, nt, ranks);
         }
     }
-    best.in_turns = fine && K > LONG_DEPTH;
+    best.in_turns = K > one_go;
     return best;
 }
 
@@ -86,7 +86,7 @@ namespace {
 // The last plans of this thread: weighing the candidates takes 1 us of a call's 4.
 struct Planned {
     long long M, N, K;
-    int ragged, groups, sums, fine, sms;
+    int ragged, groups, sums, go, sms;
     Plan plan;
 };
 
@@ -94,14 +94,14 @@ Plan planned(const Product &q, int sms)
 {
     static thread_local Planned last[8];
     static thread_local unsigned next = 0;
-    const int sums = q.partial != nullptr, fine = sums || q.out_type == FGEMM_F32;
+    const int sums = q.partial != nullptr, go = (int)one_go(q.out_type, sums != 0);
     for (const Planned &p : last)
         if (p.M == q.M && p.N == q.N && p.K == q.K && p.ragged == q.ragged && p.groups == q.groups && p.sums == sums &&
-            p.fine == fine && p.sms == sms)
+            p.go == go && p.sms == sms)
             return p.plan;
     Planned &p = last[next++ % 8];
-    p = Planned{q.M, q.N, q.K, q.ragged, q.groups, sums, fine, sms,
-                plan_product(q.M, q.N, q.K, q.ragged, q.groups, sums != 0, fine != 0, sms)};
+    p = Planned{q.M, q.N, q.K, q.ragged, q.groups, sums, go, sms,
+                plan_product(q.M, q.N, q.K, q.ragged, q.groups, sums != 0, go, sms)};
     return p.plan;
 }
 

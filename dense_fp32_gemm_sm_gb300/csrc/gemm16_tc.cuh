@@ -538,7 +538,8 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
 // LONG: the accumulators take a depth of LONG_DEPTH (768) at a time, and the epilogue's warps add these
 // sums up in their registers.  The tensor core cuts where FP32 addition rounds: over a depth of
 // 2048, sums come out 2.1e-6 off (2-norm, random operands), of 768 at a time 0.6e-6, which counts where
-// they are kept in FP32.  (4096 x 11008 of a depth of 2048: 122 us in turns, 119 in one go.)
+// they are kept in FP32 and, of a depth beyond one_go(), in 16 bits.  (4096 x 11008 of a depth of 2048: 122 us
+// in turns, 119 in one go.)
 template <bool PAIR, class T, class O, bool LONG, Kind KIND>
 __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __grid_constant__ Args p, unsigned *err)
 {

@@ -552,8 +552,9 @@ fgemm_status fgemm_mxfp4_linear(fgemm_dtype type, int M, int N, int K, const voi
  * hold) a gradient is 0 whatever it was; act(-inf) is 0, and act' at an infinity its limit.
  *
  * `type` (FGEMM_BF16 or FGEMM_F16) is the element type of A, B and Z; `out_type` (the same or
- * FGEMM_F32) that of Y and R.  bias and col_sums hold FP32.  Sums are formed in FP32 and each
- * output is rounded once; col_sums are sums of Y before that rounding, in a fixed order.
+ * FGEMM_F32) that of Y and R.  bias and col_sums hold FP32.  Sums are formed in FP32, beyond a depth of
+ * 768 in turns of 768 (16-bit outputs without col_sums: beyond 2^14 for F16, 2^17 for BF16), and each output is
+ * rounded once; col_sums are sums of Y before that rounding, in a fixed order.
  * Matrices are row-major with leading dimensions in elements, as for fgemm_sgemm: A is M x K (K x M
  * for transa = FGEMM_OP_T), B is K x N (N x K).  Pointers are aligned to an element; any alignment
  * and leading dimension is accepted:
@@ -650,7 +651,7 @@ fgemm_status fgemm_act16_grad(fgemm_dtype type, int groups, int M, int N, const 
 /*
  * How a product runs on a GPU with `num_sms` SMs: 16 * rows + ranks (tiles of 128 columns of Y by at most
  * `rows` rows, each tile's depth divided among `ranks` CTAs), + 8192 where pairs of CTAs take 256 columns,
- * + 16384 where the sums of a long depth are added up in turns of 768 (col_sums, or FP32 out).
+ * + 16384 where the sums of a long depth are added up in turns (fgemm_gemm16_weight_grad: by all groups' rows).
  * grouped 0: fgemm_gemm16 and its gradient (sums: with col_sums), 1: by groups, 2:
  * fgemm_gemm16_weight_grad (sizes as that call has them).  -1 for arguments out of range.  Host-only: no CUDA call.
  */
