@@ -90,7 +90,7 @@ static fgemm_status launch_instance(const Product &q, const Plan &plan, cudaStre
     p.block_bytes = (W_BYTES + x_bytes + 1023) / 1024 * 1024;
     const int table_bytes = q.ragged == RAGGED_NONE ? 0 : 2 * 4 * (q.groups + 1);
     const int join_bytes = !PAIR && plan.ranks > 1 ? (p.nt + plan.ranks) * TILE_F * 4 : 0;  // (shares are rounded up)
-    const int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 48;
+    const int room = MOST_SMEM - 1024 - table_bytes - join_bytes - bar_bytes(MAX_STAGES) - 40;
     p.blocks = room >= 6 * p.block_bytes ? 2 : 1;
     p.stage_bytes = p.blocks * p.block_bytes;
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;

@@ -62,8 +62,8 @@ struct Args {
     int withhold;
 };
 
-// Offsets in shared memory behind the ring: barriers, then the slot for tensor memory's address.
-__host__ __device__ constexpr int bar_bytes(int stages) { return (4 * stages + 5) * 8 + 8; }
+// Offsets in shared memory behind the ring: barriers, then a word for tensor memory's address and one for a count of stages.
+__host__ __device__ constexpr int bar_bytes(int stages) { return (4 * stages + 6) * 8 + 8; }
 
 // MMA descriptors.  Along the depth: as of the other tensor-core kernels.  Across it: boxes of 64 elements x
 // 64 deep, 128 bytes an entry of depth; 8 of depth are 1024 bytes apart (stride), 64 elements a box (leading).
@@ -161,6 +161,11 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
 __device__ __forceinline__ void store_remote(uint32_t cluster_addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 // A tile: rows t0 .. t0 + valid of the output, columns from f0, group e, depth k0 .. k0 + depth;
@@ -531,6 +536,43 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
         : "memory");
 }
 
+// In CTA 0 of a pair whose producer has given up behind g stages: what CTA 1 has asked for beyond them is expected by
+// the barriers that count it, too.  Returns the stages that are to be waited for.
+// (Not before the error is known: these barriers let the MMA go on with a part of its operands missing.)
+static __device__ __noinline__ int follow(const Args &p, const int *table, int first_tile, int tile_step, uint32_t full0,
+                                          uint32_t asked_bar, const volatile uint32_t *asked_slot, int g, unsigned *err)
+{
+    const unsigned long long lim = p.wait_limit_ns;
+    const uint64_t t0 = tc::global_timer();
+    while (*(volatile unsigned *)err == 0u)
+        if (tc::global_timer() - t0 > 2 * lim) atomicOr(err, tc::ERR_PRODUCER);
+    // (CTA 1 is past its waits soon after that.)
+    const bool told = tc::mbar_wait(asked_bar, 0, err, tc::ERR_DRAIN, 2 * lim, false);
+    if (!__all_sync(0xFFFFFFFFu, told) || !warp_wait<true>(asked_bar, 0, err, tc::ERR_DRAIN, lim)) return g;
+    const int asked = uniform((int)*asked_slot), stage_depth = p.blocks * DEPTH;
+    const int x_step = p.x_across ? 64 : p.x_box;
+    const bool fix_depth = p.q.ragged == RAGGED_DEPTH;
+    Walk walk(p, table, 2 * TILE_F, first_tile, tile_step);
+    Tile o{};
+    for (int tile = 0, at = 0; at < asked && walk.get(tile, o); ++tile) {
+        const int n = (int)(((unsigned)o.depth + stage_depth - 1) / stage_depth), own = ((o.valid + 31) & ~31) / 2;
+        const uint32_t bytes = W_BYTES + (own + x_step - 1) / x_step * x_step * 128;
+        for (int k = 0; k < n && at < asked; ++k, ++at) {
+            if (at < g) continue;
+            const int left = o.depth - (!fix_depth ? k : k == 0 ? n - 1 : k - 1) * stage_depth;
+            const uint32_t full = full0 + 8 * (at % p.stages);
+            if ((threadIdx.x & 31) == 0) {
+                if (fix_depth && left < stage_depth && (left & 15) != 0)
+                    tc::mbar_arrive(full);  // (the end of a group: counted by CTA 1 itself)
+                else
+                    tc::mbar_arrive_expect_tx(full, stage_depth > DEPTH && left > DEPTH ? 2 * bytes : bytes);
+            }
+        }
+        __syncwarp();
+    }
+    return max(g, asked);
+}
+
 // PAIR: two CTAs work on 256 columns of Y with cta_group::2; each holds its own 128 columns of
 // op(B) and half of the tile's rows of op(A).  CTA 0 issues for both; its `full` barriers count what
 // arrives in either.  Else the `ranks` CTAs of a cluster divide the depth of one tile, or (ranks 1) a CTA
@@ -555,8 +597,9 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
     auto tail_bar = [&](int s) { return bars + 8u * (3 * S + s); };
     auto acc_full_bar = [&](int a) { return bars + 8u * (4 * S + a); };
     auto acc_free_bar = [&](int a) { return bars + 8u * (4 * S + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (4 * S + 4);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_offset + 8 * (4 * S + 5));
+    const uint32_t drain_bar = bars + 8u * (4 * S + 4), asked_bar = drain_bar + 8;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_offset + 8 * (4 * S + 6));
+    uint32_t *const asked_slot = tmem_slot + 1;  // of CTA 0 of a pair: the stages that CTA 1 has asked for
     int *const table = reinterpret_cast<int *>(smem + p.table);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -581,6 +624,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
             tc::mbar_init(acc_free_bar(a), (PAIR ? 2 : 1) * 4 * SETS);
         }
         tc::mbar_init(drain_bar, 1);
+        tc::mbar_init(asked_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -673,7 +717,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
             for (int k = 0; k < n; ++k, ++g) {
                 const int skip = (from + order(k, n)) * stage_depth, depth = o.k0 + skip, left = o.depth - skip;
                 ok = (ready || warp_wait(empty0 + 8 * at.s, at.phase ^ 1, err, tc::ERR_PRODUCER, lim)) &&
-                     g != withhold;  // (testing: as if this copy never arrived)
+                     (g != withhold || half == 1);  // (testing: as if this copy never arrived)
                 if (!ok) break;
                 const bool tail = PAIR && wants_fix(left);
                 const uint32_t here = place, full = full0 + 8 * at.s, lead = lead0 + 8 * at.s;
@@ -720,19 +764,24 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
             more = walk.get(tile, o);
             n = stages_of(o, from);
         }
+        if constexpr (PAIR) {
+            // CTA 1's copies are counted by CTA 0, which may have given up some stages before CTA 1 did (no more than the ring
+            // holds).  So CTA 1 says how many it has asked for, and CTA 0 counts the copies of those beyond its own as well.
+            if (half == 1) {
+                if (lane == 0) {
+                    store_remote(mx::map_to_rank(tc::cvta_smem(asked_slot), 0), (uint32_t)g);
+                    mx::arrive_at(mx::map_to_rank(asked_bar, 0));
+                }
+            } else if (!ok) {
+                g = follow(p, table, first_tile, tile_step, full0, asked_bar, asked_slot, g, err);
+            }
+        }
         // Never leave with copies in flight into either CTA's shared memory.
         if (half == 0)
             for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
                 tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
         for (int s = 0; s < S; ++s)
             if (tail_used >> s & 1) tc::mbar_wait(tail_bar(s), (tail_phase >> s & 1) ^ 1, err, tc::ERR_DRAIN, lim, false);
-        if (half == 1 && !ok) {
-            // Having given up, CTA 1 may have asked for stages that CTA 0 no longer counts: a millisecond
-            // for its copies to land (they take some microseconds).
-            const uint64_t t0 = tc::global_timer();
-            while (tc::global_timer() - t0 < 1000000ull) {
-            }
-        }
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA (of a pair: by CTA 0 for both) ----
