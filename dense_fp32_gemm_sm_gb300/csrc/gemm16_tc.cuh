@@ -163,11 +163,6 @@ __device__ __forceinline__ void store_remote(uint32_t cluster_addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void store_remote(uint32_t cluster_addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
-
 // A tile: rows t0 .. t0 + valid of the output, columns from f0, group e, depth k0 .. k0 + depth;
 // row_tile: its number among all tiles of rows.
 struct Tile {
@@ -538,18 +533,10 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
 
 // In CTA 0 of a pair whose producer has given up behind g stages: what CTA 1 has asked for beyond them is expected by
 // the barriers that count it, too.  Returns the stages that are to be waited for.
-// (Not before the error is known: these barriers let the MMA go on with a part of its operands missing.)
 static __device__ __noinline__ int follow(const Args &p, const int *table, int first_tile, int tile_step, uint32_t full0,
-                                          uint32_t asked_bar, const volatile uint32_t *asked_slot, int g, unsigned *err)
+                                          uint32_t asked_slot, uint32_t asked_bar, int g, unsigned *err)
 {
-    const unsigned long long lim = p.wait_limit_ns;
-    const uint64_t t0 = tc::global_timer();
-    while (*(volatile unsigned *)err == 0u)
-        if (tc::global_timer() - t0 > 2 * lim) atomicOr(err, tc::ERR_PRODUCER);
-    // (CTA 1 is past its waits soon after that.)
-    const bool told = tc::mbar_wait(asked_bar, 0, err, tc::ERR_DRAIN, 2 * lim, false);
-    if (!__all_sync(0xFFFFFFFFu, told) || !warp_wait<true>(asked_bar, 0, err, tc::ERR_DRAIN, lim)) return g;
-    const int asked = uniform((int)*asked_slot), stage_depth = p.blocks * DEPTH;
+    const int asked = mx::asked_by_other(asked_slot, asked_bar, g, err, p.wait_limit_ns), stage_depth = p.blocks * DEPTH;
     const int x_step = p.x_across ? 64 : p.x_box;
     const bool fix_depth = p.q.ragged == RAGGED_DEPTH;
     Walk walk(p, table, 2 * TILE_F, first_tile, tile_step);
@@ -570,7 +557,7 @@ static __device__ __noinline__ int follow(const Args &p, const int *table, int f
         }
         __syncwarp();
     }
-    return max(g, asked);
+    return asked;
 }
 
 // PAIR: two CTAs work on 256 columns of Y with cta_group::2; each holds its own 128 columns of
@@ -599,7 +586,7 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
     auto acc_free_bar = [&](int a) { return bars + 8u * (4 * S + 2 + a); };
     const uint32_t drain_bar = bars + 8u * (4 * S + 4), asked_bar = drain_bar + 8;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_offset + 8 * (4 * S + 6));
-    uint32_t *const asked_slot = tmem_slot + 1;  // of CTA 0 of a pair: the stages that CTA 1 has asked for
+    const uint32_t asked_slot = asked_bar + 12;  // of CTA 0 of a pair: the stages that CTA 1 has asked for
     int *const table = reinterpret_cast<int *>(smem + p.table);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -765,15 +752,10 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
             n = stages_of(o, from);
         }
         if constexpr (PAIR) {
-            // CTA 1's copies are counted by CTA 0, which may have given up some stages before CTA 1 did (no more than the ring
-            // holds).  So CTA 1 says how many it has asked for, and CTA 0 counts the copies of those beyond its own as well.
             if (half == 1) {
-                if (lane == 0) {
-                    store_remote(mx::map_to_rank(tc::cvta_smem(asked_slot), 0), (uint32_t)g);
-                    mx::arrive_at(mx::map_to_rank(asked_bar, 0));
-                }
+                if (lane == 0) mx::tell_asked(asked_slot, asked_bar, g);
             } else if (!ok) {
-                g = follow(p, table, first_tile, tile_step, full0, asked_bar, asked_slot, g, err);
+                g = follow(p, table, first_tile, tile_step, full0, asked_slot, asked_bar, g, err);
             }
         }
         // Never leave with copies in flight into either CTA's shared memory.

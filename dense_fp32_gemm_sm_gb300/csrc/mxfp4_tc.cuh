@@ -595,7 +595,7 @@ struct PairTile {
     static constexpr int STAGES = NT == 256 ? 6 : 7;
     static constexpr int ACC_STEP = 192, SF_BASE = ACC_STEP + NT, SF_COLS = 24;
     static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
-    static constexpr int SMEM_BYTES = 1024 + BAR_OFFSET + (2 * STAGES + 5) * 8 + 8;
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFFSET + (2 * STAGES + 6) * 8 + 8;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     static_assert(STAGE_BYTES % 1024 == 0, "the swizzle's alignment");
 };
@@ -666,6 +666,35 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
         : "memory");
 }
 
+// The copies of a pair's CTA 1 are counted by CTA 0's barriers.  Where CTA 0 gives up some stages before CTA 1 (no more than the
+// ring holds), these have to expect what CTA 1 has on its way, or nobody waits for it: CTA 1 tells how many stages it
+// has asked for (tell_asked, at its producer's end), and CTA 0's producer, having given up behind g, learns it
+// here; g where it is not told.  Not before the error is known: the barriers then let the MMA go on with a part
+// of its operands missing.  (The count comes as a copy does, with its bytes on a barrier: 4096 cubed 25.98 us, 25.87
+// without; by a store and an arrival that releases it 0.3 us more than without.)
+__device__ __forceinline__ void tell_asked(uint32_t slot, uint32_t bar, int g)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(map_to_rank(slot, 0)), "r"(g),
+                 "r"(map_to_rank(bar, 0))
+                 : "memory");
+}
+
+__device__ __forceinline__ int asked_by_other(uint32_t slot, uint32_t bar, int g, unsigned *err, unsigned long long lim)
+{
+    const uint64_t t0 = tc::global_timer();
+    while (*(volatile unsigned *)err == 0u)
+        if (tc::global_timer() - t0 > 2 * lim) atomicOr(err, tc::ERR_PRODUCER);
+    if (elect_one()) tc::mbar_arrive_expect_tx(bar, 4);
+    __syncwarp();
+    // (CTA 1 is past its own waits soon after the error.)
+    const bool told = tc::mbar_wait(bar, 0, err, tc::ERR_DRAIN, 2 * lim, false);
+    if (!__all_sync(0xFFFFFFFFu, told)) return g;
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    int asked;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(asked) : "r"(slot) : "memory");
+    return max(g, __shfl_sync(0xFFFFFFFFu, asked, 0));
+}
+
 template <int NT, class T>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ PairArgs args, unsigned *err)
@@ -680,8 +709,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto acc_full_bar = [&](int a) { return bars + 8u * (2 * S + a); };
     auto acc_free_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (2 * S + 4);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 5));
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4), asked_bar = bars + 8u * (2 * S + 5);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFFSET + 8 * (2 * S + 6));
+    const uint32_t asked_slot = bars + 8u * (2 * S + 6) + 4;  // of CTA 0: the stages that CTA 1 has asked for
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -711,6 +741,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             tc::mbar_init(acc_free_bar(a), 2 * EPI_WARPS);
         }
         tc::mbar_init(drain_bar, 1);
+        tc::mbar_init(asked_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -735,7 +766,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             for (int k = 0; k < stages_k; ++k, ++g) {
                 const int s = g % S, round = g / S;
                 ok = (round == 0 || warp_wait(empty_bar(s), (round - 1) & 1, err, tc::ERR_PRODUCER, lim)) &&
-                     g != p.withhold;  // (testing: as if this copy never arrived)
+                     (g != p.withhold || rank == 1);  // (testing: as if this copy never arrived)
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t at = sbase + s * L::STAGE_BYTES, sf = at + L::W_BYTES + L::X_BYTES;
@@ -750,6 +781,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
         }
         // Never leave with copies in flight into either CTA's shared memory.
+        if (rank == 1) {
+            if (elect_one()) tell_asked(asked_slot, asked_bar, g);
+        } else if (!ok) {
+            for (const int asked = asked_by_other(asked_slot, asked_bar, g, err, lim); g < asked; ++g)
+                if (elect_one()) tc::mbar_arrive_expect_tx(full_bar(g % S), L::STAGE_BYTES);
+        }
+        __syncwarp();
         if (rank == 0)
             for (int k = g - S < 0 ? 0 : g - S; k < g; ++k)
                 tc::mbar_wait(full_bar(k % S), (k / S) & 1, err, tc::ERR_DRAIN, lim, false);
