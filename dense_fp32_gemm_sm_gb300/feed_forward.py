@@ -6,7 +6,9 @@ input goes through act'(Z) in the product's epilogue, which also gives the gradi
 With weights of E experts (E x K x N, E x N x K) rows offsets[e] .. offsets[e+1] - 1 of X belong to
 expert e; the offsets stay on the device.
 
-Calls allocate their outputs and workspaces from torch, so they may run on any streams of one device.
+Calls allocate their outputs and workspaces from torch on the current stream, and may run on any streams of one device.
+A backward on another stream than its forward's has to come after it (``wait_stream``); what the forward left is then
+not given out again before that stream is done with it.  The caller's own tensors are the caller's to ``record_stream``.
 ``python -m dense_fp32_gemm_sm_gb300.feed_forward`` fits a small block of experts to another one's outputs.
 """
 
@@ -23,8 +25,15 @@ ACTIVATIONS = {"none": fg.ACT_NONE, "relu": fg.ACT_RELU, "gelu": fg.ACT_GELU, "s
 class Saved:
     """What a forward leaves for its backward."""
 
-    def __init__(self, x, z, h, offsets):
+    def __init__(self, x, z, h, offsets, stream=None):
         self.x, self.z, self.h, self.offsets = x, z, h, offsets
+        self.stream = stream  # that they were made on
+
+    def used_on(self, stream):
+        if self.stream is not None and stream != self.stream:
+            for t in (self.x, self.z, self.h, self.offsets):
+                if t is not None:
+                    t.record_stream(stream)
 
 
 class FeedForward:
@@ -134,7 +143,7 @@ class FeedForward:
         z, h = self._empty(M, self.N), self._empty(M, self.N)
         self._layer(x, self.w1, self.b1, self.act, z, None, h, offsets)
         y = self._layer(h, self.w2, self.b2, fg.ACT_NONE, None, x if self.residual else None, self._empty(M, self.K), offsets)
-        return y, Saved(x, z, h, offsets)
+        return y, Saved(x, z, h, offsets, torch.cuda.current_stream(self.w1.device))
 
     def __call__(self, x, offsets=None):
         """Y for tokens x (M x K); nothing is kept."""
@@ -155,6 +164,7 @@ class FeedForward:
             raise ValueError("saved by a block of %d columns of %s" % (saved.z.shape[1], saved.z.dtype))
         lead = () if self.experts is None else (self.experts,)
         dev = self.w1.device
+        saved.used_on(torch.cuda.current_stream(dev))
         db1 = torch.empty(*lead, self.N, device=dev) if self.b1 is not None else None
         db2 = None
         if self.b2 is not None:
