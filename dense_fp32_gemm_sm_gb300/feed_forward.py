@@ -160,8 +160,9 @@ class FeedForward:
         if M != saved.x.shape[0]:
             raise ValueError("%d gradients for %d tokens" % (M, saved.x.shape[0]))
         self._rows(saved.x, self.K)
-        if tuple(saved.z.shape) != (M, self.N) or saved.z.dtype != self.dtype:
-            raise ValueError("saved by a block of %d columns of %s" % (saved.z.shape[1], saved.z.dtype))
+        for t in (saved.z, saved.h):
+            if tuple(t.shape) != (M, self.N) or t.dtype != self.dtype or not t.is_contiguous():
+                raise ValueError("saved: %s of %s, for %s" % (tuple(t.shape), t.dtype, (M, self.N)))
         lead = () if self.experts is None else (self.experts,)
         dev = self.w1.device
         saved.used_on(torch.cuda.current_stream(dev))
