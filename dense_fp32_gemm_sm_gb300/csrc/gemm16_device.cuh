@@ -141,9 +141,9 @@ __device__ __forceinline__ Two bell(Two x) { return exp2_fast(mul(mul(both(-0.72
 
 // z Phi(z) = max(0, z) - a q for a = |z| and the normal tail q = Phi(-a) = exp(-a^2/2) g(a).  g falls from 1/2
 // as 1/a: a polynomial (TAIL times t) in t = 1 / (1 + 0.31 a), the variable of Hastings' approximations
-// (1955), its coefficients a minimax fit of the relative error for a up to 20 (1.7e-7; 5e-7 as evaluated in
-// FP32).  From 20 on q is 0.  (By normcdff the layer's epilogue took 1.3 times the whole product: 8192 x 11008
-// x 4096, Z kept, 562 us against 431 without an activation.)
+// (1955), its coefficients a minimax fit of the relative error for a up to 20 (1.9e-7; 5e-7 as evaluated in
+// FP32, 6.5e-7 where the reciprocal is a unit off).  From 20 on q is 0.  (By normcdff the layer's epilogue took
+// 1.3 times the whole product: 8192 x 11008 x 4096, Z kept, 562 us against 431 without an activation.)
 __device__ constexpr float TAIL[] = {0.0359170846f, -0.141935625f, 0.155671924f, -0.0154948533f,
                                      0.110444422f,  0.107662495f,  0.124079033f, 0.123655601f};
 
@@ -157,7 +157,7 @@ __device__ __forceinline__ void gelu(float &z0, float &z1)
 // The slope Phi(z) + z phi(z), with Phi(z) = 1/2 + z P(2 z^2 / 5.5^2 - 1) for |z| up to 5.5, beyond which Phi is 0 or
 // 1 to within FP32's rounding: P (CDF) is a Chebyshev fit of this even function, off by less than 1e-8, its
 // coefficients add up to 0.4, and Phi as evaluated is 1.6e-8 off on average, 9e-8 at most.  (A gradient is
-// rounded to 16 bits, to the other side the more often the less exact it is.  By the tail above it is 2.3e-7 off,
+// rounded to 16 bits, to the other side the more often the less exact it is.  By the tail above it is up to 3.3e-7 off,
 // and the weights' gradient of 2048 rows was twice as far off.)
 __device__ constexpr float CDF[] = {0.000118079995f, -0.000285676331f, 0.000183916665f, -0.000356754608f, 0.00140742643f, -0.00265870243f,
                                     0.00407412974f,  -0.00665067835f,  0.0104686385f,   -0.015062524f,    0.0203073174f,  -0.0260361508f,
@@ -175,7 +175,7 @@ __device__ __forceinline__ Two gelu_slope(float z0, float z1)
 }
 
 // The same by the tail: 1/2 - (1/2 - s) for z < 0, 1/2 + (1/2 - s) for z > 0, with s = Phi(-|z|) - |z| phi(z),
-// off by less than 6e-7; fewer operations.
+// off by 3.3e-7 at most; fewer operations.
 __device__ __forceinline__ float gelu_slope_near(float z)
 {
     const float a = at_most(fabsf(z), 20.0f), t = reciprocal_fast(fmaf(0.31f, a, 1.0f));
@@ -221,10 +221,11 @@ static __device__ __noinline__ float slope_by_definition(float z, int act)
     return __fmul_rn(s, __fadd_rn(1.0f, __fmul_rn(c, __fadd_rn(1.0f, -s))));
 }
 
-// v act'(z) of two values, and the pair rounded to T as when act' is evaluated by its definition: by the fast
+// v act'(z) of two values, and the pair rounded to T as when act' is evaluated by its definition in FP32: by the fast
 // evaluation where all values within both evaluations' errors round alike, else by the definition (one
-// BF16 element in 1500).  GELU's slope is off by less than 6e-7 and 2.5e-7, SiLU's by (1 + |z|) times 2.5e-7 in
-// both.
+// BF16 element in 1500).  GELU's slope is off by 3.3e-7 and 1.3e-7 at most, SiLU's by (1 + |z|) times 1.1e-7 in
+// both; the bracket is about twice their sum.  (By gelu_slope, as the products do, the error is the definition's, 2.8e-8 and
+// 2.5e-8 in the 2-norm over normal arguments; the tail's is 5.6e-8.  This is agreement with that order of operations.)
 template <class T, int ACT>
 __device__ __forceinline__ uint32_t through_exactly(float &v0, float &v1, float z0, float z1)
 {
