@@ -14,7 +14,9 @@ double most(double a, double b) { return a > b ? a : b; }
 double least(double a, double b) { return a < b ? a : b; }
 
 // The estimate in us.  Fitted to 660 measurements of 60 products (1 to 8192 rows, 80 to 11008 columns, depths of 72
-// to 11008, operands not in L2): the plan of the least estimate took 1.6 % longer than the best one on average.
+// to 11008, operands not in L2), before the kernel came in kinds and divided a last round's tiles, which are counted as a whole
+// round here.  On 80 other products of these ranges with GELU, as the kernel is now, the plan of the least estimate is the
+// best one for 55, and takes 1.9 % longer on average, 20 % at most.
 //   64 of depth through a pair's barriers 0.151 us and more with the rows of its tile, through one CTA's
 //   0.151; a tile's epilogue and its way through the roles; what all CTAs bring through L2 at 15.8 TB/s, and from memory
 //   at 6.6; the launch, and the joining of ranks.

@@ -38,7 +38,8 @@ class Saved:
 
 class FeedForward:
     """``w1`` (K x N), ``w2`` (N x K), or E of each; biases are float32 (N, K; E x N, E x K) or None.  All
-    stay the caller's.  ``grad_type``: of the weights' gradients."""
+    stay the caller's.  ``grad_type``: of the weights' gradients.  Rows of no expert are 0 in Y and in dX, with
+    ``residual`` too (X and the gradient are added to rows of experts alone)."""
 
     def __init__(self, w1, w2, b1=None, b2=None, act: str = "gelu", residual: bool = False, grad_type=torch.float32):
         if w1.dtype not in (torch.bfloat16, torch.float16) or w1.dim() not in (2, 3) or not w1.is_contiguous():
