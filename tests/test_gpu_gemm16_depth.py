@@ -63,3 +63,22 @@ def test_weights_gradient_of_many_rows(t):
     for e in (0, 2):
         i, j = at[e], at[e + 1]
         check(c[e], 2.0**-10 * summed(x[i:j], d[i:j]), j - i, dt)
+
+
+@pytest.mark.parametrize("M,N", [(24, 128), (512, 2048)])
+def test_gradients(M, N):
+    """Through a gate, without column sums and with them."""
+    K, dt = 1 << 18, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = positive(g, K, M, dtype=dt), positive(g, K, N, dtype=dt)
+    want, z = 2.0**-10 * summed(x, w), torch.randn(M, N, generator=g, device="cuda").half()
+    shut = z <= 0
+    for s in (None, torch.empty(N, device="cuda")):
+        y = torch.empty(M, N, dtype=dt, device="cuda")
+        ws = torch.empty(fg.gemm16_sums_workspace_size(1, M, N), dtype=torch.uint8, device="cuda")
+        fg.gemm16_grad(fg.F16, fg.F16, 1, 0, M, N, K, 2.0**-10, x, M, w, N, fg.ACT_RELU, z, N, y, N, s, ws, ws.numel())
+        assert not y[shut].any()
+        check(y[~shut], want[~shut], K, dt)
+    sums = want.masked_fill(shut, 0).sum(0)  # M additions in FP32, each half a unit at most of a unit's magnitude
+    open_ = sums > 0
+    assert ((s.double() - sums).abs()[open_] <= (96 * 2.0**-23 + (K / 768 + M) * 2.0**-24) * sums[open_]).all()
