@@ -531,12 +531,12 @@ __device__ __forceinline__ void store_sums(uint32_t taddr, const float (&v)[CHUN
         : "memory");
 }
 
-// In CTA 0 of a pair whose producer has given up behind g stages: what CTA 1 has asked for beyond them is expected by
-// the barriers that count it, too.  Returns the stages that are to be waited for.
-static __device__ __noinline__ int follow(const Args &p, const int *table, int first_tile, int tile_step, uint32_t full0,
-                                          uint32_t asked_slot, uint32_t asked_bar, int g, unsigned *err)
+// In CTA 0 of a pair whose producer has given up behind g stages: those up to `asked`, which CTA 1 has asked for, are
+// expected by the barriers that count them, too.
+static __device__ __noinline__ void follow(const Args &p, const int *table, int first_tile, int tile_step, uint32_t full0, int g,
+                                           int asked)
 {
-    const int asked = mx::asked_by_other(asked_slot, asked_bar, g, err, p.wait_limit_ns), stage_depth = p.blocks * DEPTH;
+    const int stage_depth = p.blocks * DEPTH;
     const int x_step = p.x_across ? 64 : p.x_box;
     const bool fix_depth = p.q.ragged == RAGGED_DEPTH;
     Walk walk(p, table, 2 * TILE_F, first_tile, tile_step);
@@ -557,7 +557,6 @@ static __device__ __noinline__ int follow(const Args &p, const int *table, int f
         }
         __syncwarp();
     }
-    return asked;
 }
 
 // PAIR: two CTAs work on 256 columns of Y with cta_group::2; each holds its own 128 columns of
@@ -754,8 +753,10 @@ __global__ void __launch_bounds__(threads_of(PAIR), 1) gemm16_kernel(const __gri
         if constexpr (PAIR) {
             if (half == 1) {
                 if (lane == 0) mx::tell_asked(asked_slot, asked_bar, g);
-            } else if (!ok) {
-                g = follow(p, table, first_tile, tile_step, full0, asked_slot, asked_bar, g, err);
+            } else {
+                const int asked = mx::asked_by_other(asked_slot, asked_bar, g, ok, err, lim);
+                if (asked > g) follow(p, table, first_tile, tile_step, full0, g, asked);
+                g = asked;
             }
         }
         // Never leave with copies in flight into either CTA's shared memory.

@@ -668,10 +668,10 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
 
 // The copies of a pair's CTA 1 are counted by CTA 0's barriers.  Where CTA 0 gives up some stages before CTA 1 (no more than the
 // ring holds), these have to expect what CTA 1 has on its way, or nobody waits for it: CTA 1 tells how many stages it
-// has asked for (tell_asked, at its producer's end), and CTA 0's producer, having given up behind g, learns it
-// here; g where it is not told.  Not before the error is known: the barriers then let the MMA go on with a part
-// of its operands missing.  (The count comes as a copy does, with its bytes on a barrier: 4096 cubed 25.98 us, 25.87
-// without; by a store and an arrival that releases it 0.3 us more than without.)
+// has asked for (tell_asked, at its producer's end), and CTA 0's producer, `ok` or having given up behind g, waits
+// for that here and returns it; g where it is less or not told.  Having given up, not before the error is known: the barriers
+// then let the MMA go on with a part of its operands missing.  (The count comes as a copy does, with its bytes on a
+// barrier, and like one it is always waited for.  By a store and an arrival that releases it 4096 cubed took 0.3 us longer.)
 __device__ __forceinline__ void tell_asked(uint32_t slot, uint32_t bar, int g)
 {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(map_to_rank(slot, 0)), "r"(g),
@@ -679,14 +679,16 @@ __device__ __forceinline__ void tell_asked(uint32_t slot, uint32_t bar, int g)
                  : "memory");
 }
 
-__device__ __forceinline__ int asked_by_other(uint32_t slot, uint32_t bar, int g, unsigned *err, unsigned long long lim)
+__device__ __forceinline__ int asked_by_other(uint32_t slot, uint32_t bar, int g, bool ok, unsigned *err, unsigned long long lim)
 {
-    const uint64_t t0 = tc::global_timer();
-    while (*(volatile unsigned *)err == 0u)
-        if (tc::global_timer() - t0 > 2 * lim) atomicOr(err, tc::ERR_PRODUCER);
+    if (!ok) {
+        const uint64_t t0 = tc::global_timer();
+        while (*(volatile unsigned *)err == 0u)
+            if (tc::global_timer() - t0 > 2 * lim) atomicOr(err, tc::ERR_PRODUCER);
+    }
     if (elect_one()) tc::mbar_arrive_expect_tx(bar, 4);
     __syncwarp();
-    // (CTA 1 is past its own waits soon after the error.)
+    // (CTA 1 is past its own waits soon after an error.)
     const bool told = tc::mbar_wait(bar, 0, err, tc::ERR_DRAIN, 2 * lim, false);
     if (!__all_sync(0xFFFFFFFFu, told)) return g;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -783,8 +785,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         // Never leave with copies in flight into either CTA's shared memory.
         if (rank == 1) {
             if (elect_one()) tell_asked(asked_slot, asked_bar, g);
-        } else if (!ok) {
-            for (const int asked = asked_by_other(asked_slot, asked_bar, g, err, lim); g < asked; ++g)
+        } else {
+            for (const int asked = asked_by_other(asked_slot, asked_bar, g, ok, err, lim); g < asked; ++g)
                 if (elect_one()) tc::mbar_arrive_expect_tx(full_bar(g % S), L::STAGE_BYTES);
         }
         __syncwarp();
